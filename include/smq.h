@@ -411,6 +411,146 @@ SMQ_API int sparse_mqa_write_k_cache(const smq_plan *plan, const uint16_t *k, co
 SMQ_API int sparse_mqa_quantize_q(const smq_plan *plan, const uint16_t *q, const float *weights, int32_t rows,
                                   uint8_t *q_fp8, float *q_scale, uint16_t *weights_bf16, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * The attention that consumes the indexer's token ids, over its own paged
+ * key-value cache: three operators that share one plan and one cache.
+ *   sparse_mqa_append_kv          rotate a step's queries and keys by their
+ *                                 positions; write keys and values into the cache
+ *   sparse_mqa_attention_decode   one query row over its cached range [ks, ke)
+ *   sparse_mqa_attention_selected one query row over selected token ids
+ * (Source: sparse_mqa_indexer docs, SparseMQAIndexer: the layer returns the
+ * top-k token ids to the attention layer, which reads them. The pages do not
+ * show that layer; the formulas are the textbook ones.)
+ *
+ * With H query heads on KVH key-value heads, query head h reads key-value
+ * head h / (H / KVH). For a row with queries q[h] and a set of tokens T,
+ *     s[h][t] = softmax_scale * q[h] . k[t]
+ *     out[h]  = sum_t exp(s[h][t] - lse[h]) v[t],  lse[h] = log sum_t exp(s[h][t]).
+ * A row without tokens gets out = 0 and lse = -infinity. Sums, maxima and
+ * scores are fp32. Keys and values of tokens outside T are never used,
+ * whatever they hold.
+ *
+ * The cache: keys and values are two arrays of pages [KVH][page_size][D],
+ * page p at base + p * page_stride elements, so that both may be views of one
+ * allocation. Elements are bfloat16, or E4M3 codes with one positive float
+ * scale per token, kv head and side: [KVH][page_size] floats, page p at
+ * scales + p * scale_page_stride.
+ * --------------------------------------------------------------------------- */
+typedef struct smq_attn_plan smq_attn_plan;
+
+enum { SMQ_CACHE_BF16 = 0, SMQ_CACHE_E4M3 = 1 };
+
+typedef struct smq_attn_plan_desc {
+  uint32_t struct_size;
+  int32_t num_heads;     /* H: a multiple of num_kv_heads, <= 1024, H / KVH <= 128 */
+  int32_t num_kv_heads;  /* KVH: 1 .. 128 */
+  int32_t head_dim;      /* D: 64 or 128 */
+  int32_t page_size;     /* tokens per page, 1 .. 65536 */
+  int32_t cache_type;    /* SMQ_CACHE_BF16 or SMQ_CACHE_E4M3 */
+  int32_t max_rows;      /* upper bound on rows per call, <= 8192 */
+  int32_t device;        /* CUDA device ordinal the plan runs on */
+  float softmax_scale;   /* finite; 0 picks 1 / sqrt(D) */
+} smq_attn_plan_desc;
+
+/* As smq_plan_create / destroy / set_wait_limit / inject_stall: host memory
+ * only, geometry checked once. inject_stall withholds the hand-off of the
+ * first CTA's tile `tile` (a tile is 128 tokens). */
+SMQ_API int smq_attn_plan_create(const smq_attn_plan_desc *desc, smq_attn_plan **plan);
+SMQ_API int smq_attn_plan_destroy(smq_attn_plan *plan);
+SMQ_API int smq_attn_plan_set_wait_limit(smq_attn_plan *plan, int64_t ns);
+SMQ_API int smq_attn_plan_inject_stall(smq_attn_plan *plan, int32_t tile);
+
+/* Device workspace bytes of every call with this plan: the status word and
+ * the partial results of rows whose tokens several CTAs share. It does not
+ * depend on rows or lengths. Zero the status word with
+ * smq_attn_workspace_init; smq_get_status reads it. Calls that overlap on the
+ * GPU need workspaces of their own. */
+SMQ_API int smq_attn_workspace_size(const smq_attn_plan *plan, size_t *bytes);
+SMQ_API int smq_attn_workspace_init(const smq_attn_plan *plan, void *workspace, size_t workspace_bytes,
+                                    void *stream);
+
+/* Rotate and append. Token t's query and key elements in the first rot_dim
+ * places of a head turn by the angles of row positions[t] of cos_sin: pair i
+ * (i < rot_dim / 2) is (i, i + rot_dim / 2), or (2 i, 2 i + 1) with
+ * interleaved, and becomes (a c - b s, b c + a s) with c = cos_sin[i] and
+ * s = cos_sin[rot_dim / 2 + i]. The other elements and the values pass
+ * unchanged. Each product and sum rounds to fp32, then once to the nearest-even
+ * bfloat16 for queries and a bfloat16 cache. An E4M3 cache takes, per token,
+ * kv head and side, scale = amax / 448 (1 for zeros; both in float) and
+ * x / scale to the nearest E4M3 value, ties to even: the rounding of
+ * sparse_mqa_quantize_q. Inputs to an E4M3 cache must be finite. */
+typedef struct smq_append_args {
+  uint32_t struct_size;
+  int32_t rows;               /* tokens >= 0 */
+  const uint16_t *q;          /* device bf16, row t at q + t * q_stride: [H][D], 16-byte aligned; or NULL */
+  const uint16_t *k;          /* device bf16, row t at k + t * k_stride: [KVH][D], 16-byte aligned */
+  const uint16_t *v;          /* device bf16, row t at v + t * v_stride: [KVH][D], 16-byte aligned */
+  int64_t q_stride;           /* elements, multiples of 8 */
+  int64_t k_stride;
+  int64_t v_stride;
+  const int64_t *positions;   /* device [rows]; one outside the table raises SMQ_ERR_BOUNDS and skips
+                                 the token's query, key and value */
+  const float *cos_sin;       /* device [num_positions][rot_dim]: cosines, then sines; 16-byte aligned */
+  int64_t num_positions;
+  int32_t rot_dim;            /* a multiple of 16, 0 .. D (0: no rotation, positions and cos_sin unread) */
+  int32_t interleaved;
+  const int64_t *slot_mapping;/* device [rows]: page slot / page_size, place slot % page_size. A negative
+                                 slot skips the key and value; one past the cache also raises
+                                 SMQ_ERR_BOUNDS. Tokens that share a slot race. */
+  uint16_t *q_out;            /* device [rows][H][D] bf16, 16-byte aligned; NULL exactly when q is. It may
+                                 not overlap q. */
+  void *k_cache;              /* device pages, 16-byte aligned */
+  void *v_cache;
+  float *k_scales;            /* device scales of an E4M3 cache, else NULL */
+  float *v_scales;
+  int64_t num_pages;
+  int64_t page_stride;        /* elements, >= KVH * page_size * D, a multiple of 16 */
+  int64_t scale_page_stride;  /* floats, >= KVH * page_size (E4M3) */
+  void *workspace;            /* device, the status word: at least 256 bytes */
+  size_t workspace_bytes;
+} smq_append_args;
+
+SMQ_API int sparse_mqa_append_kv(const smq_attn_plan *plan, const smq_append_args *args, void *stream);
+
+/* Attention rows. sparse_mqa_attention_decode takes T = the positions
+ * [row_ks, row_ke) of the row's sequence (row_ks NULL: zero; a window of a
+ * sliding layer otherwise). sparse_mqa_attention_selected takes T = the
+ * non-negative entries of token_ids[row][0 .. num_ids), positions in the row's
+ * sequence such as topk_out of the indexer calls; -1 entries may stand
+ * anywhere and an id listed twice counts twice. A position's page is
+ * block_table[row_indices[row]][position / page_size]. A position past the
+ * block table, or a page or table row out of range, raises SMQ_ERR_BOUNDS and
+ * is left out. */
+typedef struct smq_attention_args {
+  uint32_t struct_size;
+  int32_t rows;               /* R >= 0 */
+  const uint16_t *q;          /* device bf16, row r at q + r * q_stride: [H][D], 16-byte aligned */
+  int64_t q_stride;           /* elements, a multiple of 8 */
+  const void *k_cache;        /* device pages, 16-byte aligned */
+  const void *v_cache;
+  const float *k_scales;      /* device scales of an E4M3 cache, else NULL */
+  const float *v_scales;
+  int64_t num_pages;
+  int64_t page_stride;        /* elements, >= KVH * page_size * D, a multiple of 16 */
+  int64_t scale_page_stride;  /* floats, >= KVH * page_size (E4M3) */
+  const int32_t *block_table; /* device [bt_rows][bt_stride] page ids */
+  int32_t bt_rows;
+  int32_t bt_stride;
+  const int32_t *row_indices; /* device [R] row -> block-table row, or NULL = identity */
+  const int32_t *row_ks;      /* decode: device [R] first position, or NULL; selected: NULL */
+  const int32_t *row_ke;      /* decode: device [R] end position; selected: NULL */
+  const int32_t *token_ids;   /* selected: device [R][ids_ld]; decode: NULL */
+  int32_t num_ids;            /* selected: 1 .. 1048576 */
+  int32_t ids_ld;             /* selected: >= num_ids */
+  uint16_t *out;              /* device [R][H][D] bf16, 16-byte aligned */
+  float *lse;                 /* device [R][H] natural log-sum-exp, or NULL */
+  void *workspace;            /* device, >= smq_attn_workspace_size(plan), 16-byte aligned */
+  size_t workspace_bytes;
+} smq_attention_args;
+
+SMQ_API int sparse_mqa_attention_decode(const smq_attn_plan *plan, const smq_attention_args *args, void *stream);
+SMQ_API int sparse_mqa_attention_selected(const smq_attn_plan *plan, const smq_attention_args *args, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,6 +1,6 @@
 """Build libsmq.so, the sm_103a C-ABI library, in-tree with nvcc.
 
-Three translation units are compiled in parallel and then linked. Only the
+The translation units are compiled in parallel and then linked. Only the
 SMQ_API entry points of include/smq.h are exported.
 """
 
@@ -16,8 +16,9 @@ ROOT = os.path.dirname(PKG)
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsmq.so")
 TRACE_LIB = os.path.join(PKG, "libsmq_trace.so")  # -DSMQ_TRACE: phase timestamps (include/smq_trace.h)
-SOURCES = ["smq_api.cu", "smq_kernels.cu", "smq_producers.cu", "smq_prefill.cu"]
-HEADERS = ["smq_kernels.cuh", "smq_ptx.cuh"]
+SOURCES = ["smq_api.cu", "smq_kernels.cu", "smq_producers.cu", "smq_prefill.cu", "smq_attn_api.cu", "smq_append.cu",
+           "smq_attn.cu"]
+HEADERS = ["smq_kernels.cuh", "smq_ptx.cuh", "smq_attn.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",

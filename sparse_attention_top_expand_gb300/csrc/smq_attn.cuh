@@ -1,0 +1,76 @@
+// Parameter blocks and launchers of the attention operators: the append of
+// rotated keys and values (smq_append.cu) and the attention over the paged
+// cache (smq_attn.cu). Shared with their host side (smq_attn_api.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+namespace smq {
+
+constexpr int kAttnTile = 128;  // tokens per tile
+
+struct AppendParams {
+  int32_t rows;
+  int32_t heads;
+  int32_t kv_heads;
+  int32_t page_size;
+  int32_t rot_dim;
+  int32_t interleaved;
+  int64_t num_positions;
+  int64_t num_pages;
+  int64_t page_stride;        // elements
+  int64_t scale_page_stride;  // floats
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  int64_t q_stride;
+  int64_t k_stride;
+  int64_t v_stride;
+  const int64_t* positions;
+  const float* cos_sin;
+  const int64_t* slot_mapping;
+  uint16_t* q_out;
+  void* k_cache;
+  void* v_cache;
+  float* k_scales;
+  float* v_scales;
+  int32_t* status;
+};
+
+struct AttnParams {
+  int32_t rows;
+  int32_t kv_heads;
+  int32_t group;      // query heads per kv head
+  int32_t head_dim;
+  int32_t page_size;
+  float scale_log2;   // softmax_scale * log2(e)
+  const uint16_t* q;
+  int64_t q_stride;
+  const void* k_cache;
+  const void* v_cache;
+  const float* k_scales;
+  const float* v_scales;
+  int64_t num_pages;
+  int64_t page_stride;        // elements
+  int64_t scale_page_stride;  // floats
+  const int32_t* block_table;
+  int32_t bt_rows;
+  int32_t bt_stride;
+  const int32_t* row_indices;  // may be null
+  const int32_t* row_ks;       // may be null
+  const int32_t* row_ke;       // null: selected
+  const int32_t* token_ids;    // null: decode
+  int32_t num_ids;
+  int32_t ids_ld;
+  uint16_t* out;
+  float* lse;  // may be null
+  int32_t* status;
+};
+
+cudaError_t launch_append(const AppendParams& p, int head_dim, bool e4m3, int num_sms, cudaStream_t stream);
+cudaError_t launch_attention(const AttnParams& p, bool e4m3, cudaStream_t stream);
+
+}  // namespace smq
