@@ -1,118 +1,1002 @@
 // Attention of query rows over a paged key-value cache (sm_103a).
+//
+// For a (row, kv head) pair with G query heads and tiles of 128 tokens:
+//   S^T = K Q^T    one tcgen05.mma chain, M = 128 tokens, N = G heads (padded)
+//   P^T = 2^(S^T scale - m)
+//   O^T += V^T P^T one chain, M = head dim, N = G heads
+// with a running maximum m and sum l per head (one pass over the cache). The
+// tokens are the M side, so any G from 1 to 128 fills the tensor core's rows,
+// one thread owns one token in the softmax (its mask and, for an E4M3 cache,
+// its scales are per-thread constants), and K and V tiles are read by the MMA
+// from the layout the cache has: K as a K-major and V as an M-major operand,
+// both 128-byte rows per token. m is raised only when a score exceeds it by
+// more than kTau (in log2), which keeps the rescale of O out of the common path:
+// P stays below 2^kTau, and sums in fp32 do not mind.
+//
+// The tiles of all (row, kv head) items form one list, cut into equal ranges,
+// one per CTA and SM. A range that starts or ends inside an item leaves an
+// unnormalised partial (O, m, l) in the workspace, and combine_kernel joins
+// the partials of an item in tile order, so results do not depend on timing.
+//
+// E4M3 cache: kind::f8f6f4 wants both operands in 8 bits. Q and P are split in
+// two E4M3 numbers each (x = hi + lo, 8 significant bits together, as many as
+// bf16 has), and each chain runs twice into the same accumulators; the cache
+// itself is read in 8 bits and never widened. The token's key scale multiplies
+// its scores; its value scale joins P (as log2 in the exponent), and l adds
+// P / value scale.
+//
+// Roles (512 threads): warps 0-3 copy K, V and Q tiles (cp.async), warp 4
+// schedules segments, warp 5 issues MMAs, warps 6-7 look up addresses, warps
+// 8-15 are two softmax groups of 128 threads, each with half of the heads.
 #include "smq_attn.cuh"
 #include "smq_kernels.cuh"
 #include "smq_ptx.cuh"
 
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 
 namespace smq {
 
 namespace {
 
-constexpr int kAttnThreads = 128;
+constexpr int kThreads = 512;
+constexpr int kLoaders = 128;
+constexpr int kSoftmax = 256;
+constexpr int kAddrRing = 8;    // tiles whose addresses, masks and scales may be ahead of the softmax
+constexpr int kSegRing = 8;     // segments published ahead
+// Query scales of E4M3 segments: the loader is at most four segments ahead of the softmax (its
+// buffers free with the MMA, the MMA runs up to two tiles ahead), so eight sets never collide.
+constexpr int kQScales = 8;
+constexpr int kSegReaders = 4 + 1 + 2 + 8;   // loader, MMA, address and softmax warps
+constexpr int kAddrReaders = 4 + 8;          // loader and softmax warps
+constexpr float kUnset = -3.0e38f;           // the running maximum before the first score
+constexpr int kSmemLimit = 232448 - 1024;  // less the static part
 
-template <bool kE4m3>
-__device__ __forceinline__ float load_element(const void* base, int64_t at) {
-  if (kE4m3) {
-    __nv_fp8_e4m3 v;
-    v.__x = static_cast<const uint8_t*>(base)[at];
-    return static_cast<float>(v);
-  }
-  return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(base)[at]) << 16);
+// A run of tiles of one (row, kv head) item.
+struct AttnSeg {
+  int32_t row, kvh;
+  int32_t tile0, ntiles;  // ntiles = 0: the end of this CTA's work
+  int32_t first, last;    // decode: positions [first, last); selected: entries [0, num_ids)
+  int32_t slot;           // partial slot, -1: the whole item, write the result
+  int32_t pad;
+};
+static_assert(sizeof(AttnSeg) == 32, "");
+
+template <int D, bool kE4m3, int N>
+struct Shape {
+  static constexpr int kRow = D * (kE4m3 ? 1 : 2);               // bytes per token
+  static constexpr int kBlocks = kRow > 128 ? 2 : 1;             // 128-byte columns
+  static constexpr int kUnit = kBlocks * 128 * 128;              // bytes of a K or V tile
+  static constexpr int kQParts = kE4m3 ? 2 : 1;                  // hi and lo of Q
+  static constexpr int kQPart = kBlocks * N * 128;
+  static constexpr int kQBytes = kQParts * kQPart;
+  static constexpr int kQBufs = N == 128 ? 1 : 2;
+  static constexpr int kPRow = N * (kE4m3 ? 1 : 2) > 128 ? 128 : N * (kE4m3 ? 1 : 2);  // bytes of a P row in a block
+  static constexpr int kPPart = 128 * N * (kE4m3 ? 1 : 2);
+  static constexpr int kPBytes = 2 * kPPart;                     // hi and lo of P
+  static constexpr int kCols = N / 2;                            // heads per softmax thread
+  static constexpr int kRingBytes = kAddrRing * 128 * (8 + (kE4m3 ? 8 : 0));
+  static constexpr int kMisc = kRingBytes + kAddrRing * 16 + kSegRing * 32 + 640 /*barriers*/ + N * 8 /*m, alpha*/ +
+                               (kE4m3 ? kQScales * N * 4 : 0) + 8 * kCols * 4 /*scratch*/ + 64;
+  static constexpr int kFixed = kQBufs * kQBytes + kPBytes + kMisc;
+  static constexpr int kFit = (kSmemLimit - kFixed) / kUnit;
+  static constexpr int kSlots = kFit > 12 ? 12 : kFit;
+  static constexpr int kAhead = kSlots > 8 ? 6 : kSlots - 2;     // units in flight per loader thread
+  static constexpr int kSmem = kSlots * kUnit + kFixed;
+  static constexpr int kTmem = 3 * N <= 64 ? 64 : 3 * N <= 128 ? 128 : 3 * N <= 256 ? 256 : 512;
+  static constexpr float kTop = kE4m3 ? 8.f : 0.f;               // log2 of P at the maximum
+  static constexpr float kTau = kE4m3 ? 8.8f : 8.f;              // log2 of the largest P: 2^8.8 < 448
+  static_assert(kSlots >= 3 && kSmem <= kSmemLimit && kAhead < kSlots, "");
+  static_assert(!kE4m3 || N >= 32, "");
+  static_assert(kBlocks == 2 || kFixed >= 16384, "an M = 128 operand of a 64-wide bf16 head reads past its unit");
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// Position `pos` of the row's sequence as a page and an offset in it; false
-// (and the status bit) where it has none.
-__device__ __forceinline__ bool place_of(const AttnParams& p, int64_t table_row, int64_t pos, int64_t* page, int* off) {
-  if (table_row < 0 || table_row >= p.bt_rows || pos / p.page_size >= p.bt_stride) {
-    atomicOr(p.status, kStatusBounds);
-    return false;
+// 16-byte asynchronous copy; `bytes` 0 fills with zeros and reads nothing.
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("barrier.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// Barrier of `threads` threads that returns whether any of them said `v`.
+__device__ __forceinline__ bool bar_or(int id, int threads, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %3, 0;\n barrier.red.or.pred q, %1, %2, p;\n selp.b32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(v))
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ void sts16(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* v) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "r"(taddr)
+               : "memory");
+}
+// Keeps uses of loaded registers behind the wait that makes them valid.
+__device__ __forceinline__ void pin8(float* v) {
+  asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Shared-memory matrix descriptor. K-major with 128-byte rows: sbo = 1024 (the
+// next 8 rows). M- or N-major: rows of `row` bytes hold consecutive M or N of
+// one k; sbo = 8 row (the next 8 k), lbo = the next block of M or N.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr, uint32_t row, uint32_t lbo) {
+  const uint64_t swizzle = row == 128 ? 2 : row == 64 ? 4 : 6;
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
+         (static_cast<uint64_t>((8 * row) >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (swizzle << 61);
+}
+
+// Instruction descriptor: fp32 accumulation; kind::f16 with bf16 operands or
+// kind::f8f6f4 with E4M3 operands; `mn` for M-major A and N-major B.
+__host__ __device__ constexpr uint32_t mma_idesc(bool e4m3, bool mn, int n) {
+  return (1u << 4) | ((e4m3 ? 0u : 1u) << 7) | ((e4m3 ? 0u : 1u) << 10) | ((mn ? 3u : 0u) << 15) |
+         (static_cast<uint32_t>(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+template <bool kE4m3>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  const uint32_t acc = accumulate ? 1 : 0;
+  if (kE4m3)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// x0, x1 as two bf16 pairs, hi + lo: hi is x cut to bf16, lo the rest rounded (16 bits together).
+__device__ __forceinline__ void split_bf16x2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  const uint32_t u0 = __float_as_uint(x0), u1 = __float_as_uint(x1);
+  hi = __byte_perm(u0, u1, 0x7632);
+  lo = bf16x2(x0 - __uint_as_float(u0 & 0xffff0000u), x1 - __uint_as_float(u1 & 0xffff0000u));
+}
+
+// x0, x1 as two E4M3 pairs, hi + lo: hi is x rounded, lo the rest rounded.
+__device__ __forceinline__ void split_e4m3x2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  uint32_t h, l;
+  asm("{\n .reg .b32 f, g;\n .reg .b16 a, b;\n"
+      " cvt.rn.f16x2.f32 f, %3, %2;\n"
+      " cvt.rn.satfinite.e4m3x2.f16x2 a, f;\n"
+      " cvt.rn.f16x2.e4m3x2 g, a;\n"
+      " sub.rn.f16x2 f, f, g;\n"
+      " cvt.rn.satfinite.e4m3x2.f16x2 b, f;\n"
+      " cvt.u32.u16 %0, a;\n cvt.u32.u16 %1, b;\n}"
+      : "=r"(h), "=r"(l)
+      : "f"(x0), "f"(x1));
+  hi = h;
+  lo = l;
+}
+
+// Reduce kN values over the 32 lanes of a warp, halving the values a lane
+// keeps at every step: lane i ends with value `first` (and the next, for 64).
+// Fewer than 32 values end with copies in neighbouring lanes.
+template <int kN, bool kMax>
+__device__ __forceinline__ int reduce_columns(float (&v)[kN]) {
+  const int lane = threadIdx.x & 31;
+  int first = 0, n = kN;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    if (n > 1) {
+      n >>= 1;
+      const bool upper = lane & off;
+#pragma unroll
+      for (int i = 0; i < kN / 2; ++i) {
+        if (i < n) {
+          const float send = upper ? v[i] : v[i + n], keep = upper ? v[i + n] : v[i];
+          const float got = __shfl_xor_sync(0xffffffffu, send, off);
+          v[i] = kMax ? fmaxf(keep, got) : keep + got;
+        }
+      }
+      if (upper) first += n;
+    } else {
+      const float got = __shfl_xor_sync(0xffffffffu, v[0], off);
+      v[0] = kMax ? fmaxf(v[0], got) : v[0] + got;
+    }
   }
-  *page = p.block_table[table_row * p.bt_stride + pos / p.page_size];
-  *off = static_cast<int>(pos % p.page_size);
-  if (*page < 0 || *page >= p.num_pages) {
-    atomicOr(p.status, kStatusBounds);
-    return false;
+  return first;
+}
+
+// The tokens of a row: decode positions [first, last), or entries of its ids.
+__device__ __forceinline__ void row_range(const AttnParams& p, int row, bool report, int32_t& first, int32_t& last) {
+  if (p.token_ids) {
+    first = 0;
+    last = p.num_ids;
+    return;
   }
-  return true;
+  const int64_t cap = static_cast<int64_t>(p.bt_stride) * p.page_size;
+  const int32_t ke = p.row_ke[row];
+  first = p.row_ks ? max(p.row_ks[row], 0) : 0;
+  last = ke > cap ? static_cast<int32_t>(cap) : ke;
+  if (report && ke > cap && ke > first) atomicOr(p.status, kStatusBounds);
+  if (last < first) last = first;
+}
+
+__device__ __forceinline__ int64_t row_tiles(int32_t first, int32_t last) {
+  const int64_t n = (static_cast<int64_t>(last) - first + kAttnTile - 1) / kAttnTile;
+  return n > 0 ? n : 1;  // a row without tokens still has a result to write
 }
 
 }  // namespace
 
-// One CTA per (row, query head). Each warp takes every fourth token with a
-// running maximum and sum; the four joined at the end.
-template <int D, bool kE4m3>
-__global__ void __launch_bounds__(kAttnThreads) attention_kernel(const __grid_constant__ AttnParams p) {
-  constexpr int kPer = D / 32;
-  constexpr int kWarps = kAttnThreads / 32;
+template <int D, bool kE4m3, int N>
+__global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ AttnParams p) {
+  using S = Shape<D, kE4m3, N>;
+  constexpr int C = S::kCols;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  // operands first (1024-byte aligned), then rings, state and barriers
+  uint8_t* const units = smem;
+  uint8_t* const q_s = units + S::kSlots * S::kUnit;
+  uint8_t* const p_s = q_s + S::kQBufs * S::kQBytes;
+  int64_t* const ring_off = reinterpret_cast<int64_t*>(p_s + S::kPBytes);          // [ring][128]
+  float2* const ring_scale = reinterpret_cast<float2*>(ring_off + kAddrRing * 128);  // [ring][128], E4M3
+  uint32_t* const ring_mask = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(ring_off) + S::kRingBytes);
+  AttnSeg* const segs = reinterpret_cast<AttnSeg*>(ring_mask + kAddrRing * 4);
+  float* const m_s = reinterpret_cast<float*>(segs + kSegRing);  // [N] running maxima
+  float* const alpha_s = m_s + N;                                // [N] rescale factors, then 1 / l
+  float* const qscale_s = alpha_s + N;                           // [kQScales][N], E4M3: 1 / the scale Q was stored with
+  float* const scratch = qscale_s + (kE4m3 ? kQScales * N : 0);                       // [2][4][C]
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(scratch + 8 * C);
+  // barriers
+  constexpr int kFull = 0, kEmpty = kFull + S::kSlots, kSFull = kEmpty + S::kSlots, kSEmpty = kSFull + 2, kPFull = kSEmpty + 2,
+                kPvDone = kPFull + 1, kQEmpty = kPvDone + 1, kSegFull = kQEmpty + 2, kSegEmpty = kSegFull + kSegRing,
+                kAFull = kSegEmpty + kSegRing, kAEmpty = kAFull + kAddrRing, kDrain = kAEmpty + kAddrRing, kBars = kDrain + 1;
+  static_assert(kBars * 8 <= 640, "");
+  auto bar = [&](int i) { return smem_addr(bars + i); };
+
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  __shared__ long long warp_sum[kThreads / 32];
+  __shared__ long long start_idx;
+  __shared__ int start_row;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint64_t limit = static_cast<uint64_t>(p.wait_ns);
   griddep_launch_dependents();
+
+  if (tid == 0) {
+    for (int i = 0; i < S::kSlots; ++i) {
+      mbar_init(bar(kFull + i), kLoaders);
+      mbar_init(bar(kEmpty + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kSFull + i), 1);
+      mbar_init(bar(kSEmpty + i), kSoftmax);
+      mbar_init(bar(kQEmpty + i), 1);
+    }
+    mbar_init(bar(kPFull), kSoftmax);
+    mbar_init(bar(kPvDone), 1);
+    for (int i = 0; i < kSegRing; ++i) {
+      mbar_init(bar(kSegFull + i), 1);
+      mbar_init(bar(kSegEmpty + i), kSegReaders);
+    }
+    for (int i = 0; i < kAddrRing; ++i) {
+      mbar_init(bar(kAFull + i), 1);
+      mbar_init(bar(kAEmpty + i), kAddrReaders);
+    }
+    mbar_init(bar(kDrain), 1);
+    mbar_init_fence();
+    abort_flag = 0;
+    start_row = -1;
+  }
+  if (warp == 5) tmem_alloc(smem_addr(&tmem_slot), S::kTmem);
   griddep_wait();
-  __shared__ float acc_s[kWarps][D];
-  __shared__ float max_s[kWarps], sum_s[kWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int row = blockIdx.x, head = blockIdx.y, kv = head / p.group, heads = p.kv_heads * p.group;
-  const int64_t table_row = p.row_indices ? p.row_indices[row] : row;
-  float q[kPer], acc[kPer];
-  for (int i = 0; i < kPer; ++i) {
-    q[i] = load_element<false>(p.q, row * p.q_stride + static_cast<int64_t>(head) * D + lane + 32 * i);
-    acc[i] = 0.f;
+
+  // ---- this CTA's range of the tile list: prefix sums over the rows
+  const int per_thread = (p.rows + kThreads - 1) / kThreads;
+  long long mine = 0;
+  for (int i = 0; i < per_thread; ++i) {
+    const int r = tid * per_thread + i;
+    if (r >= p.rows) break;
+    int32_t first, last;
+    row_range(p, r, blockIdx.x == 0, first, last);
+    mine += row_tiles(first, last) * p.kv_heads;
   }
-  int64_t first = 0, last = p.num_ids;
-  if (!p.token_ids) {
-    first = p.row_ks ? max(p.row_ks[row], 0) : 0;
-    last = p.row_ke[row];
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
   }
-  float m = -INFINITY, l = 0.f;
-  for (int64_t t = first + warp; t < last; t += kWarps) {
-    const int64_t pos = p.token_ids ? p.token_ids[static_cast<int64_t>(row) * p.ids_ld + t] : t;
-    if (pos < 0) continue;
-    int64_t page;
-    int off;
-    if (!place_of(p, table_row, pos, &page, &off)) continue;
-    const int64_t in_page = static_cast<int64_t>(kv) * p.page_size + off;
-    const int64_t at = page * p.page_stride + in_page * D + lane;
-    float dot = 0.f;
-    for (int i = 0; i < kPer; ++i) dot = fmaf(q[i], load_element<kE4m3>(p.k_cache, at + 32 * i), dot);
-    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-    if (kE4m3) dot *= p.k_scales[page * p.scale_page_stride + in_page];
-    const float s = dot * p.scale_log2;
-    const float m_new = fmaxf(m, s);
-    const float old = exp2f(m - m_new), w = exp2f(s - m_new);
-    l = l * old + w;
-    const float wv = kE4m3 ? w * p.v_scales[page * p.scale_page_stride + in_page] : w;
-    for (int i = 0; i < kPer; ++i) acc[i] = fmaf(acc[i], old, wv * load_element<kE4m3>(p.v_cache, at + 32 * i));
-    m = m_new;
-  }
-  for (int i = 0; i < kPer; ++i) acc_s[warp][lane + 32 * i] = acc[i];
-  if (lane == 0) max_s[warp] = m, sum_s[warp] = l;
+  if (lane == 31) warp_sum[warp] = incl;
+  tc_fence_before();
   __syncthreads();
-  float most = -INFINITY, total = 0.f;
-  for (int w = 0; w < kWarps; ++w) most = fmaxf(most, max_s[w]);
-  for (int w = 0; w < kWarps; ++w) total += sum_s[w] > 0.f || sum_s[w] != sum_s[w] ? sum_s[w] * exp2f(max_s[w] - most) : 0.f;
-  const int64_t out_row = static_cast<int64_t>(row) * heads + head;
-  for (int d = threadIdx.x; d < D; d += kAttnThreads) {
-    float o = 0.f;
-    for (int w = 0; w < kWarps; ++w)
-      if (max_s[w] != -INFINITY) o += acc_s[w][d] * exp2f(max_s[w] - most);
-    p.out[out_row * D + d] = __bfloat16_as_ushort(__float2bfloat16_rn(total != 0.f ? o / total : 0.f));
+  tc_fence_after();
+  long long before = incl - mine, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += warp_sum[w];
+    total += warp_sum[w];
   }
-  if (p.lse && threadIdx.x == 0) p.lse[out_row] = (most + log2f(total)) * 0.69314718055994531f;
+  const long long chunk = (total + gridDim.x - 1) / gridDim.x;
+  const long long begin = chunk * blockIdx.x;
+  const long long work = begin < total ? min(chunk, total - begin) : 0;
+  if (work > 0 && begin >= before && begin < before + mine) {
+    long long at = before;
+    for (int i = 0; i < per_thread; ++i) {
+      const int r = tid * per_thread + i;
+      int32_t first, last;
+      row_range(p, r, false, first, last);
+      const long long t = row_tiles(first, last) * p.kv_heads;
+      if (begin < at + t) {
+        start_row = r;
+        start_idx = begin - at;
+        break;
+      }
+      at += t;
+    }
+  }
+  __syncthreads();
+  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem_o = tmem, tmem_sc = tmem + N;
+  const volatile int* const abort = &abort_flag;
+  auto fail = [&] {
+    abort_flag = 1;
+    atomicOr(p.status, kStatusTimeout);
+  };
+
+  // the softmax threads take registers that the others do not need: 256 x 72 + 256 x 184 = 512 x 128
+  if (warp < 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+  if (warp < 4) {
+    // ------------------------------------------------------------ loaders
+    const int cta0_stall = blockIdx.x == 0 ? p.stall_tile : -1;
+    constexpr int kChunks = S::kRow / 16;         // 16-byte pieces of a token
+    constexpr int kTok = 32 / kChunks;            // tokens per warp instruction
+    const int piece = lane % kChunks, sub = lane / kChunks;
+    const uint32_t units_a = smem_addr(units);
+    int issued = 0, signalled = 0;
+    bool ok = true;
+    auto signal = [&](int unit) {
+      // unit 2 t - 1 (and 0) is the K tile t: the stall test withholds it
+      if (cta0_stall >= 0 && unit == (cta0_stall == 0 ? 0 : 2 * cta0_stall - 1)) return;
+      mbar_arrive(bar(kFull + unit % S::kSlots));
+    };
+    auto drain = [&] {  // hand over everything issued: before any wait that could depend on it
+      cp_wait<0>();
+      fence_proxy_async_smem();
+      for (; signalled < issued; ++signalled) signal(signalled);
+    };
+    auto wait = [&](int b, uint32_t parity) {
+      if (ok && !mbar_test_wait(bar(b), parity)) {
+        drain();
+        ok = mbar_wait(bar(b), parity, abort, limit);
+        if (!ok) fail();
+      }
+      ok = __all_sync(0xffffffffu, ok);
+    };
+    auto copy_unit = [&](const uint8_t* base, int64_t off) {
+      const int slot = issued % S::kSlots;
+      if (issued >= S::kSlots) wait(kEmpty + slot, (issued / S::kSlots - 1) & 1);
+      if (!ok) return;
+      const uint32_t dst0 = units_a + slot * S::kUnit + (piece >> 3) * 16384;
+#pragma unroll
+      for (int i = 0; i < 32 / kTok; ++i) {
+        const int t = i * kTok + sub;
+        const int64_t o = __shfl_sync(0xffffffffu, off, t);
+        const int tok = warp * 32 + t;
+        cp16(dst0 + tok * 128 + (((piece & 7) ^ (tok & 7)) << 4), base + (o < 0 ? 0 : o) + piece * 16, o < 0 ? 0 : 16);
+      }
+      cp_commit();
+      ++issued;
+      if (issued > S::kAhead) {
+        cp_wait<S::kAhead>();
+        if (signalled < issued - S::kAhead) {
+          fence_proxy_async_smem();
+          signal(signalled++);
+        }
+      }
+    };
+    int64_t prev = -1;
+    int it = 0;
+    for (int seg = 0; ok; ++seg) {
+      wait(kSegFull + seg % kSegRing, (seg / kSegRing) & 1);
+      if (!ok) break;
+      const AttnSeg sg = segs[seg % kSegRing];
+      if (sg.ntiles == 0) break;
+      // the segment's queries, in the commit group of its first K tile
+      const int qb = seg % S::kQBufs;
+      if (seg >= S::kQBufs) wait(kQEmpty + qb, (seg / S::kQBufs - 1) & 1);
+      if (!ok) break;
+      const uint16_t* qrow = p.q + sg.row * p.q_stride + static_cast<int64_t>(sg.kvh) * p.group * D;
+      uint8_t* const qdst = q_s + qb * S::kQBytes;
+      if (!kE4m3) {
+        constexpr int kQChunks = D * 2 / 16, kQTok = 32 / kQChunks;
+        const int c = lane % kQChunks;
+        for (int i = warp * kQTok + lane / kQChunks; i < N; i += 4 * kQTok)
+          cp16(smem_addr(qdst) + (c >> 3) * (N * 128) + i * 128 + (((c & 7) ^ (i & 7)) << 4),
+               qrow + (i < p.group ? i * D + c * 8 : 0), i < p.group ? 16 : 0);
+      } else {
+        // a head per D / 8 lanes; each stored as hi + lo times a power of two that brings its amax to (224, 448]
+        constexpr int kL = D / 8;
+        const int c = lane % kL;
+        for (int i0 = warp * (32 / kL); i0 < N; i0 += 4 * (32 / kL)) {
+          const int i = i0 + lane / kL;
+          uint4 w = make_uint4(0, 0, 0, 0);
+          if (i < p.group) w = *reinterpret_cast<const uint4*>(qrow + i * D + c * 8);
+          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+          float x[8], amax = 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            x[2 * k] = __uint_as_float(ws[k] << 16);
+            x[2 * k + 1] = __uint_as_float(ws[k] & 0xffff0000u);
+            amax = fmaxf(amax, fmaxf(fabsf(x[2 * k]), fabsf(x[2 * k + 1])));
+          }
+#pragma unroll
+          for (int o = kL / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          // amax = f * 2^e with f in [1, 2): the factor 2^(7 - e), or 2^(8 - e) where f <= 1.75
+          const uint32_t bits = __float_as_uint(amax);
+          int e = static_cast<int>(bits >> 23) - 127;
+          e = e < -100 ? -100 : e;
+          const int up = 7 - e + ((bits & 0x7fffffu) <= 0x600000u ? 1 : 0);
+          const float mul = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) split_e4m3x2(x[2 * k] * mul, x[2 * k + 1] * mul, hi[k], lo[k]);
+          uint8_t* dst = qdst + i * 128 + (((c >> 1) ^ (i & 7)) << 4) + (c & 1) * 8;
+          *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+          *reinterpret_cast<uint2*>(dst + S::kQPart) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+          if (c == 0) qscale_s[(seg % kQScales) * N + i] = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+        }
+      }
+      for (int j = 0; j < sg.ntiles && ok; ++j, ++it) {
+        const int a = it % kAddrRing;
+        wait(kAFull + a, (it / kAddrRing) & 1);
+        if (!ok) break;
+        const int64_t off = ring_off[a * 128 + warp * 32 + lane];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kAEmpty + a));
+        copy_unit(static_cast<const uint8_t*>(p.k_cache), off);
+        if (it > 0) copy_unit(static_cast<const uint8_t*>(p.v_cache), prev);
+        prev = off;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kSegEmpty + seg % kSegRing));
+    }
+    if (ok && it > 0) copy_unit(static_cast<const uint8_t*>(p.v_cache), prev);
+    drain();
+  } else if (warp == 4) {
+    // ---------------------------------------------------------- scheduler
+    long long left = work;
+    int row = start_row;
+    long long idx = work > 0 ? start_idx : 0;
+    int4 info = make_int4(0, 0, 0, 0);
+    int base = -64, seg = 0;
+    int32_t first_l = 0, last_l = 0;
+    bool ok = true;
+    while (ok) {
+      AttnSeg sg;
+      sg.ntiles = 0;
+      if (left > 0) {
+        if (row >= base + 32) {  // the next 32 rows' ranges, one per lane
+          base = row;
+          if (row + lane < p.rows) row_range(p, row + lane, false, first_l, last_l);
+        }
+        sg.first = __shfl_sync(0xffffffffu, first_l, row - base);
+        sg.last = __shfl_sync(0xffffffffu, last_l, row - base);
+        const long long t = row_tiles(sg.first, sg.last);
+        sg.row = row;
+        sg.kvh = static_cast<int>(idx / t);
+        sg.tile0 = static_cast<int>(idx % t);
+        const long long n = min(t - sg.tile0, left);
+        sg.ntiles = static_cast<int>(n);
+        const bool starts = sg.tile0 == 0, ends = sg.tile0 + n == t;
+        sg.slot = starts && ends ? -1 : 2 * static_cast<int>(blockIdx.x) + (starts ? 1 : 0);
+        if (starts && !ends) info = make_int4(row, sg.kvh, static_cast<int>((t - n + chunk - 1) / chunk), 0);
+        left -= n;
+        idx += n;
+        if (idx == t * p.kv_heads) {
+          ++row;
+          idx = 0;
+        }
+      }
+      if (seg >= kSegRing) ok = warp_wait(bar(kSegEmpty + seg % kSegRing), (seg / kSegRing - 1) & 1, abort, limit);
+      if (!ok) break;
+      if (lane == 0) {
+        segs[seg % kSegRing] = sg;
+        mbar_arrive(bar(kSegFull + seg % kSegRing));
+      }
+      ++seg;
+      if (sg.ntiles == 0) break;
+    }
+    if (lane == 0) {
+      if (!ok) fail();
+      p.seg_info[blockIdx.x] = info;
+    }
+  } else if (warp == 5) {
+    // ---------------------------------------------------------------- MMA
+    if (lane == 0) {
+      constexpr uint32_t kQkDesc = mma_idesc(kE4m3, false, N), kPvDesc = mma_idesc(kE4m3, true, N);
+      constexpr int kQkSteps = S::kRow / 32;       // 32 bytes of K per MMA
+      constexpr int kPvSteps = kE4m3 ? 4 : 8;      // 128 tokens, 32 or 16 per MMA
+      const uint32_t units_a = smem_addr(units), q_a = smem_addr(q_s), p_a = smem_addr(p_s);
+      bool ok = true;
+      auto wait = [&](int b, uint32_t parity) {
+        ok = ok && mbar_wait(bar(b), parity, abort, limit);
+        return ok;
+      };
+      int unit = 0, it = 0;
+      bool prev_first = false;
+      auto pv = [&](int t, bool fresh) {
+        const int slot = unit % S::kSlots;
+        if (!wait(kFull + slot, (unit / S::kSlots) & 1) || !wait(kPFull, t & 1)) return;
+        tc_fence_after();
+        const uint32_t v = units_a + slot * S::kUnit;
+        for (int part = 0; part < 2; ++part)
+          for (int k = 0; k < kPvSteps; ++k)
+            mma<kE4m3>(tmem_o, operand_desc(v + k * (kE4m3 ? 4096 : 2048), 128, 16384),
+                       operand_desc(p_a + part * S::kPPart + k * (kE4m3 ? 32 : 16) * S::kPRow, S::kPRow, 16384), kPvDesc,
+                       !(fresh && part == 0 && k == 0));
+        mma_commit(bar(kEmpty + slot));
+        mma_commit(bar(kPvDone));
+        ++unit;
+      };
+      for (int seg = 0; ok; ++seg) {
+        if (!wait(kSegFull + seg % kSegRing, (seg / kSegRing) & 1)) break;
+        const int n = segs[seg % kSegRing].ntiles;
+        mbar_arrive(bar(kSegEmpty + seg % kSegRing));
+        if (n == 0) break;
+        const int qb = seg % S::kQBufs;
+        for (int j = 0; j < n && ok; ++j, ++it) {
+          const int slot = unit % S::kSlots;
+          if (!wait(kFull + slot, (unit / S::kSlots) & 1)) break;
+          if (it >= 2 && !wait(kSEmpty + (it & 1), ((it >> 1) - 1) & 1)) break;
+          tc_fence_after();
+          const uint32_t k0 = units_a + slot * S::kUnit, q0 = q_a + qb * S::kQBytes;
+          for (int part = 0; part < S::kQParts; ++part)
+            for (int k = 0; k < kQkSteps; ++k)
+              mma<kE4m3>(tmem_sc + (it & 1) * N, operand_desc(k0 + (k >> 2) * 16384 + (k & 3) * 32, 128, 16),
+                         operand_desc(q0 + part * S::kQPart + (k >> 2) * (N * 128) + (k & 3) * 32, 128, 16), kQkDesc,
+                         part + k > 0);
+          mma_commit(bar(kEmpty + slot));
+          mma_commit(bar(kSFull + (it & 1)));
+          if (j == n - 1) mma_commit(bar(kQEmpty + qb));
+          ++unit;
+          if (it > 0) pv(it - 1, prev_first);
+          prev_first = j == 0;
+        }
+      }
+      if (ok && it > 0) pv(it - 1, prev_first);
+      if (!ok) {
+        fail();
+        // let the MMAs issued so far finish before TMEM is freed
+        mma_commit(bar(kDrain));
+        int never = 0;
+        mbar_wait(bar(kDrain), 0, &never, limit);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------- addresses
+    int it = 0;
+    bool ok = true;
+    for (int seg = 0; ok; ++seg) {
+      ok = warp_wait(bar(kSegFull + seg % kSegRing), (seg / kSegRing) & 1, abort, limit);
+      if (!ok) break;
+      const AttnSeg sg = segs[seg % kSegRing];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kSegEmpty + seg % kSegRing));
+      if (sg.ntiles == 0) break;
+      const int64_t table_row = p.row_indices ? p.row_indices[sg.row] : sg.row;
+      const bool row_ok = table_row >= 0 && table_row < p.bt_rows;
+      const int32_t* table = p.block_table + (row_ok ? table_row : 0) * p.bt_stride;
+      for (int j = 0; j < sg.ntiles; ++j, ++it) {
+        if ((it & 1) != (warp & 1)) continue;
+        const int a = it % kAddrRing;
+        if (it >= kAddrRing) ok = warp_wait(bar(kAEmpty + a), (it / kAddrRing - 1) & 1, abort, limit);
+        if (!ok) break;
+        int32_t pos[4], page[4];
+        bool bad = false;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int64_t e = static_cast<int64_t>(sg.tile0 + j) * kAttnTile + k * 32 + lane;
+          pos[k] = -1;
+          if (p.token_ids) {
+            if (e < sg.last) pos[k] = p.token_ids[static_cast<int64_t>(sg.row) * p.ids_ld + e];
+          } else if (sg.first + e < sg.last) {
+            pos[k] = static_cast<int32_t>(sg.first + e);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          page[k] = -1;
+          if (pos[k] >= 0) {
+            const int32_t col = pos[k] / p.page_size;
+            if (row_ok && col < p.bt_stride)
+              page[k] = table[col];
+            if (page[k] < 0 || page[k] >= p.num_pages) {
+              bad = true;
+              page[k] = -1;
+            }
+          }
+        }
+        float2 sc[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          int64_t off = -1;
+          sc[k] = make_float2(1.f, 1.f);
+          if (page[k] >= 0) {
+            const int64_t in_page = static_cast<int64_t>(sg.kvh) * p.page_size + pos[k] % p.page_size;
+            off = (page[k] * p.page_stride + in_page * D) * (kE4m3 ? 1 : 2);
+            if (kE4m3) {
+              const int64_t at = page[k] * p.scale_page_stride + in_page;
+              sc[k] = make_float2(p.k_scales[at], p.v_scales[at]);
+            }
+          }
+          ring_off[a * 128 + k * 32 + lane] = off;
+          const uint32_t mask = __ballot_sync(0xffffffffu, off >= 0);
+          if (lane == 0) ring_mask[a * 4 + k] = mask;
+        }
+        if (kE4m3)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) ring_scale[a * 128 + k * 32 + lane] = sc[k];
+        if (bad) atomicOr(p.status, kStatusBounds);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kAFull + a));
+      }
+    }
+    if (!ok && lane == 0) fail();
+  }
+  } else {
+    // ------------------------------------------------------------ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    const int wg = (warp - 8) >> 2, quarter = warp & 3;
+    const int t = quarter * 32 + lane;          // this thread's token, and its row of O^T
+    const int c0 = wg * C;                      // its first head
+    const int bar_id = 1 + wg, wt = tid & 127;
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t o_col = tmem_o + lanes + c0;
+    float* const red = scratch + wg * 4 * C;
+    const uint32_t p_a = smem_addr(p_s);
+    bool failed = false, leave = false;
+    int it = 0;
+    auto wait = [&](int b, uint32_t parity) {
+      if (!failed && !mbar_wait(bar(b), parity, abort, limit)) {
+        failed = true;
+        fail();
+      }
+    };
+    float l[C];
+    for (int seg = 0;; ++seg) {
+      wait(kSegFull + seg % kSegRing, (seg / kSegRing) & 1);
+      // a group leaves together: a failed wait anywhere in it ends all of it
+      if (bar_or(bar_id, 128, failed)) break;
+      const AttnSeg sg = segs[seg % kSegRing];
+      if (sg.ntiles == 0) break;
+      if (wt < C) m_s[c0 + wt] = kUnset;
+#pragma unroll
+      for (int c = 0; c < C; ++c) l[c] = 0.f;
+      bar_sync(bar_id, 128);
+      const float* const qscale = qscale_s + (seg % kQScales) * N + c0;
+      for (int j = 0; j < sg.ntiles; ++j, ++it) {
+        const int a = it % kAddrRing;
+        wait(kAFull + a, (it / kAddrRing) & 1);
+        wait(kSFull + (it & 1), (it >> 1) & 1);
+        float s[C];
+        bool over = failed;
+        float add = 0.f, inv_vs = 1.f;
+        if (!failed) {
+          tc_fence_after();
+          const uint32_t s_col = tmem_sc + lanes + (it & 1) * N + c0;
+#pragma unroll
+          for (int c = 0; c < C; c += 8) tmem_ld8(s_col + c, reinterpret_cast<uint32_t*>(&s[c]));
+          float mul = p.scale_log2;
+          const bool valid = (ring_mask[a * 4 + quarter] >> lane) & 1;
+          if (kE4m3) {
+            const float2 sc = ring_scale[a * 128 + t];
+            mul *= sc.x;
+            add = lg2(sc.y);
+            inv_vs = 1.f / sc.y;
+          }
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < C; c += 8) pin8(&s[c]);
+          tc_fence_before();
+          mbar_arrive(bar(kSEmpty + (it & 1)));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kAEmpty + a));
+#pragma unroll
+          for (int c = 0; c < C; ++c) s[c] = (kE4m3 ? s[c] * qscale[c] : s[c]) * mul + add;
+          if (!valid) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) s[c] = -INFINITY;
+          }
+          float most = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < C; ++c) most = fmaxf(most, s[c] - m_s[c0 + c]);
+          over = most > S::kTau;
+        }
+        if (bar_or(bar_id, 128, over)) {
+          // raise the maxima of this group's heads to the tile's
+          if (j > 0) wait(kPvDone, (it - 1) & 1);  // O is final up to the previous tile
+          float v[C];
+#pragma unroll
+          for (int c = 0; c < C; ++c) v[c] = s[c];
+          const int first = reduce_columns<C, true>(v);
+#pragma unroll
+          for (int i = 0; i < (C > 32 ? C / 32 : 1); ++i) red[quarter * C + first + i] = v[i];
+          if (bar_or(bar_id, 128, failed)) {
+            leave = true;
+            break;
+          }
+          if (wt < C) {
+            const float old = m_s[c0 + wt];
+            const float top = fmaxf(fmaxf(red[wt], red[C + wt]), fmaxf(red[2 * C + wt], red[3 * C + wt])) - S::kTop;
+            const float now = fmaxf(old, top);
+            m_s[c0 + wt] = now;
+            alpha_s[c0 + wt] = ex2(old - now);
+          }
+          bar_sync(bar_id, 128);
+#pragma unroll
+          for (int c = 0; c < C; ++c) l[c] *= alpha_s[c0 + c];
+          if (j > 0) {
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < C; c += 8) {
+              float o[8];
+              tmem_ld8(o_col + c, reinterpret_cast<uint32_t*>(o));
+              tmem_wait_ld();
+              pin8(o);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) o[i] *= alpha_s[c0 + c + i];
+              tmem_st8(o_col + c, reinterpret_cast<uint32_t*>(o));
+            }
+            tmem_wait_st();
+            tc_fence_before();
+          }
+        }
+        if (it > 0) wait(kPvDone, (it - 1) & 1);  // P is free
+        // this thread's row of P: C heads of token t
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          s[c] = ex2(s[c] - m_s[c0 + c]);
+          l[c] = kE4m3 ? fmaf(s[c], inv_vs, l[c]) : l[c] + s[c];
+        }
+        const int swz = S::kPRow == 128 ? (t & 7) : S::kPRow == 64 ? ((t >> 1) & 3) : ((t >> 2) & 1);
+        if (!kE4m3) {
+          const uint32_t row_a = p_a + t * S::kPRow + (N == 128 ? wg * 16384 : 0);
+          const int chunk0 = N == 128 ? 0 : wg * (C / 8);
+#pragma unroll
+          for (int c = 0; c < C; c += 8) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) split_bf16x2(s[c + 2 * i], s[c + 2 * i + 1], hi[i], lo[i]);
+            const uint32_t at = row_a + (((chunk0 + c / 8) ^ swz) << 4);
+            sts16(at, hi[0], hi[1], hi[2], hi[3]);
+            sts16(at + S::kPPart, lo[0], lo[1], lo[2], lo[3]);
+          }
+        } else {
+          const uint32_t row_a = p_a + t * S::kPRow;
+#pragma unroll
+          for (int c = 0; c < C; c += 16) {
+            uint32_t hi[8], lo[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) split_e4m3x2(s[(c + 2 * i) % C], s[(c + 2 * i + 1) % C], hi[i], lo[i]);
+            const uint32_t at = row_a + (((wg * (C / 16) + c / 16) ^ swz) << 4);
+            sts16(at, hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16), hi[4] | (hi[5] << 16), hi[6] | (hi[7] << 16));
+            sts16(at + S::kPPart, lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16), lo[4] | (lo[5] << 16),
+                  lo[6] | (lo[7] << 16));
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(bar(kPFull));
+      }
+      if (leave) break;
+      // ---- the segment's result
+      wait(kPvDone, (it - 1) & 1);
+      const int first = reduce_columns<C, false>(l);
+#pragma unroll
+      for (int i = 0; i < (C > 32 ? C / 32 : 1); ++i) red[quarter * C + first + i] = l[i];
+      bar_sync(bar_id, 128);
+      if (wt < C && c0 + wt < p.group) {
+        const int h = c0 + wt;
+        const float sum = red[wt] + red[C + wt] + red[2 * C + wt] + red[3 * C + wt];
+        if (sg.slot < 0) {
+          alpha_s[h] = sum == 0.f ? 0.f : 1.f / sum;
+          if (p.lse)
+            p.lse[static_cast<int64_t>(sg.row) * p.kv_heads * p.group + sg.kvh * p.group + h] =
+                (m_s[h] + log2f(sum)) * 0.69314718055994531f;
+        } else {
+          alpha_s[h] = 1.f;
+          p.part_ml[static_cast<int64_t>(sg.slot) * p.group + h] = make_float2(m_s[h], sum);
+        }
+      }
+      bar_sync(bar_id, 128);
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < C; c += 8) {
+        if (c0 + c >= p.group) break;
+        float o[8];
+        tmem_ld8(o_col + c, reinterpret_cast<uint32_t*>(o));
+        tmem_wait_ld();
+        pin8(o);
+        if (t < D) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int h = c0 + c + i;
+            if (h < p.group) {
+              const float x = o[i] * alpha_s[h];
+              if (sg.slot < 0)
+                p.out[((static_cast<int64_t>(sg.row) * p.kv_heads + sg.kvh) * p.group + h) * D + t] =
+                    __bfloat16_as_ushort(__float2bfloat16_rn(x));
+              else
+                p.part_o[(static_cast<int64_t>(sg.slot) * p.group + h) * D + t] = x;
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kSegEmpty + seg % kSegRing));
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 5) tmem_dealloc(tmem, S::kTmem);
 }
 
-cudaError_t launch_attention(const AttnParams& p, bool e4m3, cudaStream_t stream) {
+// Join the partials of the item that CTA blockIdx.x of the attention kernel
+// began and others continued: out = sum_i w_i O_i / sum_i w_i l_i with
+// w_i = 2^(m_i - max m). blockIdx.y picks p.heads_per_cta heads. With one head
+// the eight warps share the partials, with eight each warp has a head.
+template <int D>
+__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ AttnParams p, int heads_per_cta) {
+  constexpr int kPer = D / 32;
+  griddep_launch_dependents();
+  griddep_wait();
+  const int4 info = p.seg_info[blockIdx.x];
+  const int parts = info.z + 1;
+  if (parts == 1) return;
+  __shared__ float acc_s[8][D], sum_s[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int shares = heads_per_cta == 1 ? 8 : 1;  // warps per head
+  const int h = blockIdx.y * heads_per_cta + (shares == 1 ? warp : 0);
+  const bool live = h < p.group;
+  auto slot = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i)); };
+  float m = -INFINITY, l = 0.f, acc[kPer];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
+  if (live) {
+    const int i0 = shares == 1 ? 0 : warp;
+    for (int i = lane; i < parts; i += 32) m = fmaxf(m, p.part_ml[slot(i) * p.group + h].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+#pragma unroll 8
+    for (int i = i0; i < parts; i += shares) {
+      const float2 ml = p.part_ml[slot(i) * p.group + h];
+      const float* src = p.part_o + (slot(i) * p.group + h) * D + lane * kPer;
+      float x[kPer];
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) x[k] = src[k];
+      const float w = exp2f(ml.x - m);
+      l = fmaf(ml.y, w, l);
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) acc[k] = fmaf(x[k], w, acc[k]);
+    }
+  }
+  if (shares > 1) {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) acc_s[warp][lane * kPer + k] = acc[k];
+    if (lane == 0) sum_s[warp] = l;
+    __syncthreads();
+    if (warp != 0) return;
+    l = 0.f;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
+    for (int w = 0; w < 8; ++w) {
+      l += sum_s[w];
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) acc[k] += acc_s[w][lane * kPer + k];
+    }
+  }
+  if (!live) return;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int64_t out_row = (static_cast<int64_t>(info.x) * p.kv_heads + info.y) * p.group + h;
+#pragma unroll
+  for (int k = 0; k < kPer; k += 2)
+    *reinterpret_cast<uint32_t*>(p.out + out_row * D + lane * kPer + k) = bf16x2(acc[k] * inv, acc[k + 1] * inv);
+  if (p.lse && lane == 0) p.lse[out_row] = (m + log2f(l)) * 0.69314718055994531f;
+}
+
+namespace {
+
+template <typename K, typename... A>
+cudaError_t launch(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.rows, p.kv_heads * p.group);
-  cfg.blockDim = dim3(kAttnThreads);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  auto kernel = p.head_dim == 128 ? (e4m3 ? attention_kernel<128, true> : attention_kernel<128, false>)
-                                  : (e4m3 ? attention_kernel<64, true> : attention_kernel<64, false>);
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Calls f with the kernel of a geometry and its shared-memory bytes.
+template <typename F>
+cudaError_t with_kernel(int head_dim, bool e4m3, int group, F f) {
+#define SMQ_ATTN(D, E, N) return f(attention_kernel<D, E, N>, static_cast<size_t>(Shape<D, E, N>::kSmem))
+  if (head_dim == 128) {
+    if (e4m3) {
+      if (group <= 32) SMQ_ATTN(128, true, 32);
+      if (group <= 64) SMQ_ATTN(128, true, 64);
+      SMQ_ATTN(128, true, 128);
+    }
+    if (group <= 16) SMQ_ATTN(128, false, 16);
+    if (group <= 32) SMQ_ATTN(128, false, 32);
+    if (group <= 64) SMQ_ATTN(128, false, 64);
+    SMQ_ATTN(128, false, 128);
+  }
+  if (e4m3) {
+    if (group <= 32) SMQ_ATTN(64, true, 32);
+    if (group <= 64) SMQ_ATTN(64, true, 64);
+    SMQ_ATTN(64, true, 128);
+  }
+  if (group <= 16) SMQ_ATTN(64, false, 16);
+  if (group <= 32) SMQ_ATTN(64, false, 32);
+  if (group <= 64) SMQ_ATTN(64, false, 64);
+  SMQ_ATTN(64, false, 128);
+#undef SMQ_ATTN
+}
+
+}  // namespace
+
+cudaError_t prepare_attention(int head_dim, bool e4m3, int group) {
+  return with_kernel(head_dim, e4m3, group, [](auto kernel, size_t smem) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  });
+}
+
+cudaError_t launch_attention(const AttnParams& p, bool e4m3, int grid, cudaStream_t stream) {
+  cudaError_t rc = with_kernel(p.head_dim, e4m3, p.group, [&](auto kernel, size_t smem) {
+    return launch(kernel, dim3(grid), kThreads, smem, stream, p);
+  });
+  if (rc != cudaSuccess) return rc;
+  // few items: an item has many partials, shared by a CTA per head
+  const int64_t items = static_cast<int64_t>(p.rows) * p.kv_heads;
+  const int heads_per_cta = items * 4 >= grid ? 8 : 1;
+  return launch(p.head_dim == 128 ? combine_kernel<128> : combine_kernel<64>,
+                dim3(grid, (p.group + heads_per_cta - 1) / heads_per_cta), 256, 0, stream, p, heads_per_cta);
 }
 
 }  // namespace smq

@@ -67,10 +67,20 @@ struct AttnParams {
   int32_t ids_ld;
   uint16_t* out;
   float* lse;  // may be null
+  // partial results: CTA c leaves slot 2 c for an item that an earlier CTA began and slot 2 c + 1 for
+  // one that a later CTA continues; seg_info[c] = (row, kv head, CTAs that continue it, 0) of the latter
+  int4* seg_info;    // [grid]
+  float2* part_ml;   // [2 grid][group] running maximum (log2) and sum
+  float* part_o;     // [2 grid][group][head_dim]
   int32_t* status;
+  // failure path: every wait gives up after wait_ns; with stall_tile >= 0 the loaders of CTA 0
+  // withhold that tile's keys (tests of the failure path only)
+  int64_t wait_ns;
+  int32_t stall_tile;
 };
 
 cudaError_t launch_append(const AppendParams& p, int head_dim, bool e4m3, int num_sms, cudaStream_t stream);
-cudaError_t launch_attention(const AttnParams& p, bool e4m3, cudaStream_t stream);
+cudaError_t prepare_attention(int head_dim, bool e4m3, int group);  // raise the dynamic-smem limit, once per plan
+cudaError_t launch_attention(const AttnParams& p, bool e4m3, int grid, cudaStream_t stream);
 
 }  // namespace smq

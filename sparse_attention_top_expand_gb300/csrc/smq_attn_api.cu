@@ -18,6 +18,7 @@ struct smq_attn_plan {
   int32_t stall_tile;  // failure-path tests: a withheld hand-off, -1: none
   int32_t num_sms;
   float scale;
+  bool prepared;
 };
 
 namespace {
@@ -26,12 +27,34 @@ constexpr size_t kStatusBytes = 256;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-size_t workspace_bytes_for(const smq_attn_plan*) { return kStatusBytes; }
+// Workspace: [status word, 256 B][one int4 per CTA][maxima and sums][partial outputs], two partials per CTA.
+struct Scratch {
+  size_t info, ml, o, end;
+};
 
-int check_device(const smq_attn_plan* p) {
+Scratch scratch_of(const smq_attn_plan* p) {
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const size_t slots = 2 * static_cast<size_t>(p->num_sms);
+  const size_t group = p->desc.num_heads / p->desc.num_kv_heads;
+  Scratch s;
+  s.info = kStatusBytes;
+  s.ml = s.info + up(p->num_sms * sizeof(int4));
+  s.o = s.ml + up(slots * group * sizeof(float2));
+  s.end = s.o + slots * group * p->desc.head_dim * sizeof(float);
+  return s;
+}
+
+int check_device(smq_attn_plan* p) {
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return SMQ_ERR_CUDA;
-  return dev == p->desc.device ? SMQ_OK : SMQ_ERR_INVALID_ARG;
+  if (dev != p->desc.device) return SMQ_ERR_INVALID_ARG;
+  if (!p->prepared) {
+    if (smq::prepare_attention(p->desc.head_dim, p->desc.cache_type == SMQ_CACHE_E4M3,
+                               p->desc.num_heads / p->desc.num_kv_heads) != cudaSuccess)
+      return SMQ_ERR_CUDA;
+    p->prepared = true;
+  }
+  return SMQ_OK;
 }
 
 struct CacheArgs {
@@ -79,8 +102,8 @@ int run_attention(const smq_attn_plan* plan, const smq_attention_args* args, boo
   }
   if (!a.out || !aligned(a.out, 16) || !aligned(a.lse, 4) || !a.workspace || !aligned(a.workspace, 16))
     return SMQ_ERR_INVALID_ARG;
-  if (a.workspace_bytes < workspace_bytes_for(plan)) return SMQ_ERR_WORKSPACE_TOO_SMALL;
-  rc = check_device(plan);
+  if (a.workspace_bytes < scratch_of(plan).end) return SMQ_ERR_WORKSPACE_TOO_SMALL;
+  rc = check_device(const_cast<smq_attn_plan*>(plan));
   if (rc != SMQ_OK) return rc;
   smq::AttnParams p;
   std::memset(&p, 0, sizeof p);
@@ -110,8 +133,15 @@ int run_attention(const smq_attn_plan* plan, const smq_attention_args* args, boo
   p.ids_ld = a.ids_ld;
   p.out = a.out;
   p.lse = a.lse;
+  const Scratch w = scratch_of(plan);
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  p.seg_info = reinterpret_cast<int4*>(ws + w.info);
+  p.part_ml = reinterpret_cast<float2*>(ws + w.ml);
+  p.part_o = reinterpret_cast<float*>(ws + w.o);
   p.status = static_cast<int32_t*>(a.workspace);
-  return smq::launch_attention(p, d.cache_type == SMQ_CACHE_E4M3, static_cast<cudaStream_t>(stream)) == cudaSuccess
+  p.wait_ns = plan->wait_ns;
+  p.stall_tile = plan->stall_tile;
+  return smq::launch_attention(p, d.cache_type == SMQ_CACHE_E4M3, plan->num_sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? SMQ_OK
              : SMQ_ERR_CUDA;
 }
@@ -145,6 +175,7 @@ SMQ_API int smq_attn_plan_create(const smq_attn_plan_desc* desc, smq_attn_plan**
   p->wait_ns = 2000000000ll;  // 2 s: far beyond any legitimate wait
   p->stall_tile = -1;
   p->num_sms = sms;
+  p->prepared = false;
   p->scale = d.softmax_scale != 0.f ? d.softmax_scale : 1.f / std::sqrt(static_cast<float>(d.head_dim));
   *plan = p;
   return SMQ_OK;
@@ -169,7 +200,7 @@ SMQ_API int smq_attn_plan_inject_stall(smq_attn_plan* plan, int32_t tile) {
 
 SMQ_API int smq_attn_workspace_size(const smq_attn_plan* plan, size_t* bytes) {
   if (!plan || !bytes) return SMQ_ERR_INVALID_ARG;
-  *bytes = workspace_bytes_for(plan);
+  *bytes = scratch_of(plan).end;
   return SMQ_OK;
 }
 
@@ -199,7 +230,7 @@ SMQ_API int sparse_mqa_append_kv(const smq_attn_plan* plan, const smq_append_arg
   if (rc != SMQ_OK) return rc;
   if (!a.workspace || !aligned(a.workspace, 16)) return SMQ_ERR_INVALID_ARG;
   if (a.workspace_bytes < kStatusBytes) return SMQ_ERR_WORKSPACE_TOO_SMALL;
-  rc = check_device(plan);
+  rc = check_device(const_cast<smq_attn_plan*>(plan));
   if (rc != SMQ_OK) return rc;
   smq::AppendParams p;
   std::memset(&p, 0, sizeof p);
