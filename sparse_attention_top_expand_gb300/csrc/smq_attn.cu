@@ -69,7 +69,7 @@ struct Shape {
   static constexpr int kQParts = kE4m3 ? 2 : 1;                  // hi and lo of Q
   static constexpr int kQPart = kBlocks * N * 128;
   static constexpr int kQBytes = kQParts * kQPart;
-  static constexpr int kQBufs = N == 128 ? 1 : 2;
+  static constexpr int kQBufs = N >= 64 ? 1 : 2;
   static constexpr int kPRow = N * (kE4m3 ? 1 : 2) > 128 ? 128 : N * (kE4m3 ? 1 : 2);  // bytes of a P row in a block
   static constexpr int kPPart = 128 * N * (kE4m3 ? 1 : 2);
   static constexpr int kPBytes = 2 * kPPart;                     // hi and lo of P
@@ -80,12 +80,11 @@ struct Shape {
   static constexpr int kFixed = kQBufs * kQBytes + kPBytes + kMisc;
   static constexpr int kFit = (kSmemLimit - kFixed) / kUnit;
   static constexpr int kSlots = kFit > 12 ? 12 : kFit;
-  static constexpr int kAhead = kSlots > 8 ? 6 : kSlots - 2;     // units in flight per loader thread
   static constexpr int kSmem = kSlots * kUnit + kFixed;
   static constexpr int kTmem = 3 * N <= 64 ? 64 : 3 * N <= 128 ? 128 : 3 * N <= 256 ? 256 : 512;
   static constexpr float kTop = kE4m3 ? 8.f : 0.f;               // log2 of P at the maximum
   static constexpr float kTau = kE4m3 ? 8.8f : 8.f;              // log2 of the largest P: 2^8.8 < 448
-  static_assert(kSlots >= 3 && kSmem <= kSmemLimit && kAhead < kSlots, "");
+  static_assert(kSlots >= 3 && kSmem <= kSmemLimit, "");
   static_assert(!kE4m3 || N >= 32, "");
   static_assert(kBlocks == 2 || kFixed >= 16384, "an M = 128 operand of a 64-wide bf16 head reads past its unit");
 };
@@ -105,10 +104,10 @@ __device__ __forceinline__ float lg2(float x) {
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kLeft>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// Arrive on an mbarrier, as one of its expected arrivals, once this thread's copies so far have landed.
+__device__ __forceinline__ void cp_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ void bar_sync(int id, int threads) {
@@ -146,13 +145,19 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Shared-memory matrix descriptor. K-major with 128-byte rows: sbo = 1024 (the
-// next 8 rows). M- or N-major: rows of `row` bytes hold consecutive M or N of
-// one k; sbo = 8 row (the next 8 k), lbo = the next block of M or N.
-__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr, uint32_t row, uint32_t lbo) {
-  const uint64_t swizzle = row == 128 ? 2 : row == 64 ? 4 : 6;
-  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
-         (static_cast<uint64_t>((8 * row) >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (swizzle << 61);
+// Shared-memory matrix descriptors, in two words. The high word: K-major with
+// 128-byte rows, or M- / N-major where rows of `row` bytes hold consecutive M
+// or N of one k; 8 rows are the stride. The low word: the address and, for
+// M- / N-major, the distance to the next block of M or N.
+__host__ __device__ constexpr uint32_t desc_hi(int row) {
+  return ((8 * row) >> 4) | (1u << 14) | (static_cast<uint32_t>(row == 128 ? 2 : row == 64 ? 4 : 6) << 29);
+}
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | ((lbo >> 4) << 16); }
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r != 0;
 }
 
 // Instruction descriptor: fp32 accumulation; kind::f16 with bf16 operands or
@@ -162,18 +167,21 @@ __host__ __device__ constexpr uint32_t mma_idesc(bool e4m3, bool mn, int n) {
          (static_cast<uint32_t>(n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
+// D[tmem] (+)= A x B; a and b are descriptors' low words.
 template <bool kE4m3>
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
-  const uint32_t acc = accumulate ? 1 : 0;
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t a_hi, uint32_t b, uint32_t b_hi, uint32_t idesc,
+                                    uint32_t accumulate) {
   if (kE4m3)
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n .reg .pred p;\n .reg .b64 x, y;\n mov.b64 x, {%1, %2};\n mov.b64 y, {%3, %4};\n setp.ne.b32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %5, p;\n}" ::"r"(d),
+        "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "r"(accumulate)
         : "memory");
   else
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n .reg .pred p;\n .reg .b64 x, y;\n mov.b64 x, {%1, %2};\n mov.b64 y, {%3, %4};\n setp.ne.b32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n}" ::"r"(d),
+        "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 
@@ -276,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   uint64_t* const bars = reinterpret_cast<uint64_t*>(scratch + 8 * C);
   // barriers
   constexpr int kFull = 0, kEmpty = kFull + S::kSlots, kSFull = kEmpty + S::kSlots, kSEmpty = kSFull + 2, kPFull = kSEmpty + 2,
-                kPvDone = kPFull + 1, kQEmpty = kPvDone + 1, kSegFull = kQEmpty + 2, kSegEmpty = kSegFull + kSegRing,
+                kPvDone = kPFull + 1, kQEmpty = kPvDone + 1, kQFull = kQEmpty + 2, kSegFull = kQFull + 2, kSegEmpty = kSegFull + kSegRing,
                 kAFull = kSegEmpty + kSegRing, kAEmpty = kAFull + kAddrRing, kDrain = kAEmpty + kAddrRing, kBars = kDrain + 1;
   static_assert(kBars * 8 <= 640, "");
   auto bar = [&](int i) { return smem_addr(bars + i); };
@@ -300,6 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       mbar_init(bar(kSFull + i), 1);
       mbar_init(bar(kSEmpty + i), kSoftmax);
       mbar_init(bar(kQEmpty + i), 1);
+      mbar_init(bar(kQFull + i), kLoaders);
     }
     mbar_init(bar(kPFull), kSoftmax);
     mbar_init(bar(kPvDone), 1);
@@ -376,61 +385,58 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   if (warp < 4) {
     // ------------------------------------------------------------ loaders
-    const int cta0_stall = blockIdx.x == 0 ? p.stall_tile : -1;
+    const int stall_unit = blockIdx.x != 0 || p.stall_tile < 0 ? -1 : p.stall_tile == 0 ? 0 : 2 * p.stall_tile - 1;
     constexpr int kChunks = S::kRow / 16;         // 16-byte pieces of a token
     constexpr int kTok = 32 / kChunks;            // tokens per warp instruction
     const int piece = lane % kChunks, sub = lane / kChunks;
     const uint32_t units_a = smem_addr(units);
-    int issued = 0, signalled = 0;
+    int unit = 0;
     bool ok = true;
-    auto signal = [&](int unit) {
-      // unit 2 t - 1 (and 0) is the K tile t: the stall test withholds it
-      if (cta0_stall >= 0 && unit == (cta0_stall == 0 ? 0 : 2 * cta0_stall - 1)) return;
-      mbar_arrive(bar(kFull + unit % S::kSlots));
-    };
-    auto drain = [&] {  // hand over everything issued: before any wait that could depend on it
-      cp_wait<0>();
-      fence_proxy_async_smem();
-      for (; signalled < issued; ++signalled) signal(signalled);
-    };
     auto wait = [&](int b, uint32_t parity) {
-      if (ok && !mbar_test_wait(bar(b), parity)) {
-        drain();
-        ok = mbar_wait(bar(b), parity, abort, limit);
-        if (!ok) fail();
-      }
-      ok = __all_sync(0xffffffffu, ok);
+      ok = ok && warp_wait(bar(b), parity, abort, limit);
+      if (!ok && lane == 0) fail();
     };
-    auto copy_unit = [&](const uint8_t* base, int64_t off) {
-      const int slot = issued % S::kSlots;
-      if (issued >= S::kSlots) wait(kEmpty + slot, (issued / S::kSlots - 1) & 1);
+    // The barrier counts each thread's copies when they land; the MMA thread's proxy fence, after its wait,
+    // orders them before the tensor core's reads.
+    auto copy_unit = [&](const uint8_t* base, int tile) {
+      const int slot = unit % S::kSlots;
+      if (unit >= S::kSlots) wait(kEmpty + slot, (unit / S::kSlots - 1) & 1);
       if (!ok) return;
       const uint32_t dst0 = units_a + slot * S::kUnit + (piece >> 3) * 16384;
+      const int64_t* const offs = ring_off + tile % kAddrRing * 128 + warp * 32 + sub;
+      constexpr int kBatch = 32 / kTok < 8 ? 32 / kTok : 8;  // addresses first, so that the copies issue back to back
 #pragma unroll
-      for (int i = 0; i < 32 / kTok; ++i) {
-        const int t = i * kTok + sub;
-        const int64_t o = __shfl_sync(0xffffffffu, off, t);
-        const int tok = warp * 32 + t;
-        cp16(dst0 + tok * 128 + (((piece & 7) ^ (tok & 7)) << 4), base + (o < 0 ? 0 : o) + piece * 16, o < 0 ? 0 : 16);
-      }
-      cp_commit();
-      ++issued;
-      if (issued > S::kAhead) {
-        cp_wait<S::kAhead>();
-        if (signalled < issued - S::kAhead) {
-          fence_proxy_async_smem();
-          signal(signalled++);
+      for (int i0 = 0; i0 < 32 / kTok; i0 += kBatch) {
+        const uint8_t* src[kBatch];
+        uint32_t bytes[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int64_t o = offs[(i0 + i) * kTok];
+          bytes[i] = o < 0 ? 0 : 16;
+          src[i] = base + piece * 16 + (o < 0 ? 0 : o);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int tok = warp * 32 + (i0 + i) * kTok + sub;
+          cp16(dst0 + tok * 128 + (((piece & 7) ^ (tok & 7)) << 4), src[i], bytes[i]);
         }
       }
+      // unit 2 t - 1 (0 for t = 0) is the K tile t: the stall test withholds it
+      if (stall_unit < 0 || unit != stall_unit) cp_arrive(bar(kFull + slot));
+      ++unit;
     };
-    int64_t prev = -1;
+    auto copy_values = [&](int tile) {
+      copy_unit(static_cast<const uint8_t*>(p.v_cache), tile);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kAEmpty + tile % kAddrRing));
+    };
     int it = 0;
     for (int seg = 0; ok; ++seg) {
       wait(kSegFull + seg % kSegRing, (seg / kSegRing) & 1);
       if (!ok) break;
       const AttnSeg sg = segs[seg % kSegRing];
       if (sg.ntiles == 0) break;
-      // the segment's queries, in the commit group of its first K tile
+      // the segment's queries: in bf16 its first K tile's barrier covers them, split in E4M3 they have one
       const int qb = seg % S::kQBufs;
       if (seg >= S::kQBufs) wait(kQEmpty + qb, (seg / S::kQBufs - 1) & 1);
       if (!ok) break;
@@ -474,23 +480,20 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           *reinterpret_cast<uint2*>(dst + S::kQPart) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
           if (c == 0) qscale_s[(seg % kQScales) * N + i] = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
         }
+        mbar_arrive(bar(kQFull + qb));
       }
       for (int j = 0; j < sg.ntiles && ok; ++j, ++it) {
         const int a = it % kAddrRing;
         wait(kAFull + a, (it / kAddrRing) & 1);
         if (!ok) break;
-        const int64_t off = ring_off[a * 128 + warp * 32 + lane];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kAEmpty + a));
-        copy_unit(static_cast<const uint8_t*>(p.k_cache), off);
-        if (it > 0) copy_unit(static_cast<const uint8_t*>(p.v_cache), prev);
-        prev = off;
+        copy_unit(static_cast<const uint8_t*>(p.k_cache), it);
+        if (it > 0) copy_values(it - 1);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kSegEmpty + seg % kSegRing));
     }
-    if (ok && it > 0) copy_unit(static_cast<const uint8_t*>(p.v_cache), prev);
-    drain();
+    if (ok && it > 0) copy_values(it - 1);
+    cp_wait_all();
   } else if (warp == 4) {
     // ---------------------------------------------------------- scheduler
     long long left = work;
@@ -541,65 +544,87 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     }
   } else if (warp == 5) {
     // ---------------------------------------------------------------- MMA
-    if (lane == 0) {
-      constexpr uint32_t kQkDesc = mma_idesc(kE4m3, false, N), kPvDesc = mma_idesc(kE4m3, true, N);
-      constexpr int kQkSteps = S::kRow / 32;       // 32 bytes of K per MMA
-      constexpr int kPvSteps = kE4m3 ? 4 : 8;      // 128 tokens, 32 or 16 per MMA
-      const uint32_t units_a = smem_addr(units), q_a = smem_addr(q_s), p_a = smem_addr(p_s);
-      bool ok = true;
-      auto wait = [&](int b, uint32_t parity) {
-        ok = ok && mbar_wait(bar(b), parity, abort, limit);
-        return ok;
-      };
-      int unit = 0, it = 0;
-      bool prev_first = false;
-      auto pv = [&](int t, bool fresh) {
-        const int slot = unit % S::kSlots;
-        if (!wait(kFull + slot, (unit / S::kSlots) & 1) || !wait(kPFull, t & 1)) return;
-        tc_fence_after();
-        const uint32_t v = units_a + slot * S::kUnit;
-        for (int part = 0; part < 2; ++part)
-          for (int k = 0; k < kPvSteps; ++k)
-            mma<kE4m3>(tmem_o, operand_desc(v + k * (kE4m3 ? 4096 : 2048), 128, 16384),
-                       operand_desc(p_a + part * S::kPPart + k * (kE4m3 ? 32 : 16) * S::kPRow, S::kPRow, 16384), kPvDesc,
-                       !(fresh && part == 0 && k == 0));
+    // The whole warp runs this loop, so that descriptors stay in uniform registers, and one elected thread issues.
+    constexpr uint32_t kQkDesc = mma_idesc(kE4m3, false, N), kPvDesc = mma_idesc(kE4m3, true, N);
+    constexpr int kQkSteps = S::kRow / 32;   // 32 bytes of K per MMA
+    constexpr int kPvSteps = kE4m3 ? 4 : 8;  // 128 tokens, 32 or 16 per MMA
+    constexpr uint32_t kRowHi = desc_hi(128), kPHi = desc_hi(S::kPRow);
+    const uint32_t k_lo = desc_lo(smem_addr(units), 16), v_lo = desc_lo(smem_addr(units), 16384);
+    const uint32_t q_lo = desc_lo(smem_addr(q_s), 16), p_lo = desc_lo(smem_addr(p_s), 16384);
+    bool ok = true;
+    auto wait = [&](int b, uint32_t parity) {
+      ok = ok && mbar_wait(bar(b), parity, abort, limit);
+      ok = __all_sync(0xffffffffu, ok);
+      return ok;
+    };
+    int slot = 0, it = 0;
+    uint32_t turn = 0;  // parity of the units' barriers
+    auto next_slot = [&] {
+      if (++slot == S::kSlots) {
+        slot = 0;
+        turn ^= 1;
+      }
+    };
+    bool prev_first = false;
+    auto pv = [&](int t, bool fresh) {
+      if (!wait(kFull + slot, turn) || !wait(kPFull, t & 1)) return;
+      fence_proxy_async_smem();
+      tc_fence_after();
+      const uint32_t a = v_lo + slot * (S::kUnit >> 4);
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < kPvSteps; ++k)
+#pragma unroll
+          for (int part = 0; part < 2; ++part)
+            mma<kE4m3>(tmem_o, a + k * ((kE4m3 ? 4096 : 2048) >> 4), kRowHi,
+                       p_lo + ((part * S::kPPart + k * (kE4m3 ? 32 : 16) * S::kPRow) >> 4), kPHi, kPvDesc,
+                       part + k > 0 || !fresh);
         mma_commit(bar(kEmpty + slot));
         mma_commit(bar(kPvDone));
-        ++unit;
-      };
-      for (int seg = 0; ok; ++seg) {
-        if (!wait(kSegFull + seg % kSegRing, (seg / kSegRing) & 1)) break;
-        const int n = segs[seg % kSegRing].ntiles;
-        mbar_arrive(bar(kSegEmpty + seg % kSegRing));
-        if (n == 0) break;
-        const int qb = seg % S::kQBufs;
-        for (int j = 0; j < n && ok; ++j, ++it) {
-          const int slot = unit % S::kSlots;
-          if (!wait(kFull + slot, (unit / S::kSlots) & 1)) break;
-          if (it >= 2 && !wait(kSEmpty + (it & 1), ((it >> 1) - 1) & 1)) break;
-          tc_fence_after();
-          const uint32_t k0 = units_a + slot * S::kUnit, q0 = q_a + qb * S::kQBytes;
+      }
+      __syncwarp();
+      next_slot();
+    };
+    for (int seg = 0; ok; ++seg) {
+      if (!wait(kSegFull + seg % kSegRing, (seg / kSegRing) & 1)) break;
+      const int n = segs[seg % kSegRing].ntiles;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kSegEmpty + seg % kSegRing));
+      if (n == 0) break;
+      const int qb = seg % S::kQBufs;
+      for (int j = 0; j < n; ++j, ++it) {
+        if (!wait(kFull + slot, turn)) break;
+        if (kE4m3 && j == 0 && !wait(kQFull + qb, (seg / S::kQBufs) & 1)) break;
+        if (it >= 2 && !wait(kSEmpty + (it & 1), ((it >> 1) - 1) & 1)) break;
+        fence_proxy_async_smem();
+        tc_fence_after();
+        const uint32_t a = k_lo + slot * (S::kUnit >> 4), q = q_lo + qb * (S::kQBytes >> 4);
+        if (elect_one()) {
+#pragma unroll
           for (int part = 0; part < S::kQParts; ++part)
+#pragma unroll
             for (int k = 0; k < kQkSteps; ++k)
-              mma<kE4m3>(tmem_sc + (it & 1) * N, operand_desc(k0 + (k >> 2) * 16384 + (k & 3) * 32, 128, 16),
-                         operand_desc(q0 + part * S::kQPart + (k >> 2) * (N * 128) + (k & 3) * 32, 128, 16), kQkDesc,
+              mma<kE4m3>(tmem_sc + (it & 1) * N, a + (((k >> 2) * 16384 + (k & 3) * 32) >> 4), kRowHi,
+                         q + ((part * S::kQPart + (k >> 2) * (N * 128) + (k & 3) * 32) >> 4), kRowHi, kQkDesc,
                          part + k > 0);
           mma_commit(bar(kEmpty + slot));
           mma_commit(bar(kSFull + (it & 1)));
           if (j == n - 1) mma_commit(bar(kQEmpty + qb));
-          ++unit;
-          if (it > 0) pv(it - 1, prev_first);
-          prev_first = j == 0;
         }
+        __syncwarp();
+        next_slot();
+        if (it > 0) pv(it - 1, prev_first);
+        if (!ok) break;
+        prev_first = j == 0;
       }
-      if (ok && it > 0) pv(it - 1, prev_first);
-      if (!ok) {
-        fail();
-        // let the MMAs issued so far finish before TMEM is freed
-        mma_commit(bar(kDrain));
-        int never = 0;
-        mbar_wait(bar(kDrain), 0, &never, limit);
-      }
+    }
+    if (ok && it > 0) pv(it - 1, prev_first);
+    if (!ok) {
+      if (lane == 0) fail();
+      // let the MMAs issued so far finish before TMEM is freed
+      if (elect_one()) mma_commit(bar(kDrain));
+      const int never = 0;
+      mbar_wait(bar(kDrain), 0, &never, limit);
     }
     __syncwarp();
   } else {
