@@ -48,7 +48,6 @@ constexpr int kSegRing = 8;     // segments published ahead
 constexpr int kQScales = 8;
 constexpr int kSegReaders = 4 + 1 + 2 + 8;   // loader, MMA, address and softmax warps
 constexpr int kAddrReaders = 4 + 8;          // loader and softmax warps
-constexpr float kUnset = -3.0e38f;           // the running maximum before the first score
 constexpr int kSmemLimit = 232448 - 1024;  // less the static part
 
 // A run of tiles of one (row, kv head) item.
@@ -75,14 +74,14 @@ struct Shape {
   static constexpr int kPBytes = 2 * kPPart;                     // hi and lo of P
   static constexpr int kCols = N / 2;                            // heads per softmax thread
   static constexpr int kRingBytes = kAddrRing * 128 * (8 + (kE4m3 ? 8 : 0));
-  static constexpr int kMisc = kRingBytes + kAddrRing * 16 + kSegRing * 32 + 640 /*barriers*/ + N * 8 /*m, alpha*/ +
+  static constexpr int kMisc = kRingBytes + kAddrRing * 16 + kSegRing * 32 + 640 /*barriers*/ + N * 12 /*m, alpha, raise*/ +
                                (kE4m3 ? kQScales * N * 4 : 0) + 8 * kCols * 4 /*scratch*/ + 64;
   static constexpr int kFixed = kQBufs * kQBytes + kPBytes + kMisc;
   static constexpr int kFit = (kSmemLimit - kFixed) / kUnit;
   static constexpr int kSlots = kFit > 12 ? 12 : kFit;
   static constexpr int kSmem = kSlots * kUnit + kFixed;
-  static constexpr int kTmem = 3 * N <= 64 ? 64 : 3 * N <= 128 ? 128 : 3 * N <= 256 ? 256 : 512;
-  static constexpr float kTop = kE4m3 ? 8.f : 0.f;               // log2 of P at the maximum
+  static constexpr int kTmem = 4 * N;                            // O from hi and from lo, two buffers of S
+  static constexpr float kTop = kE4m3 ? 4.f : 0.f;               // log2 of P at the maximum
   static constexpr float kTau = kE4m3 ? 8.8f : 8.f;              // log2 of the largest P: 2^8.8 < 448
   static_assert(kSlots >= 3 && kSmem <= kSmemLimit, "");
   static_assert(!kE4m3 || N >= 32, "");
@@ -197,7 +196,9 @@ __device__ __forceinline__ void split_bf16x2(float x0, float x1, uint32_t& hi, u
   lo = bf16x2(x0 - __uint_as_float(u0 & 0xffff0000u), x1 - __uint_as_float(u1 & 0xffff0000u));
 }
 
-// x0, x1 as two E4M3 pairs, hi + lo: hi is x rounded, lo the rest rounded.
+// x0, x1 as two E4M3 pairs, hi + lo / kLift: hi is x rounded, lo the rest times kLift rounded (9 bits together).
+constexpr float kLift = 16.f;  // hi's rest is at most 1/16 of 448 / 2, so 16 times that still fits
+template <bool kLifted>
 __device__ __forceinline__ void split_e4m3x2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
   uint32_t h, l;
   asm("{\n .reg .b32 f, g;\n .reg .b16 a, b;\n"
@@ -205,10 +206,11 @@ __device__ __forceinline__ void split_e4m3x2(float x0, float x1, uint32_t& hi, u
       " cvt.rn.satfinite.e4m3x2.f16x2 a, f;\n"
       " cvt.rn.f16x2.e4m3x2 g, a;\n"
       " sub.rn.f16x2 f, f, g;\n"
+      " mul.rn.f16x2 f, f, %4;\n"
       " cvt.rn.satfinite.e4m3x2.f16x2 b, f;\n"
       " cvt.u32.u16 %0, a;\n cvt.u32.u16 %1, b;\n}"
       : "=r"(h), "=r"(l)
-      : "f"(x0), "f"(x1));
+      : "f"(x0), "f"(x1), "r"(kLifted ? 0x4c004c00u : 0x3c003c00u));
   hi = h;
   lo = l;
 }
@@ -279,7 +281,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   AttnSeg* const segs = reinterpret_cast<AttnSeg*>(ring_mask + kAddrRing * 4);
   float* const m_s = reinterpret_cast<float*>(segs + kSegRing);  // [N] running maxima
   float* const alpha_s = m_s + N;                                // [N] rescale factors, then 1 / l
-  float* const qscale_s = alpha_s + N;                           // [kQScales][N], E4M3: 1 / the scale Q was stored with
+  float* const up_s = alpha_s + N;                               // [N] the last raise of each maximum
+  float* const qscale_s = up_s + N;                              // [kQScales][N], E4M3: 1 / the scale Q was stored with
   float* const scratch = qscale_s + (kE4m3 ? kQScales * N : 0);                       // [2][4][C]
   uint64_t* const bars = reinterpret_cast<uint64_t*>(scratch + 8 * C);
   // barriers
@@ -306,11 +309,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kSFull + i), 1);
-      mbar_init(bar(kSEmpty + i), kSoftmax);
+      mbar_init(bar(kSEmpty + i), kSoftmax / 32);
       mbar_init(bar(kQEmpty + i), 1);
       mbar_init(bar(kQFull + i), kLoaders);
     }
-    mbar_init(bar(kPFull), kSoftmax);
+    mbar_init(bar(kPFull), kSoftmax / 32);
     mbar_init(bar(kPvDone), 1);
     for (int i = 0; i < kSegRing; ++i) {
       mbar_init(bar(kSegFull + i), 1);
@@ -373,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   }
   __syncthreads();
   const uint32_t tmem = tmem_slot;
-  const uint32_t tmem_o = tmem, tmem_sc = tmem + N;
+  const uint32_t tmem_o = tmem, tmem_sc = tmem + 2 * N;
   const volatile int* const abort = &abort_flag;
   auto fail = [&] {
     abort_flag = 1;
@@ -474,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           const float mul = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
           uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) split_e4m3x2(x[2 * k] * mul, x[2 * k + 1] * mul, hi[k], lo[k]);
+          for (int k = 0; k < 4; ++k) split_e4m3x2<false>(x[2 * k] * mul, x[2 * k + 1] * mul, hi[k], lo[k]);
           uint8_t* dst = qdst + i * 128 + (((c >> 1) ^ (i & 7)) << 4) + (c & 1) * 8;
           *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
           *reinterpret_cast<uint2*>(dst + S::kQPart) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
@@ -545,12 +548,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   } else if (warp == 5) {
     // ---------------------------------------------------------------- MMA
     // The whole warp runs this loop, so that descriptors stay in uniform registers, and one elected thread issues.
-    constexpr uint32_t kQkDesc = mma_idesc(kE4m3, false, N), kPvDesc = mma_idesc(kE4m3, true, N);
+    constexpr uint32_t kQkDesc = mma_idesc(kE4m3, false, N), kPvDesc = mma_idesc(kE4m3, true, 2 * N);
     constexpr int kQkSteps = S::kRow / 32;   // 32 bytes of K per MMA
     constexpr int kPvSteps = kE4m3 ? 4 : 8;  // 128 tokens, 32 or 16 per MMA
     constexpr uint32_t kRowHi = desc_hi(128), kPHi = desc_hi(S::kPRow);
     const uint32_t k_lo = desc_lo(smem_addr(units), 16), v_lo = desc_lo(smem_addr(units), 16384);
-    const uint32_t q_lo = desc_lo(smem_addr(q_s), 16), p_lo = desc_lo(smem_addr(p_s), 16384);
+    const uint32_t q_lo = desc_lo(smem_addr(q_s), 16), p_lo = desc_lo(smem_addr(p_s), 128 * S::kPRow);
     bool ok = true;
     auto wait = [&](int b, uint32_t parity) {
       ok = ok && mbar_wait(bar(b), parity, abort, limit);
@@ -574,11 +577,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < kPvSteps; ++k)
-#pragma unroll
-          for (int part = 0; part < 2; ++part)
-            mma<kE4m3>(tmem_o, a + k * ((kE4m3 ? 4096 : 2048) >> 4), kRowHi,
-                       p_lo + ((part * S::kPPart + k * (kE4m3 ? 32 : 16) * S::kPRow) >> 4), kPHi, kPvDesc,
-                       part + k > 0 || !fresh);
+          mma<kE4m3>(tmem_o, a + k * ((kE4m3 ? 4096 : 2048) >> 4), kRowHi, p_lo + ((k * (kE4m3 ? 32 : 16) * S::kPRow) >> 4),
+                     kPHi, kPvDesc, k > 0 || !fresh);
         mma_commit(bar(kEmpty + slot));
         mma_commit(bar(kPvDone));
       }
@@ -724,25 +724,28 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       if (bar_or(bar_id, 128, failed)) break;
       const AttnSeg sg = segs[seg % kSegRing];
       if (sg.ntiles == 0) break;
-      if (wt < C) m_s[c0 + wt] = kUnset;
+      if (wt < C) m_s[c0 + wt] = 0.f;
 #pragma unroll
       for (int c = 0; c < C; ++c) l[c] = 0.f;
       bar_sync(bar_id, 128);
       const float* const qscale = qscale_s + (seg % kQScales) * N + c0;
+      bool fresh = true;  // no token so far
       for (int j = 0; j < sg.ntiles; ++j, ++it) {
         const int a = it % kAddrRing;
         wait(kAFull + a, (it / kAddrRing) & 1);
         wait(kSFull + (it & 1), (it >> 1) & 1);
-        float s[C];
-        bool over = failed;
-        float add = 0.f, inv_vs = 1.f;
+        float s[C];  // scores, less the running maxima, then P
+        bool over = failed, first = false;
+        float inv_vs = 1.f;
         if (!failed) {
           tc_fence_after();
           const uint32_t s_col = tmem_sc + lanes + (it & 1) * N + c0;
 #pragma unroll
           for (int c = 0; c < C; c += 8) tmem_ld8(s_col + c, reinterpret_cast<uint32_t*>(&s[c]));
-          float mul = p.scale_log2;
-          const bool valid = (ring_mask[a * 4 + quarter] >> lane) & 1;
+          float mul = p.scale_log2, add = 0.f;
+          const uint4 mask = *reinterpret_cast<const uint4*>(ring_mask + a * 4);
+          const bool valid = ((quarter == 0 ? mask.x : quarter == 1 ? mask.y : quarter == 2 ? mask.z : mask.w) >> lane) & 1;
+          first = fresh && (mask.x | mask.y | mask.z | mask.w) != 0;
           if (kE4m3) {
             const float2 sc = ring_scale[a * 128 + t];
             mul *= sc.x;
@@ -753,94 +756,117 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 #pragma unroll
           for (int c = 0; c < C; c += 8) pin8(&s[c]);
           tc_fence_before();
-          mbar_arrive(bar(kSEmpty + (it & 1)));
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kAEmpty + a));
-#pragma unroll
-          for (int c = 0; c < C; ++c) s[c] = (kE4m3 ? s[c] * qscale[c] : s[c]) * mul + add;
-          if (!valid) {
-#pragma unroll
-            for (int c = 0; c < C; ++c) s[c] = -INFINITY;
+          if (lane == 0) {
+            mbar_arrive(bar(kSEmpty + (it & 1)));
+            mbar_arrive(bar(kAEmpty + a));
           }
           float most = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < C; ++c) most = fmaxf(most, s[c] - m_s[c0 + c]);
-          over = most > S::kTau;
+          for (int c = 0; c < C; c += 4) {
+            const float4 m4 = *reinterpret_cast<const float4*>(m_s + c0 + c);
+            float4 f4 = make_float4(mul, mul, mul, mul);
+            if (kE4m3) {
+              const float4 q4 = *reinterpret_cast<const float4*>(qscale + c);
+              f4.x *= q4.x, f4.y *= q4.y, f4.z *= q4.z, f4.w *= q4.w;
+            }
+            s[c] = fmaf(s[c], f4.x, add - m4.x);
+            s[c + 1] = fmaf(s[c + 1], f4.y, add - m4.y);
+            s[c + 2] = fmaf(s[c + 2], f4.z, add - m4.z);
+            s[c + 3] = fmaf(s[c + 3], f4.w, add - m4.w);
+            most = fmaxf(fmaxf(most, fmaxf(s[c], s[c + 1])), fmaxf(s[c + 2], s[c + 3]));
+          }
+          if (!valid) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) s[c] = -INFINITY;
+            most = -INFINITY;
+          }
+          over = most > S::kTau || first;
         }
-        if (bar_or(bar_id, 128, over)) {
-          // raise the maxima of this group's heads to the tile's
-          if (j > 0) wait(kPvDone, (it - 1) & 1);  // O is final up to the previous tile
-          float v[C];
+        const bool raise = bar_or(bar_id, 128, over);
+        if (raise) {
+          // raise this group's maxima to the tile's, or set them at the row's first tokens
+          constexpr int kHalf = C > 32 ? 32 : C;
 #pragma unroll
-          for (int c = 0; c < C; ++c) v[c] = s[c];
-          const int first = reduce_columns<C, true>(v);
+          for (int h = 0; h < C; h += kHalf) {
+            float v[kHalf];
 #pragma unroll
-          for (int i = 0; i < (C > 32 ? C / 32 : 1); ++i) red[quarter * C + first + i] = v[i];
+            for (int c = 0; c < kHalf; ++c) v[c] = s[h + c];
+            const int col = reduce_columns<kHalf, true>(v);
+            red[quarter * C + h + col] = v[0];
+          }
           if (bar_or(bar_id, 128, failed)) {
             leave = true;
             break;
           }
           if (wt < C) {
-            const float old = m_s[c0 + wt];
             const float top = fmaxf(fmaxf(red[wt], red[C + wt]), fmaxf(red[2 * C + wt], red[3 * C + wt])) - S::kTop;
-            const float now = fmaxf(old, top);
-            m_s[c0 + wt] = now;
-            alpha_s[c0 + wt] = ex2(old - now);
+            const float up = top == -INFINITY ? 0.f : first ? top : fmaxf(top, 0.f);
+            m_s[c0 + wt] += up;
+            up_s[c0 + wt] = up;
+            alpha_s[c0 + wt] = first ? 0.f : ex2(-up);
           }
           bar_sync(bar_id, 128);
 #pragma unroll
-          for (int c = 0; c < C; ++c) l[c] *= alpha_s[c0 + c];
-          if (j > 0) {
-            tc_fence_after();
+          for (int c = 0; c < C; c += 4) {
+            const float4 a4 = *reinterpret_cast<const float4*>(alpha_s + c0 + c);
+            const float4 u4 = *reinterpret_cast<const float4*>(up_s + c0 + c);
+            l[c] *= a4.x, l[c + 1] *= a4.y, l[c + 2] *= a4.z, l[c + 3] *= a4.w;
+            s[c] -= u4.x, s[c + 1] -= u4.y, s[c + 2] -= u4.z, s[c + 3] -= u4.w;
+          }
+          if (first) fresh = false;
+        }
+        // this thread's row of P: C heads of token t, in two parts
+        constexpr int kWords = kE4m3 ? C / 4 : C / 2;
+        uint32_t hi[kWords], lo[kWords];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          s[c] = ex2(s[c]);
+          l[c] = kE4m3 ? fmaf(s[c], inv_vs, l[c]) : l[c] + s[c];
+        }
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+          if (kE4m3) {
+            uint32_t h0, h1, l0, l1;
+            split_e4m3x2<true>(s[(4 * i) % C], s[(4 * i + 1) % C], h0, l0);
+            split_e4m3x2<true>(s[(4 * i + 2) % C], s[(4 * i + 3) % C], h1, l1);
+            hi[i] = h0 | (h1 << 16);
+            lo[i] = l0 | (l1 << 16);
+          } else {
+            split_bf16x2(s[(2 * i) % C], s[(2 * i + 1) % C], hi[i], lo[i]);
+          }
+        }
+        if (it > 0) wait(kPvDone, (it - 1) & 1);  // O is final up to the previous tile, and P is free
+        if (raise && j > 0) {
+          tc_fence_after();
+#pragma unroll
+          for (int part = 0; part < 2; ++part)
 #pragma unroll
             for (int c = 0; c < C; c += 8) {
               float o[8];
-              tmem_ld8(o_col + c, reinterpret_cast<uint32_t*>(o));
+              tmem_ld8(o_col + part * N + c, reinterpret_cast<uint32_t*>(o));
               tmem_wait_ld();
               pin8(o);
 #pragma unroll
               for (int i = 0; i < 8; ++i) o[i] *= alpha_s[c0 + c + i];
-              tmem_st8(o_col + c, reinterpret_cast<uint32_t*>(o));
+              tmem_st8(o_col + part * N + c, reinterpret_cast<uint32_t*>(o));
             }
-            tmem_wait_st();
-            tc_fence_before();
-          }
-        }
-        if (it > 0) wait(kPvDone, (it - 1) & 1);  // P is free
-        // this thread's row of P: C heads of token t
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          s[c] = ex2(s[c] - m_s[c0 + c]);
-          l[c] = kE4m3 ? fmaf(s[c], inv_vs, l[c]) : l[c] + s[c];
+          tmem_wait_st();
+          tc_fence_before();
         }
         const int swz = S::kPRow == 128 ? (t & 7) : S::kPRow == 64 ? ((t >> 1) & 3) : ((t >> 2) & 1);
-        if (!kE4m3) {
-          const uint32_t row_a = p_a + t * S::kPRow + (N == 128 ? wg * 16384 : 0);
-          const int chunk0 = N == 128 ? 0 : wg * (C / 8);
+        constexpr bool kWide = N == 128 && !kE4m3;  // a block of 64 heads for each group
+        const uint32_t row_a = p_a + t * S::kPRow + (kWide ? wg * 128 * S::kPRow : 0);
+        const int chunk0 = kWide ? 0 : wg * (kWords / 4);
 #pragma unroll
-          for (int c = 0; c < C; c += 8) {
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) split_bf16x2(s[c + 2 * i], s[c + 2 * i + 1], hi[i], lo[i]);
-            const uint32_t at = row_a + (((chunk0 + c / 8) ^ swz) << 4);
-            sts16(at, hi[0], hi[1], hi[2], hi[3]);
-            sts16(at + S::kPPart, lo[0], lo[1], lo[2], lo[3]);
-          }
-        } else {
-          const uint32_t row_a = p_a + t * S::kPRow;
-#pragma unroll
-          for (int c = 0; c < C; c += 16) {
-            uint32_t hi[8], lo[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) split_e4m3x2(s[(c + 2 * i) % C], s[(c + 2 * i + 1) % C], hi[i], lo[i]);
-            const uint32_t at = row_a + (((wg * (C / 16) + c / 16) ^ swz) << 4);
-            sts16(at, hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16), hi[4] | (hi[5] << 16), hi[6] | (hi[7] << 16));
-            sts16(at + S::kPPart, lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16), lo[4] | (lo[5] << 16),
-                  lo[6] | (lo[7] << 16));
-          }
+        for (int i = 0; i < kWords; i += 4) {
+          const uint32_t at = row_a + (((chunk0 + i / 4) ^ swz) << 4);
+          sts16(at, hi[i], hi[i + 1], hi[i + 2], hi[i + 3]);
+          sts16(at + S::kPPart, lo[i], lo[i + 1], lo[i + 2], lo[i + 3]);
         }
         fence_proxy_async_smem();
-        mbar_arrive(bar(kPFull));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kPFull));
       }
       if (leave) break;
       // ---- the segment's result
@@ -867,16 +893,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 #pragma unroll 1
       for (int c = 0; c < C; c += 8) {
         if (c0 + c >= p.group) break;
-        float o[8];
+        float o[8], o2[8];
         tmem_ld8(o_col + c, reinterpret_cast<uint32_t*>(o));
+        tmem_ld8(o_col + N + c, reinterpret_cast<uint32_t*>(o2));
         tmem_wait_ld();
         pin8(o);
+        pin8(o2);
         if (t < D) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int h = c0 + c + i;
             if (h < p.group) {
-              const float x = o[i] * alpha_s[h];
+              const float x = (o[i] + (kE4m3 ? o2[i] * (1.f / kLift) : o2[i])) * alpha_s[h];
               if (sg.slot < 0)
                 p.out[((static_cast<int64_t>(sg.row) * p.kv_heads + sg.kvh) * p.group + h) * D + t] =
                     __bfloat16_as_ushort(__float2bfloat16_rn(x));
