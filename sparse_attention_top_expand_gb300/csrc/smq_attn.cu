@@ -48,6 +48,7 @@ constexpr int kSegRing = 8;     // segments published ahead
 constexpr int kQScales = 8;
 constexpr int kSegReaders = 4 + 1 + 2 + 8;   // loader, MMA, address and softmax warps
 constexpr int kAddrReaders = 4 + 8;          // loader and softmax warps
+constexpr float kUnset = -3.0e38f;           // the running maximum of a partial without tokens
 constexpr int kSmemLimit = 232448 - 1024;  // less the static part
 
 // A run of tiles of one (row, kv head) item.
@@ -74,7 +75,7 @@ struct Shape {
   static constexpr int kPBytes = 2 * kPPart;                     // hi and lo of P
   static constexpr int kCols = N / 2;                            // heads per softmax thread
   static constexpr int kRingBytes = kAddrRing * 128 * (8 + (kE4m3 ? 8 : 0));
-  static constexpr int kMisc = kRingBytes + kAddrRing * 16 + kSegRing * 32 + 640 /*barriers*/ + N * 12 /*m, alpha, raise*/ +
+  static constexpr int kMisc = kRingBytes + kAddrRing * 16 + kSegRing * 32 + 640 /*barriers*/ + N * 16 /*m, alpha, raise, 1 / l*/ +
                                (kE4m3 ? kQScales * N * 4 : 0) + 8 * kCols * 4 /*scratch*/ + 64;
   static constexpr int kFixed = kQBufs * kQBytes + kPBytes + kMisc;
   static constexpr int kFit = (kSmemLimit - kFixed) / kUnit;
@@ -97,6 +98,31 @@ __device__ __forceinline__ float lg2(float x) {
   float y;
   asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Two fp32 operations at once: x = x * f + a, and x += y.
+__device__ __forceinline__ void fma2(float& x0, float& x1, float f0, float f1, float a0, float a1) {
+  asm("{\n .reg .b64 x, f, a;\n mov.b64 x, {%0, %1};\n mov.b64 f, {%2, %3};\n mov.b64 a, {%4, %5};\n"
+      " fma.rn.f32x2 x, x, f, a;\n mov.b64 {%0, %1}, x;\n}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(f0), "f"(f1), "f"(a0), "f"(a1));
+}
+__device__ __forceinline__ void add2(float& x0, float& x1, float y0, float y1) {
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(y0), "f"(y1));
+}
+
+// Wait for the phase of the given parity; false after limit_ns or once *abort is set. Every role's waits are
+// inlined in its loop, so this keeps to a few instructions.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const volatile int* abort, uint64_t limit_ns) {
+  uint64_t t0 = 0;
+  while (!mbar_try_wait_sleep(bar, parity, kWaitSleepNs)) {
+    const uint64_t now = global_ns();
+    if (t0 == 0) t0 = now;
+    if (*abort || now - t0 > limit_ns) return false;
+  }
+  return true;
 }
 
 // 16-byte asynchronous copy; `bytes` 0 fills with zeros and reads nothing.
@@ -127,19 +153,37 @@ __device__ __forceinline__ void sts16(uint32_t a, uint32_t x, uint32_t y, uint32
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* v) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-               : "r"(taddr)
-               : "memory");
+// kN consecutive columns of this thread's TMEM lane; valid after tmem_wait_ld, behind pin().
+template <int kN>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float* v) {
+  static_assert(kN == 8 || kN == 16 || kN == 32, "");
+  if (kN == 8)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                 : "r"(taddr)
+                 : "memory");
+  if (kN == 16)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+                 : "r"(taddr)
+                 : "memory");
+  if (kN == 32)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+                 : "r"(taddr)
+                 : "memory");
 }
 // Keeps uses of loaded registers behind the wait that makes them valid.
-__device__ __forceinline__ void pin8(float* v) {
-  asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]));
+template <int kN>
+__device__ __forceinline__ void pin(float* v) {
+#pragma unroll
+  for (int i = 0; i < kN; i += 8)
+    asm volatile("" : "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]), "+f"(v[i + 4]), "+f"(v[i + 5]), "+f"(v[i + 6]),
+                 "+f"(v[i + 7]));
 }
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
-               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "f"(v[0]),
+               "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
                : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -193,7 +237,9 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
 __device__ __forceinline__ void split_bf16x2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
   const uint32_t u0 = __float_as_uint(x0), u1 = __float_as_uint(x1);
   hi = __byte_perm(u0, u1, 0x7632);
-  lo = bf16x2(x0 - __uint_as_float(u0 & 0xffff0000u), x1 - __uint_as_float(u1 & 0xffff0000u));
+  float r0 = __uint_as_float(u0 & 0xffff0000u), r1 = __uint_as_float(u1 & 0xffff0000u);
+  fma2(r0, r1, -1.f, -1.f, x0, x1);
+  lo = bf16x2(r0, r1);
 }
 
 // x0, x1 as two E4M3 pairs, hi + lo / kLift: hi is x rounded, lo the rest times kLift rounded (9 bits together).
@@ -279,10 +325,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   float2* const ring_scale = reinterpret_cast<float2*>(ring_off + kAddrRing * 128);  // [ring][128], E4M3
   uint32_t* const ring_mask = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(ring_off) + S::kRingBytes);
   AttnSeg* const segs = reinterpret_cast<AttnSeg*>(ring_mask + kAddrRing * 4);
-  float* const m_s = reinterpret_cast<float*>(segs + kSegRing);  // [N] running maxima
-  float* const alpha_s = m_s + N;                                // [N] rescale factors, then 1 / l
+  float* const nm_s = reinterpret_cast<float*>(segs + kSegRing);  // [N] running maxima, negated
+  float* const alpha_s = nm_s + N;                               // [N] rescale factors
   float* const up_s = alpha_s + N;                               // [N] the last raise of each maximum
-  float* const qscale_s = up_s + N;                              // [kQScales][N], E4M3: 1 / the scale Q was stored with
+  float* const inv_s = up_s + N;                                 // [N] 1 / l of the segment being written
+  float* const qscale_s = inv_s + N;                             // [kQScales][N], E4M3: 1 / the scale Q was stored with
   float* const scratch = qscale_s + (kE4m3 ? kQScales * N : 0);                       // [2][4][C]
   uint64_t* const bars = reinterpret_cast<uint64_t*>(scratch + 8 * C);
   // barriers
@@ -328,6 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     abort_flag = 0;
     start_row = -1;
   }
+  if (tid < N) nm_s[tid] = 0.f;
   if (warp == 5) tmem_alloc(smem_addr(&tmem_slot), S::kTmem);
   griddep_wait();
 
@@ -378,33 +426,93 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   const uint32_t tmem = tmem_slot;
   const uint32_t tmem_o = tmem, tmem_sc = tmem + 2 * N;
   const volatile int* const abort = &abort_flag;
-  auto fail = [&] {
-    abort_flag = 1;
-    atomicOr(p.status, kStatusTimeout);
-  };
+  auto fail = [&] { *reinterpret_cast<volatile int*>(&abort_flag) = 1; };  // reported at the end
 
   // the softmax threads take registers that the others do not need: 256 x 72 + 256 x 184 = 512 x 128
   if (warp < 8) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   if (warp < 4) {
     // ------------------------------------------------------------ loaders
-    const int stall_unit = blockIdx.x != 0 || p.stall_tile < 0 ? -1 : p.stall_tile == 0 ? 0 : 2 * p.stall_tile - 1;
+    const int stall_tile = blockIdx.x == 0 ? p.stall_tile : -1;  // tests: its keys are not handed over
     constexpr int kChunks = S::kRow / 16;         // 16-byte pieces of a token
     constexpr int kTok = 32 / kChunks;            // tokens per warp instruction
     const int piece = lane % kChunks, sub = lane / kChunks;
     const uint32_t units_a = smem_addr(units);
-    int unit = 0;
     bool ok = true;
     auto wait = [&](int b, uint32_t parity) {
-      ok = ok && warp_wait(bar(b), parity, abort, limit);
-      if (!ok && lane == 0) fail();
+      ok = __all_sync(0xffffffffu, wait_phase(bar(b), parity, abort, limit));
+      return ok;
     };
-    // The barrier counts each thread's copies when they land; the MMA thread's proxy fence, after its wait,
-    // orders them before the tensor core's reads.
-    auto copy_unit = [&](const uint8_t* base, int tile) {
-      const int slot = unit % S::kSlots;
-      if (unit >= S::kSlots) wait(kEmpty + slot, (unit / S::kSlots - 1) & 1);
-      if (!ok) return;
+    // Units in the order of their use: K 0, K 1, V 0, K 2, V 1, ... The unit's barrier counts each thread's copies
+    // when they land; the MMA warp's proxy fence, after its wait, orders them before the tensor core's reads.
+    int slot = 0, seg = 0, left = 0, keys = 0;  // left: tiles of this segment; keys: K tiles so far
+    uint32_t turn = 1;                                    // parity that says that the slot is free
+    bool values = false, last = false;
+    while (ok) {
+      if (!values) {
+        if (left == 0) {
+          if (!wait(kSegFull + seg % kSegRing, (seg / kSegRing) & 1)) break;
+          const AttnSeg sg = segs[seg % kSegRing];
+          left = sg.ntiles;
+          last = left == 0;
+          if (last && keys == 0) break;
+          if (!last) {
+          // the segment's queries: in bf16 its first K tile's barrier covers them, split in E4M3 they have one
+          const int qb = seg % S::kQBufs;
+          if (!wait(kQEmpty + qb, (seg / S::kQBufs + 1) & 1)) break;
+          const uint16_t* qrow = p.q + sg.row * p.q_stride + static_cast<int64_t>(sg.kvh) * p.group * D;
+          uint8_t* const qdst = q_s + qb * S::kQBytes;
+          if (!kE4m3) {
+            constexpr int kQChunks = D * 2 / 16, kQTok = 32 / kQChunks;
+            const int c = lane % kQChunks;
+            for (int i = warp * kQTok + lane / kQChunks; i < N; i += 4 * kQTok)
+              cp16(smem_addr(qdst) + (c >> 3) * (N * 128) + i * 128 + (((c & 7) ^ (i & 7)) << 4),
+                   qrow + (i < p.group ? i * D + c * 8 : 0), i < p.group ? 16 : 0);
+          } else {
+            // a head per D / 8 lanes; each stored as hi + lo times a power of two that brings its amax to (224, 448]
+            constexpr int kL = D / 8;
+            const int c = lane % kL;
+            for (int i0 = warp * (32 / kL); i0 < N; i0 += 4 * (32 / kL)) {
+              const int i = i0 + lane / kL;
+              uint4 w = make_uint4(0, 0, 0, 0);
+              if (i < p.group) w = *reinterpret_cast<const uint4*>(qrow + i * D + c * 8);
+              const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+              float x[8], amax = 0.f;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                x[2 * k] = __uint_as_float(ws[k] << 16);
+                x[2 * k + 1] = __uint_as_float(ws[k] & 0xffff0000u);
+                amax = fmaxf(amax, fmaxf(fabsf(x[2 * k]), fabsf(x[2 * k + 1])));
+              }
+#pragma unroll
+              for (int o = kL / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+              // amax = f * 2^e with f in [1, 2): the factor 2^(7 - e), or 2^(8 - e) where f <= 1.75
+              const uint32_t bits = __float_as_uint(amax);
+              int e = static_cast<int>(bits >> 23) - 127;
+              e = e < -100 ? -100 : e;
+              const int up = 7 - e + ((bits & 0x7fffffu) <= 0x600000u ? 1 : 0);
+              const float mul = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
+              uint32_t hi[4], lo[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) split_e4m3x2<false>(x[2 * k] * mul, x[2 * k + 1] * mul, hi[k], lo[k]);
+              uint8_t* dst = qdst + i * 128 + (((c >> 1) ^ (i & 7)) << 4) + (c & 1) * 8;
+              *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+              *reinterpret_cast<uint2*>(dst + S::kQPart) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+              if (c == 0) qscale_s[(seg % kQScales) * N + i] = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+            }
+            mbar_arrive(bar(kQFull + qb));
+          }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kSegEmpty + seg % kSegRing));
+            ++seg;
+          }
+        }
+        if (!last && !wait(kAFull + keys % kAddrRing, (keys / kAddrRing) & 1)) break;
+      }
+      const bool v = values || last;
+      const int tile = values ? keys - 2 : last ? keys - 1 : keys;
+      if (!wait(kEmpty + slot, turn)) break;
+      const uint8_t* const base = static_cast<const uint8_t*>(v ? p.v_cache : p.k_cache) + piece * 16;
       const uint32_t dst0 = units_a + slot * S::kUnit + (piece >> 3) * 16384;
       const int64_t* const offs = ring_off + tile % kAddrRing * 128 + warp * 32 + sub;
       constexpr int kBatch = 32 / kTok < 8 ? 32 / kTok : 8;  // addresses first, so that the copies issue back to back
@@ -416,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         for (int i = 0; i < kBatch; ++i) {
           const int64_t o = offs[(i0 + i) * kTok];
           bytes[i] = o < 0 ? 0 : 16;
-          src[i] = base + piece * 16 + (o < 0 ? 0 : o);
+          src[i] = base + (o < 0 ? 0 : o);
         }
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
@@ -424,78 +532,22 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           cp16(dst0 + tok * 128 + (((piece & 7) ^ (tok & 7)) << 4), src[i], bytes[i]);
         }
       }
-      // unit 2 t - 1 (0 for t = 0) is the K tile t: the stall test withholds it
-      if (stall_unit < 0 || unit != stall_unit) cp_arrive(bar(kFull + slot));
-      ++unit;
-    };
-    auto copy_values = [&](int tile) {
-      copy_unit(static_cast<const uint8_t*>(p.v_cache), tile);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kAEmpty + tile % kAddrRing));
-    };
-    int it = 0;
-    for (int seg = 0; ok; ++seg) {
-      wait(kSegFull + seg % kSegRing, (seg / kSegRing) & 1);
-      if (!ok) break;
-      const AttnSeg sg = segs[seg % kSegRing];
-      if (sg.ntiles == 0) break;
-      // the segment's queries: in bf16 its first K tile's barrier covers them, split in E4M3 they have one
-      const int qb = seg % S::kQBufs;
-      if (seg >= S::kQBufs) wait(kQEmpty + qb, (seg / S::kQBufs - 1) & 1);
-      if (!ok) break;
-      const uint16_t* qrow = p.q + sg.row * p.q_stride + static_cast<int64_t>(sg.kvh) * p.group * D;
-      uint8_t* const qdst = q_s + qb * S::kQBytes;
-      if (!kE4m3) {
-        constexpr int kQChunks = D * 2 / 16, kQTok = 32 / kQChunks;
-        const int c = lane % kQChunks;
-        for (int i = warp * kQTok + lane / kQChunks; i < N; i += 4 * kQTok)
-          cp16(smem_addr(qdst) + (c >> 3) * (N * 128) + i * 128 + (((c & 7) ^ (i & 7)) << 4),
-               qrow + (i < p.group ? i * D + c * 8 : 0), i < p.group ? 16 : 0);
+      if (v || stall_tile != tile) cp_arrive(bar(kFull + slot));
+      if (++slot == S::kSlots) {
+        slot = 0;
+        turn ^= 1;
+      }
+      if (v) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kAEmpty + tile % kAddrRing));
+        if (last) break;
+        values = false;
       } else {
-        // a head per D / 8 lanes; each stored as hi + lo times a power of two that brings its amax to (224, 448]
-        constexpr int kL = D / 8;
-        const int c = lane % kL;
-        for (int i0 = warp * (32 / kL); i0 < N; i0 += 4 * (32 / kL)) {
-          const int i = i0 + lane / kL;
-          uint4 w = make_uint4(0, 0, 0, 0);
-          if (i < p.group) w = *reinterpret_cast<const uint4*>(qrow + i * D + c * 8);
-          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-          float x[8], amax = 0.f;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            x[2 * k] = __uint_as_float(ws[k] << 16);
-            x[2 * k + 1] = __uint_as_float(ws[k] & 0xffff0000u);
-            amax = fmaxf(amax, fmaxf(fabsf(x[2 * k]), fabsf(x[2 * k + 1])));
-          }
-#pragma unroll
-          for (int o = kL / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-          // amax = f * 2^e with f in [1, 2): the factor 2^(7 - e), or 2^(8 - e) where f <= 1.75
-          const uint32_t bits = __float_as_uint(amax);
-          int e = static_cast<int>(bits >> 23) - 127;
-          e = e < -100 ? -100 : e;
-          const int up = 7 - e + ((bits & 0x7fffffu) <= 0x600000u ? 1 : 0);
-          const float mul = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) split_e4m3x2<false>(x[2 * k] * mul, x[2 * k + 1] * mul, hi[k], lo[k]);
-          uint8_t* dst = qdst + i * 128 + (((c >> 1) ^ (i & 7)) << 4) + (c & 1) * 8;
-          *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-          *reinterpret_cast<uint2*>(dst + S::kQPart) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
-          if (c == 0) qscale_s[(seg % kQScales) * N + i] = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
-        }
-        mbar_arrive(bar(kQFull + qb));
+        --left;
+        values = ++keys > 1;
       }
-      for (int j = 0; j < sg.ntiles && ok; ++j, ++it) {
-        const int a = it % kAddrRing;
-        wait(kAFull + a, (it / kAddrRing) & 1);
-        if (!ok) break;
-        copy_unit(static_cast<const uint8_t*>(p.k_cache), it);
-        if (it > 0) copy_values(it - 1);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kSegEmpty + seg % kSegRing));
     }
-    if (ok && it > 0) copy_values(it - 1);
+    if (!ok && lane == 0) fail();
     cp_wait_all();
   } else if (warp == 4) {
     // ---------------------------------------------------------- scheduler
@@ -532,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           idx = 0;
         }
       }
-      if (seg >= kSegRing) ok = warp_wait(bar(kSegEmpty + seg % kSegRing), (seg / kSegRing - 1) & 1, abort, limit);
+      if (seg >= kSegRing) ok = __all_sync(0xffffffffu, wait_phase(bar(kSegEmpty + seg % kSegRing), (seg / kSegRing - 1) & 1, abort, limit));
       if (!ok) break;
       if (lane == 0) {
         segs[seg % kSegRing] = sg;
@@ -556,46 +608,31 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     const uint32_t q_lo = desc_lo(smem_addr(q_s), 16), p_lo = desc_lo(smem_addr(p_s), 128 * S::kPRow);
     bool ok = true;
     auto wait = [&](int b, uint32_t parity) {
-      ok = ok && mbar_wait(bar(b), parity, abort, limit);
-      ok = __all_sync(0xffffffffu, ok);
+      ok = __all_sync(0xffffffffu, wait_phase(bar(b), parity, abort, limit));
       return ok;
     };
-    int slot = 0, it = 0;
+    int slot = 0, it = 0, seg = -1, left = 0;
     uint32_t turn = 0;  // parity of the units' barriers
-    auto next_slot = [&] {
-      if (++slot == S::kSlots) {
-        slot = 0;
-        turn ^= 1;
+    bool first = false, last = false;
+    while (!last) {
+      const bool fresh = first;  // tile it - 1 begins its segment
+      if (left == 0) {
+        ++seg;
+        if (!wait(kSegFull + seg % kSegRing, (seg / kSegRing) & 1)) break;
+        left = segs[seg % kSegRing].ntiles;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kSegEmpty + seg % kSegRing));
+        first = true;
+        last = left == 0;
+      } else {
+        first = false;
       }
-    };
-    bool prev_first = false;
-    auto pv = [&](int t, bool fresh) {
-      if (!wait(kFull + slot, turn) || !wait(kPFull, t & 1)) return;
-      fence_proxy_async_smem();
-      tc_fence_after();
-      const uint32_t a = v_lo + slot * (S::kUnit >> 4);
-      if (elect_one()) {
-#pragma unroll
-        for (int k = 0; k < kPvSteps; ++k)
-          mma<kE4m3>(tmem_o, a + k * ((kE4m3 ? 4096 : 2048) >> 4), kRowHi, p_lo + ((k * (kE4m3 ? 32 : 16) * S::kPRow) >> 4),
-                     kPHi, kPvDesc, k > 0 || !fresh);
-        mma_commit(bar(kEmpty + slot));
-        mma_commit(bar(kPvDone));
-      }
-      __syncwarp();
-      next_slot();
-    };
-    for (int seg = 0; ok; ++seg) {
-      if (!wait(kSegFull + seg % kSegRing, (seg / kSegRing) & 1)) break;
-      const int n = segs[seg % kSegRing].ntiles;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kSegEmpty + seg % kSegRing));
-      if (n == 0) break;
-      const int qb = seg % S::kQBufs;
-      for (int j = 0; j < n; ++j, ++it) {
+      if (!last) {
+        // S of tile it
+        const int qb = seg % S::kQBufs;
         if (!wait(kFull + slot, turn)) break;
-        if (kE4m3 && j == 0 && !wait(kQFull + qb, (seg / S::kQBufs) & 1)) break;
-        if (it >= 2 && !wait(kSEmpty + (it & 1), ((it >> 1) - 1) & 1)) break;
+        if (kE4m3 && first && !wait(kQFull + qb, (seg / S::kQBufs) & 1)) break;
+        if (!wait(kSEmpty + (it & 1), ((it >> 1) + 1) & 1)) break;
         fence_proxy_async_smem();
         tc_fence_after();
         const uint32_t a = k_lo + slot * (S::kUnit >> 4), q = q_lo + qb * (S::kQBytes >> 4);
@@ -609,22 +646,43 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                          part + k > 0);
           mma_commit(bar(kEmpty + slot));
           mma_commit(bar(kSFull + (it & 1)));
-          if (j == n - 1) mma_commit(bar(kQEmpty + qb));
+          if (left == 1) mma_commit(bar(kQEmpty + qb));
         }
         __syncwarp();
-        next_slot();
-        if (it > 0) pv(it - 1, prev_first);
-        if (!ok) break;
-        prev_first = j == 0;
+        if (++slot == S::kSlots) {
+          slot = 0;
+          turn ^= 1;
+        }
+        --left;
       }
+      if (it > 0) {
+        // O of tile it - 1
+        if (!wait(kFull + slot, turn) || !wait(kPFull, (it - 1) & 1)) break;
+        fence_proxy_async_smem();
+        tc_fence_after();
+        const uint32_t a = v_lo + slot * (S::kUnit >> 4);
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < kPvSteps; ++k)
+            mma<kE4m3>(tmem_o, a + k * ((kE4m3 ? 4096 : 2048) >> 4), kRowHi, p_lo + ((k * (kE4m3 ? 32 : 16) * S::kPRow) >> 4),
+                       kPHi, kPvDesc, k > 0 || !fresh);
+          mma_commit(bar(kEmpty + slot));
+          mma_commit(bar(kPvDone));
+        }
+        __syncwarp();
+        if (++slot == S::kSlots) {
+          slot = 0;
+          turn ^= 1;
+        }
+      }
+      ++it;
     }
-    if (ok && it > 0) pv(it - 1, prev_first);
     if (!ok) {
       if (lane == 0) fail();
       // let the MMAs issued so far finish before TMEM is freed
       if (elect_one()) mma_commit(bar(kDrain));
       const int never = 0;
-      mbar_wait(bar(kDrain), 0, &never, limit);
+      wait_phase(bar(kDrain), 0, &never, limit);
     }
     __syncwarp();
   } else {
@@ -632,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     int it = 0;
     bool ok = true;
     for (int seg = 0; ok; ++seg) {
-      ok = warp_wait(bar(kSegFull + seg % kSegRing), (seg / kSegRing) & 1, abort, limit);
+      ok = __all_sync(0xffffffffu, wait_phase(bar(kSegFull + seg % kSegRing), (seg / kSegRing) & 1, abort, limit));
       if (!ok) break;
       const AttnSeg sg = segs[seg % kSegRing];
       __syncwarp();
@@ -644,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       for (int j = 0; j < sg.ntiles; ++j, ++it) {
         if ((it & 1) != (warp & 1)) continue;
         const int a = it % kAddrRing;
-        if (it >= kAddrRing) ok = warp_wait(bar(kAEmpty + a), (it / kAddrRing - 1) & 1, abort, limit);
+        ok = __all_sync(0xffffffffu, wait_phase(bar(kAEmpty + a), (it / kAddrRing + 1) & 1, abort, limit));
         if (!ok) break;
         int32_t pos[4], page[4];
         bool bad = false;
@@ -712,22 +770,63 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     bool failed = false, leave = false;
     int it = 0;
     auto wait = [&](int b, uint32_t parity) {
-      if (!failed && !mbar_wait(bar(b), parity, abort, limit)) {
-        failed = true;
-        fail();
+      if (!failed) failed = !wait_phase(bar(b), parity, abort, limit);
+    };
+    // Write the result of segment w, whose O is final: normalised by inv_s, or as a partial.
+    auto write_out = [&](const AttnSeg& w) {
+      tc_fence_after();
+      constexpr int kStep = C == 16 || C == 32 ? 16 : 8;
+#pragma unroll
+      for (int c = 0; c < C; c += kStep) {
+        if (c0 + c >= p.group) break;
+        float o[kStep], o2[kStep];
+        tmem_ld<kStep>(o_col + c, o);
+        tmem_ld<kStep>(o_col + N + c, o2);
+        tmem_wait_ld();
+        pin<kStep>(o);
+        pin<kStep>(o2);
+        if (t >= D) continue;  // whole warps
+        if (w.slot >= 0) {
+          float* const dst = p.part_o + (static_cast<int64_t>(w.slot) * p.group + c0 + c) * D + t;
+#pragma unroll
+          for (int i = 0; i < kStep; ++i)
+            if (c0 + c + i < p.group) dst[i * D] = o[i] + (kE4m3 ? o2[i] * (1.f / kLift) : o2[i]);
+        } else {
+          // lanes 2 i and 2 i + 1 exchange, so that each writes two elements of every other head
+          uint16_t* const dst = p.out +
+                                ((static_cast<int64_t>(w.row) * p.kv_heads + w.kvh) * p.group + c0 + c + (lane & 1)) * D +
+                                (t & ~1);
+#pragma unroll
+          for (int i = 0; i < kStep; i += 2) {
+            const float x = (o[i] + (kE4m3 ? o2[i] * (1.f / kLift) : o2[i])) * inv_s[c0 + c + i];
+            const float y = (o[i + 1] + (kE4m3 ? o2[i + 1] * (1.f / kLift) : o2[i + 1])) * inv_s[c0 + c + i + 1];
+            const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? x : y, 1);
+            if (c0 + c + i + (lane & 1) < p.group)
+              *reinterpret_cast<uint32_t*>(dst + i * D) = lane & 1 ? bf16x2(got, y) : bf16x2(x, got);
+          }
+        }
       }
+      tc_fence_before();
     };
     float l[C];
+    AttnSeg done;  // the segment whose O is still to be written: behind the next one's first tile
+    done.ntiles = 0;
     for (int seg = 0;; ++seg) {
       wait(kSegFull + seg % kSegRing, (seg / kSegRing) & 1);
       // a group leaves together: a failed wait anywhere in it ends all of it
       if (bar_or(bar_id, 128, failed)) break;
       const AttnSeg sg = segs[seg % kSegRing];
-      if (sg.ntiles == 0) break;
-      if (wt < C) m_s[c0 + wt] = 0.f;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kSegEmpty + seg % kSegRing));
+      if (sg.ntiles == 0) {
+        if (done.ntiles > 0) {
+          wait(kPvDone, (it - 1) & 1);
+          if (!failed) write_out(done);
+        }
+        break;
+      }
 #pragma unroll
       for (int c = 0; c < C; ++c) l[c] = 0.f;
-      bar_sync(bar_id, 128);
       const float* const qscale = qscale_s + (seg % kQScales) * N + c0;
       bool fresh = true;  // no token so far
       for (int j = 0; j < sg.ntiles; ++j, ++it) {
@@ -740,8 +839,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         if (!failed) {
           tc_fence_after();
           const uint32_t s_col = tmem_sc + lanes + (it & 1) * N + c0;
+          constexpr int kLd = C > 32 ? 32 : C;
 #pragma unroll
-          for (int c = 0; c < C; c += 8) tmem_ld8(s_col + c, reinterpret_cast<uint32_t*>(&s[c]));
+          for (int c = 0; c < C; c += kLd) tmem_ld<kLd>(s_col + c, s + c);
           float mul = p.scale_log2, add = 0.f;
           const uint4 mask = *reinterpret_cast<const uint4*>(ring_mask + a * 4);
           const bool valid = ((quarter == 0 ? mask.x : quarter == 1 ? mask.y : quarter == 2 ? mask.z : mask.w) >> lane) & 1;
@@ -750,11 +850,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             const float2 sc = ring_scale[a * 128 + t];
             mul *= sc.x;
             add = lg2(sc.y);
-            inv_vs = 1.f / sc.y;
+            inv_vs = __fdividef(1.f, sc.y);
           }
           tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < C; c += 8) pin8(&s[c]);
+          pin<C>(s);
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
@@ -764,16 +863,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           float most = -INFINITY;
 #pragma unroll
           for (int c = 0; c < C; c += 4) {
-            const float4 m4 = *reinterpret_cast<const float4*>(m_s + c0 + c);
-            float4 f4 = make_float4(mul, mul, mul, mul);
+            float4 a4 = *reinterpret_cast<const float4*>(nm_s + c0 + c), f4 = make_float4(mul, mul, mul, mul);
             if (kE4m3) {
               const float4 q4 = *reinterpret_cast<const float4*>(qscale + c);
-              f4.x *= q4.x, f4.y *= q4.y, f4.z *= q4.z, f4.w *= q4.w;
+              f4 = make_float4(mul * q4.x, mul * q4.y, mul * q4.z, mul * q4.w);
+              add2(a4.x, a4.y, add, add);
+              add2(a4.z, a4.w, add, add);
             }
-            s[c] = fmaf(s[c], f4.x, add - m4.x);
-            s[c + 1] = fmaf(s[c + 1], f4.y, add - m4.y);
-            s[c + 2] = fmaf(s[c + 2], f4.z, add - m4.z);
-            s[c + 3] = fmaf(s[c + 3], f4.w, add - m4.w);
+            fma2(s[c], s[c + 1], f4.x, f4.y, a4.x, a4.y);
+            fma2(s[c + 2], s[c + 3], f4.z, f4.w, a4.z, a4.w);
             most = fmaxf(fmaxf(most, fmaxf(s[c], s[c + 1])), fmaxf(s[c + 2], s[c + 3]));
           }
           if (!valid) {
@@ -784,7 +882,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           over = most > S::kTau || first;
         }
         const bool raise = bar_or(bar_id, 128, over);
-        if (raise) {
+        if (__builtin_expect(raise, 0)) {
           // raise this group's maxima to the tile's, or set them at the row's first tokens
           constexpr int kHalf = C > 32 ? 32 : C;
 #pragma unroll
@@ -802,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           if (wt < C) {
             const float top = fmaxf(fmaxf(red[wt], red[C + wt]), fmaxf(red[2 * C + wt], red[3 * C + wt])) - S::kTop;
             const float up = top == -INFINITY ? 0.f : first ? top : fmaxf(top, 0.f);
-            m_s[c0 + wt] += up;
+            nm_s[c0 + wt] -= up;
             up_s[c0 + wt] = up;
             alpha_s[c0 + wt] = first ? 0.f : ex2(-up);
           }
@@ -820,23 +918,27 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         constexpr int kWords = kE4m3 ? C / 4 : C / 2;
         uint32_t hi[kWords], lo[kWords];
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-          s[c] = ex2(s[c]);
-          l[c] = kE4m3 ? fmaf(s[c], inv_vs, l[c]) : l[c] + s[c];
-        }
+        for (int c = 0; c < C; ++c) s[c] = ex2(s[c]);
 #pragma unroll
         for (int i = 0; i < kWords; ++i) {
           if (kE4m3) {
             uint32_t h0, h1, l0, l1;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) l[(4 * i + k) % C] = fmaf(s[(4 * i + k) % C], inv_vs, l[(4 * i + k) % C]);
             split_e4m3x2<true>(s[(4 * i) % C], s[(4 * i + 1) % C], h0, l0);
             split_e4m3x2<true>(s[(4 * i + 2) % C], s[(4 * i + 3) % C], h1, l1);
             hi[i] = h0 | (h1 << 16);
             lo[i] = l0 | (l1 << 16);
           } else {
+            add2(l[(2 * i) % C], l[(2 * i + 1) % C], s[(2 * i) % C], s[(2 * i + 1) % C]);
             split_bf16x2(s[(2 * i) % C], s[(2 * i + 1) % C], hi[i], lo[i]);
           }
         }
+        // computed here, not behind the wait, where the compiler would move it
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) asm volatile("" : "+r"(hi[i]), "+r"(lo[i]));
         if (it > 0) wait(kPvDone, (it - 1) & 1);  // O is final up to the previous tile, and P is free
+        if (j == 0 && done.ntiles > 0) write_out(done);
         if (raise && j > 0) {
           tc_fence_after();
 #pragma unroll
@@ -844,12 +946,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 #pragma unroll
             for (int c = 0; c < C; c += 8) {
               float o[8];
-              tmem_ld8(o_col + part * N + c, reinterpret_cast<uint32_t*>(o));
+              tmem_ld<8>(o_col + part * N + c, o);
               tmem_wait_ld();
-              pin8(o);
+              pin<8>(o);
 #pragma unroll
               for (int i = 0; i < 8; ++i) o[i] *= alpha_s[c0 + c + i];
-              tmem_st8(o_col + part * N + c, reinterpret_cast<uint32_t*>(o));
+              tmem_st8(o_col + part * N + c, o);
             }
           tmem_wait_st();
           tc_fence_before();
@@ -869,59 +971,33 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         if (lane == 0) mbar_arrive(bar(kPFull));
       }
       if (leave) break;
-      // ---- the segment's result
-      wait(kPvDone, (it - 1) & 1);
-      const int first = reduce_columns<C, false>(l);
+      // ---- the segment's sums; its O follows behind the next tile's scores
+      const int col = reduce_columns<C, false>(l);
 #pragma unroll
-      for (int i = 0; i < (C > 32 ? C / 32 : 1); ++i) red[quarter * C + first + i] = l[i];
+      for (int i = 0; i < (C > 32 ? C / 32 : 1); ++i) red[quarter * C + col + i] = l[i];
       bar_sync(bar_id, 128);
-      if (wt < C && c0 + wt < p.group) {
+      if (wt < C) {
         const int h = c0 + wt;
         const float sum = red[wt] + red[C + wt] + red[2 * C + wt] + red[3 * C + wt];
-        if (sg.slot < 0) {
-          alpha_s[h] = sum == 0.f ? 0.f : 1.f / sum;
-          if (p.lse)
+        const float m = fresh ? kUnset : -nm_s[h];
+        nm_s[h] = 0.f;
+        inv_s[h] = sum == 0.f ? 0.f : 1.f / sum;
+        if (h < p.group) {
+          if (sg.slot >= 0)
+            p.part_ml[static_cast<int64_t>(sg.slot) * p.group + h] = make_float2(m, sum);
+          else if (p.lse)
             p.lse[static_cast<int64_t>(sg.row) * p.kv_heads * p.group + sg.kvh * p.group + h] =
-                (m_s[h] + log2f(sum)) * 0.69314718055994531f;
-        } else {
-          alpha_s[h] = 1.f;
-          p.part_ml[static_cast<int64_t>(sg.slot) * p.group + h] = make_float2(m_s[h], sum);
+                (m + log2f(sum)) * 0.69314718055994531f;
         }
       }
-      bar_sync(bar_id, 128);
-      tc_fence_after();
-#pragma unroll 1
-      for (int c = 0; c < C; c += 8) {
-        if (c0 + c >= p.group) break;
-        float o[8], o2[8];
-        tmem_ld8(o_col + c, reinterpret_cast<uint32_t*>(o));
-        tmem_ld8(o_col + N + c, reinterpret_cast<uint32_t*>(o2));
-        tmem_wait_ld();
-        pin8(o);
-        pin8(o2);
-        if (t < D) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int h = c0 + c + i;
-            if (h < p.group) {
-              const float x = (o[i] + (kE4m3 ? o2[i] * (1.f / kLift) : o2[i])) * alpha_s[h];
-              if (sg.slot < 0)
-                p.out[((static_cast<int64_t>(sg.row) * p.kv_heads + sg.kvh) * p.group + h) * D + t] =
-                    __bfloat16_as_ushort(__float2bfloat16_rn(x));
-              else
-                p.part_o[(static_cast<int64_t>(sg.slot) * p.group + h) * D + t] = x;
-            }
-          }
-        }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kSegEmpty + seg % kSegRing));
+      done = sg;
     }
+    if (failed) fail();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (tid == 0 && abort_flag) atomicOr(p.status, kStatusTimeout);
   if (warp == 5) tmem_dealloc(tmem, S::kTmem);
 }
 
