@@ -26,8 +26,8 @@
 // P / value scale.
 //
 // Roles (512 threads): warps 0-3 copy K, V and Q tiles (cp.async), warp 4
-// schedules segments, warp 5 issues MMAs, warps 6-7 look up addresses, warps
-// 8-15 are two softmax groups of 128 threads, each with half of the heads.
+// schedules segments, warps 5 and 7 issue the MMAs, warp 6 looks up addresses,
+// warps 8-15 are two softmax groups of 128 threads, each with half of the heads.
 #include "smq_attn.cuh"
 #include "smq_kernels.cuh"
 #include "smq_ptx.cuh"
@@ -46,7 +46,7 @@ constexpr int kSegRing = 8;     // segments published ahead
 // Query scales of E4M3 segments: the loader is at most four segments ahead of the softmax (its
 // buffers free with the MMA, the MMA runs up to two tiles ahead), so eight sets never collide.
 constexpr int kQScales = 8;
-constexpr int kSegReaders = 4 + 1 + 2 + 8;   // loader, MMA, address and softmax warps
+constexpr int kSegReaders = 4 + 2 + 1 + 8;   // loader, MMA, address and softmax warps
 constexpr int kAddrReaders = 4 + 8;          // loader and softmax warps
 constexpr float kUnset = -3.0e38f;           // the running maximum of a partial without tokens
 constexpr int kSmemLimit = 232448 - 1024;  // less the static part
@@ -130,6 +130,10 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src, uint32_t byt
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// 4-byte asynchronous copy.
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
 // Arrive on an mbarrier, as one of its expected arrivals, once this thread's copies so far have landed.
 __device__ __forceinline__ void cp_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
@@ -335,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   // barriers
   constexpr int kFull = 0, kEmpty = kFull + S::kSlots, kSFull = kEmpty + S::kSlots, kSEmpty = kSFull + 2, kPFull = kSEmpty + 2,
                 kPvDone = kPFull + 1, kQEmpty = kPvDone + 1, kQFull = kQEmpty + 2, kSegFull = kQFull + 2, kSegEmpty = kSegFull + kSegRing,
-                kAFull = kSegEmpty + kSegRing, kAEmpty = kAFull + kAddrRing, kDrain = kAEmpty + kAddrRing, kBars = kDrain + 1;
+                kAFull = kSegEmpty + kSegRing, kAEmpty = kAFull + kAddrRing, kDrain = kAEmpty + kAddrRing, kScFull = kDrain + 2, kBars = kScFull + (kE4m3 ? kAddrRing : 0);
   static_assert(kBars * 8 <= 640, "");
   auto bar = [&](int i) { return smem_addr(bars + i); };
 
@@ -369,8 +373,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     for (int i = 0; i < kAddrRing; ++i) {
       mbar_init(bar(kAFull + i), 1);
       mbar_init(bar(kAEmpty + i), kAddrReaders);
+      if (kE4m3) mbar_init(bar(kScFull + i), 64);  // each lane's copies, and its stores
     }
     mbar_init(bar(kDrain), 1);
+    mbar_init(bar(kDrain + 1), 1);
     mbar_init_fence();
     abort_flag = 0;
     start_row = -1;
@@ -443,20 +449,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       ok = __all_sync(0xffffffffu, wait_phase(bar(b), parity, abort, limit));
       return ok;
     };
-    // Units in the order of their use: K 0, K 1, V 0, K 2, V 1, ... The unit's barrier counts each thread's copies
-    // when they land; the MMA warp's proxy fence, after its wait, orders them before the tensor core's reads.
-    int slot = 0, seg = 0, left = 0, keys = 0;  // left: tiles of this segment; keys: K tiles so far
-    uint32_t turn = 1;                                    // parity that says that the slot is free
-    bool values = false, last = false;
-    while (ok) {
+    // Units: K 0, V 0, K 1, V 1, ... The unit's barrier counts each thread's copies when they land; the MMA warps'
+    // proxy fence, after their wait, orders them before the tensor core's reads.
+    int slot = 0, seg = 0, left = 0, tile = 0;  // left: tiles of this segment
+    uint32_t turn = 1;                          // parity that says that the slot is free
+    for (bool values = false; ok; values = !values) {
       if (!values) {
         if (left == 0) {
           if (!wait(kSegFull + seg % kSegRing, (seg / kSegRing) & 1)) break;
           const AttnSeg sg = segs[seg % kSegRing];
           left = sg.ntiles;
-          last = left == 0;
-          if (last && keys == 0) break;
-          if (!last) {
+          if (left == 0) break;
           // the segment's queries: in bf16 its first K tile's barrier covers them, split in E4M3 they have one
           const int qb = seg % S::kQBufs;
           if (!wait(kQEmpty + qb, (seg / S::kQBufs + 1) & 1)) break;
@@ -502,17 +505,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             }
             mbar_arrive(bar(kQFull + qb));
           }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kSegEmpty + seg % kSegRing));
-            ++seg;
-          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kSegEmpty + seg % kSegRing));
+          ++seg;
         }
-        if (!last && !wait(kAFull + keys % kAddrRing, (keys / kAddrRing) & 1)) break;
+        if (!wait(kAFull + tile % kAddrRing, (tile / kAddrRing) & 1)) break;
       }
-      const bool v = values || last;
-      const int tile = values ? keys - 2 : last ? keys - 1 : keys;
       if (!wait(kEmpty + slot, turn)) break;
-      const uint8_t* const base = static_cast<const uint8_t*>(v ? p.v_cache : p.k_cache) + piece * 16;
+      const uint8_t* const base = static_cast<const uint8_t*>(values ? p.v_cache : p.k_cache) + piece * 16;
       const uint32_t dst0 = units_a + slot * S::kUnit + (piece >> 3) * 16384;
       const int64_t* const offs = ring_off + tile % kAddrRing * 128 + warp * 32 + sub;
       constexpr int kBatch = 32 / kTok < 8 ? 32 / kTok : 8;  // addresses first, so that the copies issue back to back
@@ -532,19 +532,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           cp16(dst0 + tok * 128 + (((piece & 7) ^ (tok & 7)) << 4), src[i], bytes[i]);
         }
       }
-      if (v || stall_tile != tile) cp_arrive(bar(kFull + slot));
+      if (values || stall_tile != tile) cp_arrive(bar(kFull + slot));
       if (++slot == S::kSlots) {
         slot = 0;
         turn ^= 1;
       }
-      if (v) {
+      if (values) {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kAEmpty + tile % kAddrRing));
-        if (last) break;
-        values = false;
-      } else {
+        ++tile;
         --left;
-        values = ++keys > 1;
       }
     }
     if (!ok && lane == 0) fail();
@@ -597,164 +594,174 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       if (!ok) fail();
       p.seg_info[blockIdx.x] = info;
     }
-  } else if (warp == 5) {
+  } else if (warp != 6) {
     // ---------------------------------------------------------------- MMA
-    // The whole warp runs this loop, so that descriptors stay in uniform registers, and one elected thread issues.
-    constexpr uint32_t kQkDesc = mma_idesc(kE4m3, false, N), kPvDesc = mma_idesc(kE4m3, true, 2 * N);
-    constexpr int kQkSteps = S::kRow / 32;   // 32 bytes of K per MMA
-    constexpr int kPvSteps = kE4m3 ? 4 : 8;  // 128 tokens, 32 or 16 per MMA
-    constexpr uint32_t kRowHi = desc_hi(128), kPHi = desc_hi(S::kPRow);
-    const uint32_t k_lo = desc_lo(smem_addr(units), 16), v_lo = desc_lo(smem_addr(units), 16384);
-    const uint32_t q_lo = desc_lo(smem_addr(q_s), 16), p_lo = desc_lo(smem_addr(p_s), 128 * S::kPRow);
+    // Warp 5 issues S = K Q^T, warp 7 O += V^T P: apart, so that S runs ahead of the softmax. The whole warp runs
+    // the loop, so that descriptors stay in uniform registers, and one elected thread issues.
+    constexpr uint32_t kRowHi = desc_hi(128);
+    const bool scores = warp == 5;
     bool ok = true;
     auto wait = [&](int b, uint32_t parity) {
       ok = __all_sync(0xffffffffu, wait_phase(bar(b), parity, abort, limit));
       return ok;
     };
-    int slot = 0, it = 0, seg = -1, left = 0;
-    uint32_t turn = 0;  // parity of the units' barriers
-    bool first = false, last = false;
-    while (!last) {
-      const bool fresh = first;  // tile it - 1 begins its segment
-      if (left == 0) {
-        ++seg;
-        if (!wait(kSegFull + seg % kSegRing, (seg / kSegRing) & 1)) break;
-        left = segs[seg % kSegRing].ntiles;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kSegEmpty + seg % kSegRing));
-        first = true;
-        last = left == 0;
-      } else {
-        first = false;
-      }
-      if (!last) {
-        // S of tile it
-        const int qb = seg % S::kQBufs;
+    int slot = scores ? 0 : 1, it = 0;  // the tile's unit: K tiles are the even ones, V tiles the odd ones
+    uint32_t turn = 0;
+    for (int seg = 0; ok; ++seg) {
+      if (!wait(kSegFull + seg % kSegRing, (seg / kSegRing) & 1)) break;
+      const int n = segs[seg % kSegRing].ntiles;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kSegEmpty + seg % kSegRing));
+      if (n == 0) break;
+      const int qb = seg % S::kQBufs;
+      if (kE4m3 && scores && !wait(kQFull + qb, (seg / S::kQBufs) & 1)) break;
+      for (int j = 0; j < n; ++j, ++it) {
         if (!wait(kFull + slot, turn)) break;
-        if (kE4m3 && first && !wait(kQFull + qb, (seg / S::kQBufs) & 1)) break;
-        if (!wait(kSEmpty + (it & 1), ((it >> 1) + 1) & 1)) break;
+        if (!wait(scores ? kSEmpty + (it & 1) : kPFull, scores ? ((it >> 1) + 1) & 1 : it & 1)) break;
         fence_proxy_async_smem();
         tc_fence_after();
-        const uint32_t a = k_lo + slot * (S::kUnit >> 4), q = q_lo + qb * (S::kQBytes >> 4);
-        if (elect_one()) {
+        const uint32_t unit_a = smem_addr(units) + slot * S::kUnit;
+        if (scores) {
+          constexpr uint32_t kDesc = mma_idesc(kE4m3, false, N);
+          const uint32_t a = desc_lo(unit_a, 16), q = desc_lo(smem_addr(q_s) + qb * S::kQBytes, 16);
+          if (elect_one()) {
 #pragma unroll
-          for (int part = 0; part < S::kQParts; ++part)
+            for (int part = 0; part < S::kQParts; ++part)
 #pragma unroll
-            for (int k = 0; k < kQkSteps; ++k)
-              mma<kE4m3>(tmem_sc + (it & 1) * N, a + (((k >> 2) * 16384 + (k & 3) * 32) >> 4), kRowHi,
-                         q + ((part * S::kQPart + (k >> 2) * (N * 128) + (k & 3) * 32) >> 4), kRowHi, kQkDesc,
-                         part + k > 0);
-          mma_commit(bar(kEmpty + slot));
-          mma_commit(bar(kSFull + (it & 1)));
-          if (left == 1) mma_commit(bar(kQEmpty + qb));
+              for (int k = 0; k < S::kRow / 32; ++k)  // 32 bytes of K
+                mma<kE4m3>(tmem_sc + (it & 1) * N, a + (((k >> 2) * 16384 + (k & 3) * 32) >> 4), kRowHi,
+                           q + ((part * S::kQPart + (k >> 2) * (N * 128) + (k & 3) * 32) >> 4), kRowHi, kDesc,
+                           part + k > 0);
+            mma_commit(bar(kEmpty + slot));
+            mma_commit(bar(kSFull + (it & 1)));
+            if (j == n - 1) mma_commit(bar(kQEmpty + qb));
+          }
+        } else {
+          constexpr uint32_t kDesc = mma_idesc(kE4m3, true, 2 * N);
+          constexpr int kStep = kE4m3 ? 32 : 16;  // tokens
+          const uint32_t a = desc_lo(unit_a, 16384), q = desc_lo(smem_addr(p_s), 128 * S::kPRow);
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < 128 / kStep; ++k)
+              mma<kE4m3>(tmem_o, a + ((k * kStep * 128) >> 4), kRowHi, q + ((k * kStep * S::kPRow) >> 4), desc_hi(S::kPRow),
+                         kDesc, j + k > 0);
+            mma_commit(bar(kEmpty + slot));
+            mma_commit(bar(kPvDone));
+          }
         }
         __syncwarp();
-        if (++slot == S::kSlots) {
-          slot = 0;
-          turn ^= 1;
-        }
-        --left;
-      }
-      if (it > 0) {
-        // O of tile it - 1
-        if (!wait(kFull + slot, turn) || !wait(kPFull, (it - 1) & 1)) break;
-        fence_proxy_async_smem();
-        tc_fence_after();
-        const uint32_t a = v_lo + slot * (S::kUnit >> 4);
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < kPvSteps; ++k)
-            mma<kE4m3>(tmem_o, a + k * ((kE4m3 ? 4096 : 2048) >> 4), kRowHi, p_lo + ((k * (kE4m3 ? 32 : 16) * S::kPRow) >> 4),
-                       kPHi, kPvDesc, k > 0 || !fresh);
-          mma_commit(bar(kEmpty + slot));
-          mma_commit(bar(kPvDone));
-        }
-        __syncwarp();
-        if (++slot == S::kSlots) {
-          slot = 0;
+        slot += 2;
+        if (slot >= S::kSlots) {
+          slot -= S::kSlots;
           turn ^= 1;
         }
       }
-      ++it;
     }
     if (!ok) {
       if (lane == 0) fail();
       // let the MMAs issued so far finish before TMEM is freed
-      if (elect_one()) mma_commit(bar(kDrain));
+      const int drain = scores ? kDrain : kDrain + 1;
+      if (elect_one()) mma_commit(bar(drain));
       const int never = 0;
-      wait_phase(bar(kDrain), 0, &never, limit);
+      wait_phase(bar(drain), 0, &never, limit);
     }
     __syncwarp();
   } else {
     // ---------------------------------------------------------- addresses
-    int it = 0;
+    // One warp, four tokens a lane; the next tile's ids are on their way while this tile's pages are looked up.
+    const int shift = p.page_shift;
     bool ok = true;
-    for (int seg = 0; ok; ++seg) {
-      ok = __all_sync(0xffffffffu, wait_phase(bar(kSegFull + seg % kSegRing), (seg / kSegRing) & 1, abort, limit));
-      if (!ok) break;
-      const AttnSeg sg = segs[seg % kSegRing];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kSegEmpty + seg % kSegRing));
-      if (sg.ntiles == 0) break;
-      const int64_t table_row = p.row_indices ? p.row_indices[sg.row] : sg.row;
-      const bool row_ok = table_row >= 0 && table_row < p.bt_rows;
-      const int32_t* table = p.block_table + (row_ok ? table_row : 0) * p.bt_stride;
-      for (int j = 0; j < sg.ntiles; ++j, ++it) {
-        if ((it & 1) != (warp & 1)) continue;
-        const int a = it % kAddrRing;
-        ok = __all_sync(0xffffffffu, wait_phase(bar(kAEmpty + a), (it / kAddrRing + 1) & 1, abort, limit));
-        if (!ok) break;
-        int32_t pos[4], page[4];
-        bool bad = false;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int64_t e = static_cast<int64_t>(sg.tile0 + j) * kAttnTile + k * 32 + lane;
-          pos[k] = -1;
-          if (p.token_ids) {
-            if (e < sg.last) pos[k] = p.token_ids[static_cast<int64_t>(sg.row) * p.ids_ld + e];
-          } else if (sg.first + e < sg.last) {
-            pos[k] = static_cast<int32_t>(sg.first + e);
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          page[k] = -1;
-          if (pos[k] >= 0) {
-            const int32_t col = pos[k] / p.page_size;
-            if (row_ok && col < p.bt_stride)
-              page[k] = table[col];
-            if (page[k] < 0 || page[k] >= p.num_pages) {
-              bad = true;
-              page[k] = -1;
-            }
-          }
-        }
-        float2 sc[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          int64_t off = -1;
-          sc[k] = make_float2(1.f, 1.f);
-          if (page[k] >= 0) {
-            const int64_t in_page = static_cast<int64_t>(sg.kvh) * p.page_size + pos[k] % p.page_size;
-            off = (page[k] * p.page_stride + in_page * D) * (kE4m3 ? 1 : 2);
-            if (kE4m3) {
-              const int64_t at = page[k] * p.scale_page_stride + in_page;
-              sc[k] = make_float2(p.k_scales[at], p.v_scales[at]);
-            }
-          }
-          ring_off[a * 128 + k * 32 + lane] = off;
-          const uint32_t mask = __ballot_sync(0xffffffffu, off >= 0);
-          if (lane == 0) ring_mask[a * 4 + k] = mask;
-        }
-        if (kE4m3)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) ring_scale[a * 128 + k * 32 + lane] = sc[k];
-        if (bad) atomicOr(p.status, kStatusBounds);
+    auto wait = [&](int b, uint32_t parity) {
+      ok = __all_sync(0xffffffffu, wait_phase(bar(b), parity, abort, limit));
+      return ok;
+    };
+    AttnSeg sg;
+    sg.ntiles = 0;
+    int seg = -1, j = 0;
+    int64_t ids_at = 0, head_at = 0;
+    const int32_t* table = nullptr;  // the row's block-table row, null if out of range
+    // the next tile of the work: its tokens' positions, -1 where there is none; false at the end
+    auto next_tile = [&](int32_t(&pos)[4]) {
+      if (++j >= sg.ntiles) {
+        ++seg;
+        j = 0;
+        if (!wait(kSegFull + seg % kSegRing, (seg / kSegRing) & 1)) return false;
+        sg = segs[seg % kSegRing];
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kAFull + a));
+        if (lane == 0) mbar_arrive(bar(kSegEmpty + seg % kSegRing));
+        if (sg.ntiles == 0) return false;
+        const int64_t table_row = p.row_indices ? p.row_indices[sg.row] : sg.row;
+        table = table_row >= 0 && table_row < p.bt_rows ? p.block_table + table_row * p.bt_stride : nullptr;
+        ids_at = static_cast<int64_t>(sg.row) * p.ids_ld;
+        head_at = static_cast<int64_t>(sg.kvh) * p.page_size;
       }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int64_t e = static_cast<int64_t>(sg.tile0 + j) * kAttnTile + k * 32 + lane;
+        pos[k] = -1;
+        if (p.token_ids) {
+          if (e < sg.last) pos[k] = p.token_ids[ids_at + e];
+        } else if (sg.first + e < sg.last) {
+          pos[k] = static_cast<int32_t>(sg.first + e);
+        }
+      }
+      return true;
+    };
+    int32_t ahead[4];
+    bool more = next_tile(ahead);
+    for (int it = 0; more; ++it) {
+      const int a = it % kAddrRing;
+      const int64_t head = head_at;
+      int32_t in_page[4], page[4];
+      bool asked[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        asked[k] = ahead[k] >= 0;
+        page[k] = -1;
+        in_page[k] = 0;
+        if (asked[k]) {
+          const int32_t col = shift >= 0 ? ahead[k] >> shift : ahead[k] / p.page_size;
+          in_page[k] = ahead[k] - col * p.page_size;
+          if (table && col < p.bt_stride) page[k] = table[col];
+        }
+      }
+      more = next_tile(ahead);
+      if (!ok || !wait(kAEmpty + a, (it / kAddrRing + 1) & 1)) break;
+      bool bad = false;
+      int64_t off[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        off[k] = -1;
+        float2* const scale = ring_scale + a * 128 + k * 32 + lane;
+        if (page[k] >= 0 && page[k] < p.num_pages) {
+          const int64_t vec = head + in_page[k];
+          off[k] = (page[k] * p.page_stride + vec * D) * (kE4m3 ? 1 : 2);
+          if (kE4m3) {
+            const int64_t at = page[k] * p.scale_page_stride + vec;
+            cp4(smem_addr(&scale->x), p.k_scales + at);
+            cp4(smem_addr(&scale->y), p.v_scales + at);
+          }
+        } else {
+          if (kE4m3) *scale = make_float2(1.f, 1.f);
+          bad |= asked[k];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        ring_off[a * 128 + k * 32 + lane] = off[k];
+        const uint32_t mask = __ballot_sync(0xffffffffu, off[k] >= 0);
+        if (lane == 0) ring_mask[a * 4 + k] = mask;
+      }
+      if (kE4m3) {
+        cp_arrive(bar(kScFull + a));
+        mbar_arrive(bar(kScFull + a));
+      }
+      if (bad) atomicOr(p.status, kStatusBounds);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kAFull + a));
     }
     if (!ok && lane == 0) fail();
+    cp_wait_all();
   }
   } else {
     // ------------------------------------------------------------ softmax
@@ -831,7 +838,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       bool fresh = true;  // no token so far
       for (int j = 0; j < sg.ntiles; ++j, ++it) {
         const int a = it % kAddrRing;
-        wait(kAFull + a, (it / kAddrRing) & 1);
+        wait((kE4m3 ? kScFull : kAFull) + a, (it / kAddrRing) & 1);
         wait(kSFull + (it & 1), (it >> 1) & 1);
         float s[C];  // scores, less the running maxima, then P
         bool over = failed, first = false;

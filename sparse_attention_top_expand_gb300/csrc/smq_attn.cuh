@@ -46,6 +46,7 @@ struct AttnParams {
   int32_t group;      // query heads per kv head
   int32_t head_dim;
   int32_t page_size;
+  int32_t page_shift;  // log2 of page_size, or -1
   float scale_log2;   // softmax_scale * log2(e)
   const uint16_t* q;
   int64_t q_stride;

@@ -112,6 +112,9 @@ int run_attention(const smq_attn_plan* plan, const smq_attention_args* args, boo
   p.group = d.num_heads / d.num_kv_heads;
   p.head_dim = d.head_dim;
   p.page_size = d.page_size;
+  p.page_shift = -1;
+  for (int i = 0; i <= 16; ++i)
+    if (d.page_size == 1 << i) p.page_shift = i;
   p.scale_log2 = plan->scale * 1.4426950408889634f;
   p.q = a.q;
   p.q_stride = a.q_stride;
