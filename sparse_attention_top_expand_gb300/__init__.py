@@ -184,8 +184,8 @@ def _ptr(t: Optional[torch.Tensor], dtypes, name: str, device=None):
 
 
 def _stream(stream) -> int:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # the raw handle: building a torch Stream object costs more than a small call
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)

@@ -34,6 +34,8 @@
 
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 namespace smq {
 
 namespace {
@@ -57,7 +59,7 @@ struct AttnSeg {
   int32_t tile0, ntiles;  // ntiles = 0: the end of this CTA's work
   int32_t first, last;    // decode: positions [first, last); selected: entries [0, num_ids)
   int32_t slot;           // partial slot, -1: the whole item, write the result
-  int32_t pad;
+  int32_t table_row;      // of the block table, -1: out of range
 };
 static_assert(sizeof(AttnSeg) == 32, "");
 
@@ -385,50 +387,57 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   if (warp == 5) tmem_alloc(smem_addr(&tmem_slot), S::kTmem);
   griddep_wait();
 
-  // ---- this CTA's range of the tile list: prefix sums over the rows
-  const int per_thread = (p.rows + kThreads - 1) / kThreads;
-  long long mine = 0;
-  for (int i = 0; i < per_thread; ++i) {
-    const int r = tid * per_thread + i;
-    if (r >= p.rows) break;
-    int32_t first, last;
-    row_range(p, r, blockIdx.x == 0, first, last);
-    mine += row_tiles(first, last) * p.kv_heads;
-  }
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 31) warp_sum[warp] = incl;
+  // ---- this CTA's range of the tile list
   tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  long long before = incl - mine, total = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += warp_sum[w];
-    total += warp_sum[w];
-  }
-  const long long chunk = (total + gridDim.x - 1) / gridDim.x;
-  const long long begin = chunk * blockIdx.x;
-  const long long work = begin < total ? min(chunk, total - begin) : 0;
-  if (work > 0 && begin >= before && begin < before + mine) {
-    long long at = before;
+  long long total, begin, chunk;
+  if (p.token_ids) {  // rows of one length
+    total = row_tiles(0, p.num_ids) * p.kv_heads * p.rows;
+  } else {  // prefix sums over the rows
+    const int per_thread = (p.rows + kThreads - 1) / kThreads;
+    long long mine = 0;
     for (int i = 0; i < per_thread; ++i) {
       const int r = tid * per_thread + i;
+      if (r >= p.rows) break;
       int32_t first, last;
-      row_range(p, r, false, first, last);
-      const long long t = row_tiles(first, last) * p.kv_heads;
-      if (begin < at + t) {
-        start_row = r;
-        start_idx = begin - at;
-        break;
+      row_range(p, r, blockIdx.x == 0, first, last);
+      mine += row_tiles(first, last) * p.kv_heads;
+    }
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    long long before = incl - mine;
+    total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += warp_sum[w];
+      total += warp_sum[w];
+    }
+    begin = (total + gridDim.x - 1) / gridDim.x * blockIdx.x;
+    if (begin < total && begin >= before && begin < before + mine) {
+      long long at = before;
+      for (int i = 0; i < per_thread; ++i) {
+        const int r = tid * per_thread + i;
+        int32_t first, last;
+        row_range(p, r, false, first, last);
+        const long long t = row_tiles(first, last) * p.kv_heads;
+        if (begin < at + t) {
+          start_row = r;
+          start_idx = begin - at;
+          break;
+        }
+        at += t;
       }
-      at += t;
     }
   }
+  chunk = (total + gridDim.x - 1) / gridDim.x;
+  begin = chunk * blockIdx.x;
+  const long long work = begin < total ? min(chunk, total - begin) : 0;
   __syncthreads();
+  tc_fence_after();
   const uint32_t tmem = tmem_slot;
   const uint32_t tmem_o = tmem, tmem_sc = tmem + 2 * N;
   const volatile int* const abort = &abort_flag;
@@ -549,11 +558,19 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   } else if (warp == 4) {
     // ---------------------------------------------------------- scheduler
     long long left = work;
-    int row = start_row;
-    long long idx = work > 0 ? start_idx : 0;
+    int row = 0;
+    long long idx = 0;  // tile of the row, over its kv heads
+    if (work > 0 && p.token_ids) {
+      const long long per_row = row_tiles(0, p.num_ids) * p.kv_heads;
+      row = static_cast<int>(begin / per_row);
+      idx = begin % per_row;
+    } else if (work > 0) {
+      row = start_row;
+      idx = start_idx;
+    }
     int4 info = make_int4(0, 0, 0, 0);
     int base = -64, seg = 0;
-    int32_t first_l = 0, last_l = 0;
+    int32_t first_l = 0, last_l = 0, table_l = 0;
     bool ok = true;
     while (ok) {
       AttnSeg sg;
@@ -561,8 +578,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       if (left > 0) {
         if (row >= base + 32) {  // the next 32 rows' ranges, one per lane
           base = row;
-          if (row + lane < p.rows) row_range(p, row + lane, false, first_l, last_l);
+          if (row + lane < p.rows) {
+            table_l = p.row_indices ? p.row_indices[row + lane] : row + lane;
+            if (table_l < 0 || table_l >= p.bt_rows) table_l = -1;
+            row_range(p, row + lane, false, first_l, last_l);
+          }
         }
+        sg.table_row = __shfl_sync(0xffffffffu, table_l, row - base);
         sg.first = __shfl_sync(0xffffffffu, first_l, row - base);
         sg.last = __shfl_sync(0xffffffffu, last_l, row - base);
         const long long t = row_tiles(sg.first, sg.last);
@@ -690,8 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kSegEmpty + seg % kSegRing));
         if (sg.ntiles == 0) return false;
-        const int64_t table_row = p.row_indices ? p.row_indices[sg.row] : sg.row;
-        table = table_row >= 0 && table_row < p.bt_rows ? p.block_table + table_row * p.bt_stride : nullptr;
+        table = sg.table_row >= 0 ? p.block_table + static_cast<int64_t>(sg.table_row) * p.bt_stride : nullptr;
         ids_at = static_cast<int64_t>(sg.row) * p.ids_ld;
         head_at = static_cast<int64_t>(sg.kvh) * p.page_size;
       }
@@ -1008,66 +1029,112 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   if (warp == 5) tmem_dealloc(tmem, S::kTmem);
 }
 
-// Join the partials of the item that CTA blockIdx.x of the attention kernel
-// began and others continued: out = sum_i w_i O_i / sum_i w_i l_i with
-// w_i = 2^(m_i - max m). blockIdx.y picks p.heads_per_cta heads. With one head
-// the eight warps share the partials, with eight each warp has a head.
+// Join the partials of an item that CTA `first` of the attention kernel began
+// and others continued: out = sum_i w_i O_i / sum_i w_i l_i with
+// w_i = 2^(m_i - max m). blockIdx.x is that CTA, or, for few items, the item
+// (`by_item`: the block looks for the CTA, which keeps blocks without work few);
+// blockIdx.y picks heads_per_cta heads. With one head
+// the eight warps share the partials, with eight each warp has a head. Bound
+// by latency: the first partial outputs are loaded along with the maxima.
 template <int D>
-__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ AttnParams p, int heads_per_cta) {
-  constexpr int kPer = D / 32;
+__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ AttnParams p, int ctas, int by_item,
+                                                      int heads_per_cta) {
+  constexpr int kPer = D / 32, kBatch = 8;
   griddep_launch_dependents();
   griddep_wait();
-  const int4 info = p.seg_info[blockIdx.x];
+  __shared__ float acc_s[8][D], sum_s[8], max_s[8];
+  __shared__ int first_s;
+  int first = blockIdx.x;
+  if (by_item) {
+    if (threadIdx.x == 0) first_s = -1;
+    __syncthreads();
+    for (int c = threadIdx.x; c < ctas; c += 256) {
+      const int4 i = p.seg_info[c];
+      if (i.z > 0 && static_cast<int64_t>(i.x) * p.kv_heads + i.y == blockIdx.x) first_s = c;
+    }
+    __syncthreads();
+    first = first_s;
+    if (first < 0) return;
+  }
+  const int4 info = p.seg_info[first];
   const int parts = info.z + 1;
   if (parts == 1) return;
-  __shared__ float acc_s[8][D], sum_s[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int shares = heads_per_cta == 1 ? 8 : 1;  // warps per head
   const int h = blockIdx.y * heads_per_cta + (shares == 1 ? warp : 0);
-  const bool live = h < p.group;
-  auto slot = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i)); };
-  float m = -INFINITY, l = 0.f, acc[kPer];
+  const int i0 = shares == 1 ? 0 : warp;
+  const int n = h < p.group && i0 < parts ? (parts - i0 + shares - 1) / shares : 0;  // partials of this warp
+  auto slot = [&](int k) {
+    const int i = i0 + k * shares;
+    return (static_cast<int64_t>(i == 0 ? 2 * first + 1 : 2 * (first + i)) * p.group + h);
+  };
+  float m = kUnset, l = 0.f, acc[kPer];
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
-  if (live) {
-    const int i0 = shares == 1 ? 0 : warp;
-    for (int i = lane; i < parts; i += 32) m = fmaxf(m, p.part_ml[slot(i) * p.group + h].x);
+  for (int j = 0; j < kPer; ++j) acc[j] = 0.f;
+  for (int base = 0; base < n; base += 32) {
+    const int count = min(32, n - base);
+    float2 ml = make_float2(kUnset, 0.f);
+    if (lane < count) ml = p.part_ml[slot(base + lane)];
+    float w = 0.f;
+    for (int k0 = 0; k0 < count; k0 += kBatch) {
+      using Vec = typename std::conditional<kPer == 4, float4, float2>::type;
+      union {
+        Vec v;
+        float f[kPer];
+      } x[kBatch];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-#pragma unroll 8
-    for (int i = i0; i < parts; i += shares) {
-      const float2 ml = p.part_ml[slot(i) * p.group + h];
-      const float* src = p.part_o + (slot(i) * p.group + h) * D + lane * kPer;
-      float x[kPer];
+      for (int k = 0; k < kBatch; ++k)
+        if (k0 + k < count) x[k].v = *reinterpret_cast<const Vec*>(p.part_o + slot(base + k0 + k) * D + lane * kPer);
+      if (k0 == 0) {
+        float top = ml.x;
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) x[k] = src[k];
-      const float w = exp2f(ml.x - m);
-      l = fmaf(ml.y, w, l);
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float now = fmaxf(m, top), old = ex2(m - now);
+        w = ex2(ml.x - now);
+        float sum = lane < count ? w * ml.y : 0.f;
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) acc[k] = fmaf(x[k], w, acc[k]);
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        l = fmaf(l, old, sum);
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) acc[j] *= old;
+        m = now;
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w, k0 + k);
+        if (k0 + k < count)
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) acc[j] = fmaf(x[k].f[j], wk, acc[j]);
+      }
     }
   }
   if (shares > 1) {
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) acc_s[warp][lane * kPer + k] = acc[k];
-    if (lane == 0) sum_s[warp] = l;
+    for (int j = 0; j < kPer; ++j) acc_s[warp][lane * kPer + j] = acc[j];
+    if (lane == 0) {
+      sum_s[warp] = l;
+      max_s[warp] = m;
+    }
     __syncthreads();
     if (warp != 0) return;
+    m = max_s[0];
+    for (int w = 1; w < 8; ++w) m = fmaxf(m, max_s[w]);
     l = 0.f;
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
+    for (int j = 0; j < kPer; ++j) acc[j] = 0.f;
     for (int w = 0; w < 8; ++w) {
-      l += sum_s[w];
+      const float wk = ex2(max_s[w] - m);
+      l = fmaf(sum_s[w], wk, l);
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) acc[k] += acc_s[w][lane * kPer + k];
+      for (int j = 0; j < kPer; ++j) acc[j] = fmaf(acc_s[w][lane * kPer + j], wk, acc[j]);
     }
   }
-  if (!live) return;
+  if (h >= p.group) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const int64_t out_row = (static_cast<int64_t>(info.x) * p.kv_heads + info.y) * p.group + h;
 #pragma unroll
-  for (int k = 0; k < kPer; k += 2)
-    *reinterpret_cast<uint32_t*>(p.out + out_row * D + lane * kPer + k) = bf16x2(acc[k] * inv, acc[k + 1] * inv);
+  for (int j = 0; j < kPer; j += 2)
+    *reinterpret_cast<uint32_t*>(p.out + out_row * D + lane * kPer + j) = bf16x2(acc[j] * inv, acc[j + 1] * inv);
   if (p.lse && lane == 0) p.lse[out_row] = (m + log2f(l)) * 0.69314718055994531f;
 }
 
@@ -1128,11 +1195,17 @@ cudaError_t launch_attention(const AttnParams& p, bool e4m3, int grid, cudaStrea
     return launch(kernel, dim3(grid), kThreads, smem, stream, p);
   });
   if (rc != cudaSuccess) return rc;
+  // no row is shared where the tile list is cut between items only
+  const int64_t tiles = ((p.token_ids ? p.num_ids : static_cast<int64_t>(p.bt_stride) * p.page_size) + kAttnTile - 1) / kAttnTile;
+  const int64_t chunk = (tiles * p.rows * p.kv_heads + grid - 1) / grid;
+  if (tiles == 1 || (p.token_ids && chunk % tiles == 0)) return cudaSuccess;
   // few items: an item has many partials, shared by a CTA per head
   const int64_t items = static_cast<int64_t>(p.rows) * p.kv_heads;
   const int heads_per_cta = items * 4 >= grid ? 8 : 1;
+  const int by_item = heads_per_cta == 1;
   return launch(p.head_dim == 128 ? combine_kernel<128> : combine_kernel<64>,
-                dim3(grid, (p.group + heads_per_cta - 1) / heads_per_cta), 256, 0, stream, p, heads_per_cta);
+                dim3(by_item ? static_cast<unsigned>(items) : grid, (p.group + heads_per_cta - 1) / heads_per_cta), 256, 0, stream, p, grid,
+                by_item, heads_per_cta);
 }
 
 }  // namespace smq
