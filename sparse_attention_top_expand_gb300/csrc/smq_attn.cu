@@ -115,11 +115,13 @@ __device__ __forceinline__ void add2(float& x0, float& x1, float y0, float y1) {
       : "f"(y0), "f"(y1));
 }
 
-// Wait for the phase of the given parity; false after limit_ns or once *abort is set. Every role's waits are
-// inlined in its loop, so this keeps to a few instructions.
+// Wait for the phase of the given parity; false after limit_ns or once *abort is set. Some forty waits a tile share
+// the issue slots with the softmax: each try is suspended by the hardware until the phase completes or a system limit
+// passes, and the clock is read once in 16 tries.
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const volatile int* abort, uint64_t limit_ns) {
   uint64_t t0 = 0;
-  while (!mbar_try_wait_sleep(bar, parity, kWaitSleepNs)) {
+  for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
+    if (n % 16 != 0) continue;
     const uint64_t now = global_ns();
     if (t0 == 0) t0 = now;
     if (*abort || now - t0 > limit_ns) return false;
@@ -127,7 +129,10 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const 
   return true;
 }
 
-// 16-byte asynchronous copy; `bytes` 0 fills with zeros and reads nothing.
+// 16-byte asynchronous copies; of the second, `bytes` 0 fills with zeros and reads nothing.
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
@@ -525,20 +530,28 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       const uint32_t dst0 = units_a + slot * S::kUnit + (piece >> 3) * 16384;
       const int64_t* const offs = ring_off + tile % kAddrRing * 128 + warp * 32 + sub;
       constexpr int kBatch = 32 / kTok < 8 ? 32 / kTok : 8;  // addresses first, so that the copies issue back to back
+      const uint32_t dst1 = dst0 + (warp * 32 + sub) * 128;
+      const bool whole = ring_mask[tile % kAddrRing * 4 + warp] == 0xffffffffu;  // every token of the warp is there
+      if (__builtin_expect(whole, 1)) {
 #pragma unroll
-      for (int i0 = 0; i0 < 32 / kTok; i0 += kBatch) {
-        const uint8_t* src[kBatch];
-        uint32_t bytes[kBatch];
+        for (int i0 = 0; i0 < 32 / kTok; i0 += kBatch) {
+          const uint8_t* src[kBatch];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int64_t o = offs[(i0 + i) * kTok];
-          bytes[i] = o < 0 ? 0 : 16;
-          src[i] = base + (o < 0 ? 0 : o);
+          for (int i = 0; i < kBatch; ++i) src[i] = base + offs[(i0 + i) * kTok];
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i)
+            cp16(dst1 + (i0 + i) * kTok * 128 + (((piece & 7) ^ (((i0 + i) * kTok + sub) & 7)) << 4), src[i]);
         }
+      } else {
+#pragma unroll 1
+        for (int i0 = 0; i0 < 32 / kTok; i0 += 4) {
+          int64_t o[4];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int tok = warp * 32 + (i0 + i) * kTok + sub;
-          cp16(dst0 + tok * 128 + (((piece & 7) ^ (tok & 7)) << 4), src[i], bytes[i]);
+          for (int i = 0; i < 4; ++i) o[i] = offs[(i0 + i) * kTok];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            cp16(dst1 + (i0 + i) * kTok * 128 + (((piece & 7) ^ (((i0 + i) * kTok + sub) & 7)) << 4),
+                 base + (o[i] < 0 ? 0 : o[i]), o[i] < 0 ? 0 : 16);
         }
       }
       if (values || stall_tile != tile) cp_arrive(bar(kFull + slot));
@@ -794,7 +807,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t o_col = tmem_o + lanes + c0;
     float* const red = scratch + wg * 4 * C;
-    const uint32_t p_a = smem_addr(p_s);
+    // this thread's row of P: the 16-byte pieces of its heads, swizzled (its first piece is a multiple of their number)
+    constexpr int kWords = kE4m3 ? C / 4 : C / 2;
+    constexpr bool kWide = N == 128 && !kE4m3;  // a block of 64 heads for each group
+    const int p_swz = (S::kPRow == 128 ? (t & 7) : S::kPRow == 64 ? ((t >> 1) & 3) : ((t >> 2) & 1)) ^
+                      (kWide ? 0 : wg * (kWords / 4));
+    const uint32_t p_row = smem_addr(p_s) + t * S::kPRow + (kWide ? wg * 128 * S::kPRow : 0);
     bool failed = false, leave = false;
     int it = 0;
     auto wait = [&](int b, uint32_t parity) {
@@ -943,7 +961,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           if (first) fresh = false;
         }
         // this thread's row of P: C heads of token t, in two parts
-        constexpr int kWords = kE4m3 ? C / 4 : C / 2;
         uint32_t hi[kWords], lo[kWords];
 #pragma unroll
         for (int c = 0; c < C; ++c) s[c] = ex2(s[c]);
@@ -984,13 +1001,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           tmem_wait_st();
           tc_fence_before();
         }
-        const int swz = S::kPRow == 128 ? (t & 7) : S::kPRow == 64 ? ((t >> 1) & 3) : ((t >> 2) & 1);
-        constexpr bool kWide = N == 128 && !kE4m3;  // a block of 64 heads for each group
-        const uint32_t row_a = p_a + t * S::kPRow + (kWide ? wg * 128 * S::kPRow : 0);
-        const int chunk0 = kWide ? 0 : wg * (kWords / 4);
 #pragma unroll
         for (int i = 0; i < kWords; i += 4) {
-          const uint32_t at = row_a + (((chunk0 + i / 4) ^ swz) << 4);
+          const uint32_t at = p_row + ((i / 4 ^ p_swz) << 4);
           sts16(at, hi[i], hi[i + 1], hi[i + 2], hi[i + 3]);
           sts16(at + S::kPPart, lo[i], lo[i + 1], lo[i + 2], lo[i + 3]);
         }
