@@ -486,13 +486,19 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
               cp16(smem_addr(qdst) + (c >> 3) * (N * 128) + i * 128 + (((c & 7) ^ (i & 7)) << 4),
                    qrow + (i < p.group ? i * D + c * 8 : 0), i < p.group ? 16 : 0);
           } else {
-            // a head per D / 8 lanes; each stored as hi + lo times a power of two that brings its amax to (224, 448]
+            // A head per D / 8 lanes, fetched with all loads in flight into the rows where it is then stored, as hi + lo
+            // times a power of two that brings its amax to (224, 448].
             constexpr int kL = D / 8;
-            const int c = lane % kL;
-            for (int i0 = warp * (32 / kL); i0 < N; i0 += 4 * (32 / kL)) {
-              const int i = i0 + lane / kL;
-              uint4 w = make_uint4(0, 0, 0, 0);
-              if (i < p.group) w = *reinterpret_cast<const uint4*>(qrow + i * D + c * 8);
+            const int c = lane % kL, i0 = warp * (32 / kL) + lane / kL;
+            uint8_t* const piece_q = qdst + (c >> 3) * S::kQPart + (c & 7) * 16;
+            for (int i = i0; i < N; i += 4 * (32 / kL))
+              cp16(smem_addr(piece_q + i * 128), qrow + (i < p.group ? i * D + c * 8 : 0), i < p.group ? 16 : 0);
+            cp_wait_all();
+            __syncwarp();
+#pragma unroll 1
+            for (int i = i0; i < N; i += 4 * (32 / kL)) {
+              const uint4 w = *reinterpret_cast<const uint4*>(piece_q + i * 128);
+              __syncwarp();
               const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
               float x[8], amax = 0.f;
 #pragma unroll
@@ -651,6 +657,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       const int qb = seg % S::kQBufs;
       if (kE4m3 && scores && !wait(kQFull + qb, (seg / S::kQBufs) & 1)) break;
       for (int j = 0; j < n; ++j, ++it) {
+        // the softmax reads the tile's mask and scales behind S: they are there before S is issued
+        if (scores && !wait((kE4m3 ? kScFull : kAFull) + it % kAddrRing, (it / kAddrRing) & 1)) break;
         if (!wait(kFull + slot, turn)) break;
         if (!wait(scores ? kSEmpty + (it & 1) : kPFull, scores ? ((it >> 1) + 1) & 1 : it & 1)) break;
         fence_proxy_async_smem();
@@ -855,6 +863,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       tc_fence_before();
     };
     float l[C];
+    bool s_ready = false;
     AttnSeg done;  // the segment whose O is still to be written: behind the next one's first tile
     done.ntiles = 0;
     for (int seg = 0;; ++seg) {
@@ -877,8 +886,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       bool fresh = true;  // no token so far
       for (int j = 0; j < sg.ntiles; ++j, ++it) {
         const int a = it % kAddrRing;
-        wait((kE4m3 ? kScFull : kAFull) + a, (it / kAddrRing) & 1);
-        wait(kSFull + (it & 1), (it >> 1) & 1);
+        if (!s_ready) wait(kSFull + (it & 1), (it >> 1) & 1);
         float s[C];  // scores, less the running maxima, then P
         bool over = failed, first = false;
         float inv_vs = 1.f;
@@ -928,6 +936,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           over = most > S::kTau || first;
         }
         const bool raise = bar_or(bar_id, 128, over);
+        // asked early, as an answer takes its time behind the copies in the load-store queue
+        const bool pv_ready = it == 0 || mbar_test_wait(bar(kPvDone), (it - 1) & 1);
         if (__builtin_expect(raise, 0)) {
           // raise this group's maxima to the tile's, or set them at the row's first tokens
           constexpr int kHalf = C > 32 ? 32 : C;
@@ -982,7 +992,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         // computed here, not behind the wait, where the compiler would move it
 #pragma unroll
         for (int i = 0; i < kWords; ++i) asm volatile("" : "+r"(hi[i]), "+r"(lo[i]));
-        if (it > 0) wait(kPvDone, (it - 1) & 1);  // O is final up to the previous tile, and P is free
+        s_ready = mbar_test_wait(bar(kSFull + ((it + 1) & 1)), ((it + 1) >> 1) & 1);
+        if (!pv_ready) wait(kPvDone, (it - 1) & 1);  // O is final up to the previous tile, and P is free
         if (j == 0 && done.ntiles > 0) write_out(done);
         if (raise && j > 0) {
           tc_fence_after();
