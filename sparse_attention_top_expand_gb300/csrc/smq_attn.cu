@@ -109,24 +109,43 @@ __device__ __forceinline__ void fma2(float& x0, float& x1, float f0, float f1, f
       : "+f"(x0), "+f"(x1)
       : "f"(f0), "f"(f1), "f"(a0), "f"(a1));
 }
+// a += x * f
+__device__ __forceinline__ void fma2acc(float& a0, float& a1, float x0, float x1, float f) {
+  asm("{\n .reg .b64 x, f, a;\n mov.b64 x, {%2, %3};\n mov.b64 f, {%4, %4};\n mov.b64 a, {%0, %1};\n"
+      " fma.rn.f32x2 a, x, f, a;\n mov.b64 {%0, %1}, a;\n}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(x0), "f"(x1), "f"(f));
+}
+__device__ __forceinline__ void mul2(float& x0, float& x1, float y0, float y1) {
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(y0), "f"(y1));
+}
 __device__ __forceinline__ void add2(float& x0, float& x1, float y0, float y1) {
   asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
       : "+f"(x0), "+f"(x1)
       : "f"(y0), "f"(y1));
 }
 
-// Wait for the phase of the given parity; false after limit_ns or once *abort is set. Some forty waits a tile share
-// the issue slots with the softmax: each try is suspended by the hardware until the phase completes or a system limit
-// passes, and the clock is read once in 16 tries.
+// A warp waits for the phase of the given parity; false, for all of it, after limit_ns or once *abort is set. Some
+// forty waits a tile share the issue slots with the softmax: each try is suspended by the hardware until the phase
+// completes or a system limit passes, the vote keeps the loop's branches uniform, and the clock is read once in 16 tries.
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const volatile int* abort, uint64_t limit_ns) {
   uint64_t t0 = 0;
-  for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
+  for (uint32_t n = 1; !__all_sync(0xffffffffu, mbar_try_wait(bar, parity)); ++n) {
     if (n % 16 != 0) continue;
     const uint64_t now = global_ns();
     if (t0 == 0) t0 = now;
-    if (*abort || now - t0 > limit_ns) return false;
+    if (__any_sync(0xffffffffu, *abort || now - t0 > limit_ns)) return false;
   }
   return true;
+}
+
+// One lane's arrival, without a branch.
+__device__ __forceinline__ void arrive_one(uint32_t bar, int lane) {
+  asm volatile("{\n .reg .pred p;\n setp.eq.s32 p, %1, 0;\n @p mbarrier.arrive.shared::cta.b64 _, [%0];\n}" ::"r"(bar),
+               "r"(lane)
+               : "memory");
 }
 
 // 16-byte asynchronous copies; of the second, `bytes` 0 fills with zeros and reads nothing.
@@ -253,23 +272,27 @@ __device__ __forceinline__ void split_bf16x2(float x0, float x1, uint32_t& hi, u
   lo = bf16x2(r0, r1);
 }
 
-// x0, x1 as two E4M3 pairs, hi + lo / kLift: hi is x rounded, lo the rest times kLift rounded (9 bits together).
+// x0 .. x3 as E4M3 numbers hi + lo / kLift: hi is x rounded, lo the rest times kLift rounded (9 bits together).
 constexpr float kLift = 16.f;  // hi's rest is at most 1/16 of 448 / 2, so 16 times that still fits
 template <bool kLifted>
-__device__ __forceinline__ void split_e4m3x2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
-  uint32_t h, l;
-  asm("{\n .reg .b32 f, g;\n .reg .b16 a, b;\n"
+__device__ __forceinline__ void split_e4m3x4(float x0, float x1, float x2, float x3, uint32_t& hi, uint32_t& lo) {
+  asm("{\n .reg .b32 f, g, h, i;\n .reg .b16 a, b, c, d;\n"
       " cvt.rn.f16x2.f32 f, %3, %2;\n"
+      " cvt.rn.f16x2.f32 g, %5, %4;\n"
       " cvt.rn.satfinite.e4m3x2.f16x2 a, f;\n"
-      " cvt.rn.f16x2.e4m3x2 g, a;\n"
-      " sub.rn.f16x2 f, f, g;\n"
-      " mul.rn.f16x2 f, f, %4;\n"
-      " cvt.rn.satfinite.e4m3x2.f16x2 b, f;\n"
-      " cvt.u32.u16 %0, a;\n cvt.u32.u16 %1, b;\n}"
-      : "=r"(h), "=r"(l)
-      : "f"(x0), "f"(x1), "r"(kLifted ? 0x4c004c00u : 0x3c003c00u));
-  hi = h;
-  lo = l;
+      " cvt.rn.satfinite.e4m3x2.f16x2 b, g;\n"
+      " mov.b32 %0, {a, b};\n"
+      " cvt.rn.f16x2.e4m3x2 h, a;\n"
+      " cvt.rn.f16x2.e4m3x2 i, b;\n"
+      " sub.rn.f16x2 f, f, h;\n"
+      " sub.rn.f16x2 g, g, i;\n"
+      " mul.rn.f16x2 f, f, %6;\n"
+      " mul.rn.f16x2 g, g, %6;\n"
+      " cvt.rn.satfinite.e4m3x2.f16x2 c, f;\n"
+      " cvt.rn.satfinite.e4m3x2.f16x2 d, g;\n"
+      " mov.b32 %1, {c, d};\n}"
+      : "=r"(hi), "=r"(lo)
+      : "f"(x0), "f"(x1), "f"(x2), "f"(x3), "r"(kLifted ? 0x4c004c00u : 0x3c003c00u));
 }
 
 // Reduce kN values over the 32 lanes of a warp, halving the values a lane
@@ -460,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     const uint32_t units_a = smem_addr(units);
     bool ok = true;
     auto wait = [&](int b, uint32_t parity) {
-      ok = __all_sync(0xffffffffu, wait_phase(bar(b), parity, abort, limit));
+      ok = wait_phase(bar(b), parity, abort, limit);
       return ok;
     };
     // Units: K 0, V 0, K 1, V 1, ... The unit's barrier counts each thread's copies when they land; the MMA warps'
@@ -515,18 +538,19 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
               e = e < -100 ? -100 : e;
               const int up = 7 - e + ((bits & 0x7fffffu) <= 0x600000u ? 1 : 0);
               const float mul = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
-              uint32_t hi[4], lo[4];
+              uint32_t hi[2], lo[2];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) split_e4m3x2<false>(x[2 * k] * mul, x[2 * k + 1] * mul, hi[k], lo[k]);
+              for (int k = 0; k < 2; ++k)
+                split_e4m3x4<false>(x[4 * k] * mul, x[4 * k + 1] * mul, x[4 * k + 2] * mul, x[4 * k + 3] * mul, hi[k], lo[k]);
               uint8_t* dst = qdst + i * 128 + (((c >> 1) ^ (i & 7)) << 4) + (c & 1) * 8;
-              *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-              *reinterpret_cast<uint2*>(dst + S::kQPart) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+              *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
+              *reinterpret_cast<uint2*>(dst + S::kQPart) = make_uint2(lo[0], lo[1]);
               if (c == 0) qscale_s[(seg % kQScales) * N + i] = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
             }
             mbar_arrive(bar(kQFull + qb));
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kSegEmpty + seg % kSegRing));
+          arrive_one(bar(kSegEmpty + seg % kSegRing), lane);
           ++seg;
         }
         if (!wait(kAFull + tile % kAddrRing, (tile / kAddrRing) & 1)) break;
@@ -567,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       }
       if (values) {
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kAEmpty + tile % kAddrRing));
+        arrive_one(bar(kAEmpty + tile % kAddrRing), lane);
         ++tile;
         --left;
       }
@@ -622,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           idx = 0;
         }
       }
-      if (seg >= kSegRing) ok = __all_sync(0xffffffffu, wait_phase(bar(kSegEmpty + seg % kSegRing), (seg / kSegRing - 1) & 1, abort, limit));
+      if (seg >= kSegRing) ok = wait_phase(bar(kSegEmpty + seg % kSegRing), (seg / kSegRing - 1) & 1, abort, limit);
       if (!ok) break;
       if (lane == 0) {
         segs[seg % kSegRing] = sg;
@@ -643,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     const bool scores = warp == 5;
     bool ok = true;
     auto wait = [&](int b, uint32_t parity) {
-      ok = __all_sync(0xffffffffu, wait_phase(bar(b), parity, abort, limit));
+      ok = wait_phase(bar(b), parity, abort, limit);
       return ok;
     };
     int slot = scores ? 0 : 1, it = 0;  // the tile's unit: K tiles are the even ones, V tiles the odd ones
@@ -652,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       if (!wait(kSegFull + seg % kSegRing, (seg / kSegRing) & 1)) break;
       const int n = segs[seg % kSegRing].ntiles;
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kSegEmpty + seg % kSegRing));
+      arrive_one(bar(kSegEmpty + seg % kSegRing), lane);
       if (n == 0) break;
       const int qb = seg % S::kQBufs;
       if (kE4m3 && scores && !wait(kQFull + qb, (seg / S::kQBufs) & 1)) break;
@@ -715,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     const int shift = p.page_shift;
     bool ok = true;
     auto wait = [&](int b, uint32_t parity) {
-      ok = __all_sync(0xffffffffu, wait_phase(bar(b), parity, abort, limit));
+      ok = wait_phase(bar(b), parity, abort, limit);
       return ok;
     };
     AttnSeg sg;
@@ -731,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         if (!wait(kSegFull + seg % kSegRing, (seg / kSegRing) & 1)) return false;
         sg = segs[seg % kSegRing];
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kSegEmpty + seg % kSegRing));
+        arrive_one(bar(kSegEmpty + seg % kSegRing), lane);
         if (sg.ntiles == 0) return false;
         table = sg.table_row >= 0 ? p.block_table + static_cast<int64_t>(sg.table_row) * p.bt_stride : nullptr;
         ids_at = static_cast<int64_t>(sg.row) * p.ids_ld;
@@ -800,7 +824,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       }
       if (bad) atomicOr(p.status, kStatusBounds);
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kAFull + a));
+      arrive_one(bar(kAFull + a), lane);
     }
     if (!ok && lane == 0) fail();
     cp_wait_all();
@@ -872,7 +896,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       if (bar_or(bar_id, 128, failed)) break;
       const AttnSeg sg = segs[seg % kSegRing];
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kSegEmpty + seg % kSegRing));
+      arrive_one(bar(kSegEmpty + seg % kSegRing), lane);
       if (sg.ntiles == 0) {
         if (done.ntiles > 0) {
           wait(kPvDone, (it - 1) & 1);
@@ -910,17 +934,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           pin<C>(s);
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(bar(kSEmpty + (it & 1)));
-            mbar_arrive(bar(kAEmpty + a));
-          }
+          arrive_one(bar(kSEmpty + (it & 1)), lane);
+          arrive_one(bar(kAEmpty + a), lane);
           float most = -INFINITY;
 #pragma unroll
           for (int c = 0; c < C; c += 4) {
             float4 a4 = *reinterpret_cast<const float4*>(nm_s + c0 + c), f4 = make_float4(mul, mul, mul, mul);
             if (kE4m3) {
               const float4 q4 = *reinterpret_cast<const float4*>(qscale + c);
-              f4 = make_float4(mul * q4.x, mul * q4.y, mul * q4.z, mul * q4.w);
+              mul2(f4.x, f4.y, q4.x, q4.y);
+              mul2(f4.z, f4.w, q4.z, q4.w);
               add2(a4.x, a4.y, add, add);
               add2(a4.z, a4.w, add, add);
             }
@@ -937,7 +960,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         }
         const bool raise = bar_or(bar_id, 128, over);
         // asked early, as an answer takes its time behind the copies in the load-store queue
-        const bool pv_ready = it == 0 || mbar_test_wait(bar(kPvDone), (it - 1) & 1);
+        const bool pv_ready = it == 0 || __all_sync(0xffffffffu, mbar_test_wait(bar(kPvDone), (it - 1) & 1));
         if (__builtin_expect(raise, 0)) {
           // raise this group's maxima to the tile's, or set them at the row's first tokens
           constexpr int kHalf = C > 32 ? 32 : C;
@@ -977,13 +1000,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 #pragma unroll
         for (int i = 0; i < kWords; ++i) {
           if (kE4m3) {
-            uint32_t h0, h1, l0, l1;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) l[(4 * i + k) % C] = fmaf(s[(4 * i + k) % C], inv_vs, l[(4 * i + k) % C]);
-            split_e4m3x2<true>(s[(4 * i) % C], s[(4 * i + 1) % C], h0, l0);
-            split_e4m3x2<true>(s[(4 * i + 2) % C], s[(4 * i + 3) % C], h1, l1);
-            hi[i] = h0 | (h1 << 16);
-            lo[i] = l0 | (l1 << 16);
+            fma2acc(l[(4 * i) % C], l[(4 * i + 1) % C], s[(4 * i) % C], s[(4 * i + 1) % C], inv_vs);
+            fma2acc(l[(4 * i + 2) % C], l[(4 * i + 3) % C], s[(4 * i + 2) % C], s[(4 * i + 3) % C], inv_vs);
+            split_e4m3x4<true>(s[(4 * i) % C], s[(4 * i + 1) % C], s[(4 * i + 2) % C], s[(4 * i + 3) % C], hi[i], lo[i]);
           } else {
             add2(l[(2 * i) % C], l[(2 * i + 1) % C], s[(2 * i) % C], s[(2 * i + 1) % C]);
             split_bf16x2(s[(2 * i) % C], s[(2 * i + 1) % C], hi[i], lo[i]);
@@ -992,7 +1011,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         // computed here, not behind the wait, where the compiler would move it
 #pragma unroll
         for (int i = 0; i < kWords; ++i) asm volatile("" : "+r"(hi[i]), "+r"(lo[i]));
-        s_ready = mbar_test_wait(bar(kSFull + ((it + 1) & 1)), ((it + 1) >> 1) & 1);
+        s_ready = __all_sync(0xffffffffu, mbar_test_wait(bar(kSFull + ((it + 1) & 1)), ((it + 1) >> 1) & 1));
         if (!pv_ready) wait(kPvDone, (it - 1) & 1);  // O is final up to the previous tile, and P is free
         if (j == 0 && done.ntiles > 0) write_out(done);
         if (raise && j > 0) {
@@ -1020,7 +1039,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kPFull));
+        arrive_one(bar(kPFull), lane);
       }
       if (leave) break;
       // ---- the segment's sums; its O follows behind the next tile's scores
