@@ -344,6 +344,12 @@ __device__ __forceinline__ int64_t row_tiles(int32_t first, int32_t last) {
   return n > 0 ? n : 1;  // a row without tokens still has a result to write
 }
 
+// Quotients of what is nearly always short: the 64-bit division is a long routine.
+__device__ __forceinline__ long long div_of(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 }  // namespace
 
 template <int D, bool kE4m3, int N>
@@ -444,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       if (w < warp) before += warp_sum[w];
       total += warp_sum[w];
     }
-    begin = (total + gridDim.x - 1) / gridDim.x * blockIdx.x;
+    begin = div_of(total + gridDim.x - 1, gridDim.x) * blockIdx.x;
     if (begin < total && begin >= before && begin < before + mine) {
       long long at = before;
       for (int i = 0; i < per_thread; ++i) {
@@ -461,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       }
     }
   }
-  chunk = (total + gridDim.x - 1) / gridDim.x;
+  chunk = div_of(total + gridDim.x - 1, gridDim.x);
   begin = chunk * blockIdx.x;
   const long long work = begin < total ? min(chunk, total - begin) : 0;
   __syncthreads();
@@ -605,8 +611,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     long long idx = 0;  // tile of the row, over its kv heads
     if (work > 0 && p.token_ids) {
       const long long per_row = row_tiles(0, p.num_ids) * p.kv_heads;
-      row = static_cast<int>(begin / per_row);
-      idx = begin % per_row;
+      row = static_cast<int>(div_of(begin, per_row));
+      idx = begin - row * per_row;
     } else if (work > 0) {
       row = start_row;
       idx = start_idx;
@@ -632,13 +638,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         sg.last = __shfl_sync(0xffffffffu, last_l, row - base);
         const long long t = row_tiles(sg.first, sg.last);
         sg.row = row;
-        sg.kvh = static_cast<int>(idx / t);
-        sg.tile0 = static_cast<int>(idx % t);
+        sg.kvh = p.kv_heads == 1 ? 0 : static_cast<int>(div_of(idx, t));
+        sg.tile0 = static_cast<int>(idx - sg.kvh * t);
         const long long n = min(t - sg.tile0, left);
         sg.ntiles = static_cast<int>(n);
         const bool starts = sg.tile0 == 0, ends = sg.tile0 + n == t;
         sg.slot = starts && ends ? -1 : 2 * static_cast<int>(blockIdx.x) + (starts ? 1 : 0);
-        if (starts && !ends) info = make_int4(row, sg.kvh, static_cast<int>((t - n + chunk - 1) / chunk), 0);
+        if (starts && !ends) info = make_int4(row, sg.kvh, static_cast<int>(div_of(t - n + chunk - 1, chunk)), 0);
         left -= n;
         idx += n;
         if (idx == t * p.kv_heads) {
@@ -853,8 +859,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     // Write the result of segment w, whose O is final: normalised by inv_s, or as a partial.
     auto write_out = [&](const AttnSeg& w) {
       tc_fence_after();
-      constexpr int kStep = C == 16 || C == 32 ? 16 : 8;
-#pragma unroll
+      constexpr int kStep = !kE4m3 && C <= 32 && C >= 16 ? 16 : 8;
+#pragma unroll (kE4m3 || C > 32 ? 1 : 2)
       for (int c = 0; c < C; c += kStep) {
         if (c0 + c >= p.group) break;
         float o[kStep], o2[kStep];
