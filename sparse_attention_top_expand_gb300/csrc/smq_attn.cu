@@ -1,33 +1,55 @@
 // Attention of query rows over a paged key-value cache (sm_103a).
 //
-// For a (row, kv head) pair with G query heads and tiles of 128 tokens:
-//   S^T = K Q^T    one tcgen05.mma chain, M = 128 tokens, N = G heads (padded)
-//   P^T = 2^(S^T scale - m)
-//   O^T += V^T P^T one chain, M = head dim, N = G heads
-// with a running maximum m and sum l per head (one pass over the cache). The
+// For a (row, kv head) item with G query heads and tiles of 128 tokens:
+//   S   = K Q^T          one tcgen05.mma chain, M = 128 tokens, N = G heads (padded)
+//   P   = 2^(c S - m)    c = softmax scale * log2 e
+//   O^T += V^T P         one chain, M = head dim, N = heads
+// with a running maximum m and sum l per head: one pass over the cache. The
 // tokens are the M side, so any G from 1 to 128 fills the tensor core's rows,
 // one thread owns one token in the softmax (its mask and, for an E4M3 cache,
 // its scales are per-thread constants), and K and V tiles are read by the MMA
-// from the layout the cache has: K as a K-major and V as an M-major operand,
+// in the layout the cache has: K as a K-major and V as an M-major operand,
 // both 128-byte rows per token. m is raised only when a score exceeds it by
-// more than kTau (in log2), which keeps the rescale of O out of the common path:
-// P stays below 2^kTau, and sums in fp32 do not mind.
+// kTau (in log2), which keeps the rescale of O out of the common path; P stays
+// below 2^kTau, and sums in fp32 do not mind.
 //
-// The tiles of all (row, kv head) items form one list, cut into equal ranges,
-// one per CTA and SM. A range that starts or ends inside an item leaves an
-// unnormalised partial (O, m, l) in the workspace, and combine_kernel joins
-// the partials of an item in tile order, so results do not depend on timing.
+// Rounding. S, m, l and O are fp32. P goes to the tensor core in two numbers
+// of the cache's type, hi + lo, as one operand of 2 N columns with an
+// accumulator for each half, so V is read once for both. bf16: 16 bits
+// together (one bf16 alone moved results by up to 2^-9 of the weights and
+// measured 870 against 893 us on the selected chunk of its day: the second
+// number costs little). E4M3: kind::f8f6f4 wants both operands in 8 bits, so
+// the cache is never widened; P's two E4M3 numbers hold 9 bits, lo lifted by
+// 16 (undone at the end), so that what is lost of a small weight is below
+// 2^-18 of the largest; Q too is hi + lo (8 bits, what its bf16 has), two
+// chains into one accumulator. The token's key scale multiplies its scores; its value scale
+// joins P (as log2 in the exponent), and l adds P / value scale.
 //
-// E4M3 cache: kind::f8f6f4 wants both operands in 8 bits. Q and P are split in
-// two E4M3 numbers each (x = hi + lo, 8 significant bits together, as many as
-// bf16 has), and each chain runs twice into the same accumulators; the cache
-// itself is read in 8 bits and never widened. The token's key scale multiplies
-// its scores; its value scale joins P (as log2 in the exponent), and l adds
-// P / value scale.
+// Split. The tiles of all items form one list, cut into equal ranges, one per
+// CTA and SM, whatever the rows' lengths are. A range that starts or ends
+// inside an item leaves an unnormalised partial (O, m, l) in the workspace, and
+// combine_kernel joins the partials of an item in the order of the list, so
+// results do not depend on timing. Joining them in the attention kernel, by
+// the last CTAs to arrive, measured 31.4 against 26.5 us on 64 rows of 2048
+// selected tokens: the code it adds costs more than the second launch.
 //
 // Roles (512 threads): warps 0-3 copy K, V and Q tiles (cp.async), warp 4
-// schedules segments, warps 5 and 7 issue the MMAs, warp 6 looks up addresses,
-// warps 8-15 are two softmax groups of 128 threads, each with half of the heads.
+// cuts the work into segments, warps 5 and 7 issue the MMAs, warp 6 looks up
+// addresses, warps 8-15 are two softmax groups of 128 threads, each with half
+// of the heads. All roles run from one instruction cache: loops are kept short
+// and cold parts rolled (unrolled copies of the role loops cost 893 against
+// 648 us on the selected chunk).
+//
+// Bounds, measured (MEASURED: 6790 GB/s copy):
+//  - contexts of 4096 to 32768, 64 rows, 8 heads on each of 8 kv heads, bf16:
+//    707 us for 4.83 GB, 6830 GB/s: DRAM.
+//  - 4096 rows of 2048 selected tokens, 64 heads on one kv head, bf16: 605 us.
+//    Each tile's 64 KB come from L2 in 256-byte rows: 7.1 TB/s, where a kernel
+//    that only copies such rows into shared memory reaches 7.2 to 7.6.
+//  - the first batch with one kv head and an E4M3 cache: 94 us for 312 MB,
+//    3.3 TB/s: about 6500 warp instructions a tile, at half of the issue slots.
+//  - small calls: start-up (launch, three dependent loads to the first key, a
+//    tile's chain of copy, two products and softmax) and the join, 6 to 26 us.
 #include "smq_attn.cuh"
 #include "smq_kernels.cuh"
 #include "smq_ptx.cuh"
@@ -63,6 +85,9 @@ struct AttnSeg {
 };
 static_assert(sizeof(AttnSeg) == 32, "");
 
+// A kernel's shapes. N is the group of query heads rounded up to 16 (32 with an E4M3 cache, whose P rows would be
+// shorter than a swizzle), 32, 64 or 128. Shared memory holds kSlots tiles of K or V (16 or 32 KB each), Q, P and the
+// rings; what is left over after those goes to the tiles in flight.
 template <int D, bool kE4m3, int N>
 struct Shape {
   static constexpr int kRow = D * (kE4m3 ? 1 : 2);               // bytes per token
@@ -374,8 +399,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   uint64_t* const bars = reinterpret_cast<uint64_t*>(scratch + 8 * C);
   // barriers
   constexpr int kFull = 0, kEmpty = kFull + S::kSlots, kSFull = kEmpty + S::kSlots, kSEmpty = kSFull + 2, kPFull = kSEmpty + 2,
-                kPvDone = kPFull + 1, kQEmpty = kPvDone + 1, kQFull = kQEmpty + 2, kSegFull = kQFull + 2, kSegEmpty = kSegFull + kSegRing,
-                kAFull = kSegEmpty + kSegRing, kAEmpty = kAFull + kAddrRing, kDrain = kAEmpty + kAddrRing, kScFull = kDrain + 2, kBars = kScFull + (kE4m3 ? kAddrRing : 0);
+                kPvDone = kPFull + 1, kQEmpty = kPvDone + 1, kQFull = kQEmpty + 2, kSegFull = kQFull + 2,
+                kSegEmpty = kSegFull + kSegRing,
+                kAFull = kSegEmpty + kSegRing, kAEmpty = kAFull + kAddrRing, kDrain = kAEmpty + kAddrRing, kScFull = kDrain + 2,
+                kBars = kScFull + (kE4m3 ? kAddrRing : 0);
   static_assert(kBars * 8 <= 640, "");
   auto bar = [&](int i) { return smem_addr(bars + i); };
 
@@ -479,362 +506,362 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 
   // the softmax threads take registers that the others do not need: 256 x 72 + 256 x 184 = 512 x 128
   if (warp < 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-  if (warp < 4) {
-    // ------------------------------------------------------------ loaders
-    const int stall_tile = blockIdx.x == 0 ? p.stall_tile : -1;  // tests: its keys are not handed over
-    constexpr int kChunks = S::kRow / 16;         // 16-byte pieces of a token
-    constexpr int kTok = 32 / kChunks;            // tokens per warp instruction
-    const int piece = lane % kChunks, sub = lane / kChunks;
-    const uint32_t units_a = smem_addr(units);
-    bool ok = true;
-    auto wait = [&](int b, uint32_t parity) {
-      ok = wait_phase(bar(b), parity, abort, limit);
-      return ok;
-    };
-    // Units: K 0, V 0, K 1, V 1, ... The unit's barrier counts each thread's copies when they land; the MMA warps'
-    // proxy fence, after their wait, orders them before the tensor core's reads.
-    int slot = 0, seg = 0, left = 0, tile = 0;  // left: tiles of this segment
-    uint32_t turn = 1;                          // parity that says that the slot is free
-    for (bool values = false; ok; values = !values) {
-      if (!values) {
-        if (left == 0) {
-          if (!wait(kSegFull + seg % kSegRing, (seg / kSegRing) & 1)) break;
-          const AttnSeg sg = segs[seg % kSegRing];
-          left = sg.ntiles;
-          if (left == 0) break;
-          // the segment's queries: in bf16 its first K tile's barrier covers them, split in E4M3 they have one
-          const int qb = seg % S::kQBufs;
-          if (!wait(kQEmpty + qb, (seg / S::kQBufs + 1) & 1)) break;
-          const uint16_t* qrow = p.q + sg.row * p.q_stride + static_cast<int64_t>(sg.kvh) * p.group * D;
-          uint8_t* const qdst = q_s + qb * S::kQBytes;
-          if (!kE4m3) {
-            constexpr int kQChunks = D * 2 / 16, kQTok = 32 / kQChunks;
-            const int c = lane % kQChunks;
-            for (int i = warp * kQTok + lane / kQChunks; i < N; i += 4 * kQTok)
-              cp16(smem_addr(qdst) + (c >> 3) * (N * 128) + i * 128 + (((c & 7) ^ (i & 7)) << 4),
-                   qrow + (i < p.group ? i * D + c * 8 : 0), i < p.group ? 16 : 0);
-          } else {
-            // A head per D / 8 lanes, fetched with all loads in flight into the rows where it is then stored, as hi + lo
-            // times a power of two that brings its amax to (224, 448].
-            constexpr int kL = D / 8;
-            const int c = lane % kL, i0 = warp * (32 / kL) + lane / kL;
-            uint8_t* const piece_q = qdst + (c >> 3) * S::kQPart + (c & 7) * 16;
-            for (int i = i0; i < N; i += 4 * (32 / kL))
-              cp16(smem_addr(piece_q + i * 128), qrow + (i < p.group ? i * D + c * 8 : 0), i < p.group ? 16 : 0);
-            cp_wait_all();
-            __syncwarp();
-#pragma unroll 1
-            for (int i = i0; i < N; i += 4 * (32 / kL)) {
-              const uint4 w = *reinterpret_cast<const uint4*>(piece_q + i * 128);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp < 4) {
+      // ------------------------------------------------------------ loaders
+      const int stall_tile = blockIdx.x == 0 ? p.stall_tile : -1;  // tests: its keys are not handed over
+      constexpr int kChunks = S::kRow / 16;         // 16-byte pieces of a token
+      constexpr int kTok = 32 / kChunks;            // tokens per warp instruction
+      const int piece = lane % kChunks, sub = lane / kChunks;
+      const uint32_t units_a = smem_addr(units);
+      bool ok = true;
+      auto wait = [&](int b, uint32_t parity) {
+        ok = wait_phase(bar(b), parity, abort, limit);
+        return ok;
+      };
+      // Units: K 0, V 0, K 1, V 1, ... The unit's barrier counts each thread's copies when they land; the MMA warps'
+      // proxy fence, after their wait, orders them before the tensor core's reads.
+      int slot = 0, seg = 0, left = 0, tile = 0;  // left: tiles of this segment
+      uint32_t turn = 1;                          // parity that says that the slot is free
+      for (bool values = false; ok; values = !values) {
+        if (!values) {
+          if (left == 0) {
+            if (!wait(kSegFull + seg % kSegRing, (seg / kSegRing) & 1)) break;
+            const AttnSeg sg = segs[seg % kSegRing];
+            left = sg.ntiles;
+            if (left == 0) break;
+            // the segment's queries: in bf16 its first K tile's barrier covers them, split in E4M3 they have one
+            const int qb = seg % S::kQBufs;
+            if (!wait(kQEmpty + qb, (seg / S::kQBufs + 1) & 1)) break;
+            const uint16_t* qrow = p.q + sg.row * p.q_stride + static_cast<int64_t>(sg.kvh) * p.group * D;
+            uint8_t* const qdst = q_s + qb * S::kQBytes;
+            if (!kE4m3) {
+              constexpr int kQChunks = D * 2 / 16, kQTok = 32 / kQChunks;
+              const int c = lane % kQChunks;
+              for (int i = warp * kQTok + lane / kQChunks; i < N; i += 4 * kQTok)
+                cp16(smem_addr(qdst) + (c >> 3) * (N * 128) + i * 128 + (((c & 7) ^ (i & 7)) << 4),
+                     qrow + (i < p.group ? i * D + c * 8 : 0), i < p.group ? 16 : 0);
+            } else {
+              // A head per D / 8 lanes, fetched with all loads in flight into the rows where it is then stored, as hi + lo
+              // times a power of two that brings its amax to (224, 448].
+              constexpr int kL = D / 8;
+              const int c = lane % kL, i0 = warp * (32 / kL) + lane / kL;
+              uint8_t* const piece_q = qdst + (c >> 3) * S::kQPart + (c & 7) * 16;
+              for (int i = i0; i < N; i += 4 * (32 / kL))
+                cp16(smem_addr(piece_q + i * 128), qrow + (i < p.group ? i * D + c * 8 : 0), i < p.group ? 16 : 0);
+              cp_wait_all();
               __syncwarp();
-              const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-              float x[8], amax = 0.f;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                x[2 * k] = __uint_as_float(ws[k] << 16);
-                x[2 * k + 1] = __uint_as_float(ws[k] & 0xffff0000u);
-                amax = fmaxf(amax, fmaxf(fabsf(x[2 * k]), fabsf(x[2 * k + 1])));
-              }
-#pragma unroll
-              for (int o = kL / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-              // amax = f * 2^e with f in [1, 2): the factor 2^(7 - e), or 2^(8 - e) where f <= 1.75
-              const uint32_t bits = __float_as_uint(amax);
-              int e = static_cast<int>(bits >> 23) - 127;
-              e = e < -100 ? -100 : e;
-              const int up = 7 - e + ((bits & 0x7fffffu) <= 0x600000u ? 1 : 0);
-              const float mul = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
-              uint32_t hi[2], lo[2];
-#pragma unroll
-              for (int k = 0; k < 2; ++k)
-                split_e4m3x4<false>(x[4 * k] * mul, x[4 * k + 1] * mul, x[4 * k + 2] * mul, x[4 * k + 3] * mul, hi[k], lo[k]);
-              uint8_t* dst = qdst + i * 128 + (((c >> 1) ^ (i & 7)) << 4) + (c & 1) * 8;
-              *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
-              *reinterpret_cast<uint2*>(dst + S::kQPart) = make_uint2(lo[0], lo[1]);
-              if (c == 0) qscale_s[(seg % kQScales) * N + i] = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
-            }
-            mbar_arrive(bar(kQFull + qb));
-          }
-          __syncwarp();
-          arrive_one(bar(kSegEmpty + seg % kSegRing), lane);
-          ++seg;
-        }
-        if (!wait(kAFull + tile % kAddrRing, (tile / kAddrRing) & 1)) break;
-      }
-      if (!wait(kEmpty + slot, turn)) break;
-      const uint8_t* const base = static_cast<const uint8_t*>(values ? p.v_cache : p.k_cache) + piece * 16;
-      const uint32_t dst0 = units_a + slot * S::kUnit + (piece >> 3) * 16384;
-      const int64_t* const offs = ring_off + tile % kAddrRing * 128 + warp * 32 + sub;
-      constexpr int kBatch = 32 / kTok < 8 ? 32 / kTok : 8;  // addresses first, so that the copies issue back to back
-      const uint32_t dst1 = dst0 + (warp * 32 + sub) * 128;
-      const bool whole = ring_mask[tile % kAddrRing * 4 + warp] == 0xffffffffu;  // every token of the warp is there
-      if (__builtin_expect(whole, 1)) {
-#pragma unroll
-        for (int i0 = 0; i0 < 32 / kTok; i0 += kBatch) {
-          const uint8_t* src[kBatch];
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) src[i] = base + offs[(i0 + i) * kTok];
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i)
-            cp16(dst1 + (i0 + i) * kTok * 128 + (((piece & 7) ^ (((i0 + i) * kTok + sub) & 7)) << 4), src[i]);
-        }
-      } else {
 #pragma unroll 1
-        for (int i0 = 0; i0 < 32 / kTok; i0 += 4) {
-          int64_t o[4];
+              for (int i = i0; i < N; i += 4 * (32 / kL)) {
+                const uint4 w = *reinterpret_cast<const uint4*>(piece_q + i * 128);
+                __syncwarp();
+                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+                float x[8], amax = 0.f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[i] = offs[(i0 + i) * kTok];
+                for (int k = 0; k < 4; ++k) {
+                  x[2 * k] = __uint_as_float(ws[k] << 16);
+                  x[2 * k + 1] = __uint_as_float(ws[k] & 0xffff0000u);
+                  amax = fmaxf(amax, fmaxf(fabsf(x[2 * k]), fabsf(x[2 * k + 1])));
+                }
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            cp16(dst1 + (i0 + i) * kTok * 128 + (((piece & 7) ^ (((i0 + i) * kTok + sub) & 7)) << 4),
-                 base + (o[i] < 0 ? 0 : o[i]), o[i] < 0 ? 0 : 16);
-        }
-      }
-      if (values || stall_tile != tile) cp_arrive(bar(kFull + slot));
-      if (++slot == S::kSlots) {
-        slot = 0;
-        turn ^= 1;
-      }
-      if (values) {
-        __syncwarp();
-        arrive_one(bar(kAEmpty + tile % kAddrRing), lane);
-        ++tile;
-        --left;
-      }
-    }
-    if (!ok && lane == 0) fail();
-    cp_wait_all();
-  } else if (warp == 4) {
-    // ---------------------------------------------------------- scheduler
-    long long left = work;
-    int row = 0;
-    long long idx = 0;  // tile of the row, over its kv heads
-    if (work > 0 && p.token_ids) {
-      const long long per_row = row_tiles(0, p.num_ids) * p.kv_heads;
-      row = static_cast<int>(div_of(begin, per_row));
-      idx = begin - row * per_row;
-    } else if (work > 0) {
-      row = start_row;
-      idx = start_idx;
-    }
-    int4 info = make_int4(0, 0, 0, 0);
-    int base = -64, seg = 0;
-    int32_t first_l = 0, last_l = 0, table_l = 0;
-    bool ok = true;
-    while (ok) {
-      AttnSeg sg;
-      sg.ntiles = 0;
-      if (left > 0) {
-        if (row >= base + 32) {  // the next 32 rows' ranges, one per lane
-          base = row;
-          if (row + lane < p.rows) {
-            table_l = p.row_indices ? p.row_indices[row + lane] : row + lane;
-            if (table_l < 0 || table_l >= p.bt_rows) table_l = -1;
-            row_range(p, row + lane, false, first_l, last_l);
+                for (int o = kL / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                // amax = f * 2^e with f in [1, 2): the factor 2^(7 - e), or 2^(8 - e) where f <= 1.75
+                const uint32_t bits = __float_as_uint(amax);
+                int e = static_cast<int>(bits >> 23) - 127;
+                e = e < -100 ? -100 : e;
+                const int up = 7 - e + ((bits & 0x7fffffu) <= 0x600000u ? 1 : 0);
+                const float mul = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
+                uint32_t hi[2], lo[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                  split_e4m3x4<false>(x[4 * k] * mul, x[4 * k + 1] * mul, x[4 * k + 2] * mul, x[4 * k + 3] * mul, hi[k], lo[k]);
+                uint8_t* dst = qdst + i * 128 + (((c >> 1) ^ (i & 7)) << 4) + (c & 1) * 8;
+                *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
+                *reinterpret_cast<uint2*>(dst + S::kQPart) = make_uint2(lo[0], lo[1]);
+                if (c == 0) qscale_s[(seg % kQScales) * N + i] = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+              }
+              mbar_arrive(bar(kQFull + qb));
+            }
+            __syncwarp();
+            arrive_one(bar(kSegEmpty + seg % kSegRing), lane);
+            ++seg;
           }
+          if (!wait(kAFull + tile % kAddrRing, (tile / kAddrRing) & 1)) break;
         }
-        sg.table_row = __shfl_sync(0xffffffffu, table_l, row - base);
-        sg.first = __shfl_sync(0xffffffffu, first_l, row - base);
-        sg.last = __shfl_sync(0xffffffffu, last_l, row - base);
-        const long long t = row_tiles(sg.first, sg.last);
-        sg.row = row;
-        sg.kvh = p.kv_heads == 1 ? 0 : static_cast<int>(div_of(idx, t));
-        sg.tile0 = static_cast<int>(idx - sg.kvh * t);
-        const long long n = min(t - sg.tile0, left);
-        sg.ntiles = static_cast<int>(n);
-        const bool starts = sg.tile0 == 0, ends = sg.tile0 + n == t;
-        sg.slot = starts && ends ? -1 : 2 * static_cast<int>(blockIdx.x) + (starts ? 1 : 0);
-        if (starts && !ends) info = make_int4(row, sg.kvh, static_cast<int>(div_of(t - n + chunk - 1, chunk)), 0);
-        left -= n;
-        idx += n;
-        if (idx == t * p.kv_heads) {
-          ++row;
-          idx = 0;
-        }
-      }
-      if (seg >= kSegRing) ok = wait_phase(bar(kSegEmpty + seg % kSegRing), (seg / kSegRing - 1) & 1, abort, limit);
-      if (!ok) break;
-      if (lane == 0) {
-        segs[seg % kSegRing] = sg;
-        mbar_arrive(bar(kSegFull + seg % kSegRing));
-      }
-      ++seg;
-      if (sg.ntiles == 0) break;
-    }
-    if (lane == 0) {
-      if (!ok) fail();
-      p.seg_info[blockIdx.x] = info;
-    }
-  } else if (warp != 6) {
-    // ---------------------------------------------------------------- MMA
-    // Warp 5 issues S = K Q^T, warp 7 O += V^T P: apart, so that S runs ahead of the softmax. The whole warp runs
-    // the loop, so that descriptors stay in uniform registers, and one elected thread issues.
-    constexpr uint32_t kRowHi = desc_hi(128);
-    const bool scores = warp == 5;
-    bool ok = true;
-    auto wait = [&](int b, uint32_t parity) {
-      ok = wait_phase(bar(b), parity, abort, limit);
-      return ok;
-    };
-    int slot = scores ? 0 : 1, it = 0;  // the tile's unit: K tiles are the even ones, V tiles the odd ones
-    uint32_t turn = 0;
-    for (int seg = 0; ok; ++seg) {
-      if (!wait(kSegFull + seg % kSegRing, (seg / kSegRing) & 1)) break;
-      const int n = segs[seg % kSegRing].ntiles;
-      __syncwarp();
-      arrive_one(bar(kSegEmpty + seg % kSegRing), lane);
-      if (n == 0) break;
-      const int qb = seg % S::kQBufs;
-      if (kE4m3 && scores && !wait(kQFull + qb, (seg / S::kQBufs) & 1)) break;
-      for (int j = 0; j < n; ++j, ++it) {
-        // the softmax reads the tile's mask and scales behind S: they are there before S is issued
-        if (scores && !wait((kE4m3 ? kScFull : kAFull) + it % kAddrRing, (it / kAddrRing) & 1)) break;
-        if (!wait(kFull + slot, turn)) break;
-        if (!wait(scores ? kSEmpty + (it & 1) : kPFull, scores ? ((it >> 1) + 1) & 1 : it & 1)) break;
-        fence_proxy_async_smem();
-        tc_fence_after();
-        const uint32_t unit_a = smem_addr(units) + slot * S::kUnit;
-        if (scores) {
-          constexpr uint32_t kDesc = mma_idesc(kE4m3, false, N);
-          const uint32_t a = desc_lo(unit_a, 16), q = desc_lo(smem_addr(q_s) + qb * S::kQBytes, 16);
-          if (elect_one()) {
+        if (!wait(kEmpty + slot, turn)) break;
+        const uint8_t* const base = static_cast<const uint8_t*>(values ? p.v_cache : p.k_cache) + piece * 16;
+        const uint32_t dst0 = units_a + slot * S::kUnit + (piece >> 3) * 16384;
+        const int64_t* const offs = ring_off + tile % kAddrRing * 128 + warp * 32 + sub;
+        constexpr int kBatch = 32 / kTok < 8 ? 32 / kTok : 8;  // addresses first, so that the copies issue back to back
+        const uint32_t dst1 = dst0 + (warp * 32 + sub) * 128;
+        const bool whole = ring_mask[tile % kAddrRing * 4 + warp] == 0xffffffffu;  // every token of the warp is there
+        if (__builtin_expect(whole, 1)) {
 #pragma unroll
-            for (int part = 0; part < S::kQParts; ++part)
+          for (int i0 = 0; i0 < 32 / kTok; i0 += kBatch) {
+            const uint8_t* src[kBatch];
 #pragma unroll
-              for (int k = 0; k < S::kRow / 32; ++k)  // 32 bytes of K
-                mma<kE4m3>(tmem_sc + (it & 1) * N, a + (((k >> 2) * 16384 + (k & 3) * 32) >> 4), kRowHi,
-                           q + ((part * S::kQPart + (k >> 2) * (N * 128) + (k & 3) * 32) >> 4), kRowHi, kDesc,
-                           part + k > 0);
-            mma_commit(bar(kEmpty + slot));
-            mma_commit(bar(kSFull + (it & 1)));
-            if (j == n - 1) mma_commit(bar(kQEmpty + qb));
+            for (int i = 0; i < kBatch; ++i) src[i] = base + offs[(i0 + i) * kTok];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+              cp16(dst1 + (i0 + i) * kTok * 128 + (((piece & 7) ^ (((i0 + i) * kTok + sub) & 7)) << 4), src[i]);
           }
         } else {
-          constexpr uint32_t kDesc = mma_idesc(kE4m3, true, 2 * N);
-          constexpr int kStep = kE4m3 ? 32 : 16;  // tokens
-          const uint32_t a = desc_lo(unit_a, 16384), q = desc_lo(smem_addr(p_s), 128 * S::kPRow);
-          if (elect_one()) {
+#pragma unroll 1
+          for (int i0 = 0; i0 < 32 / kTok; i0 += 4) {
+            int64_t o[4];
 #pragma unroll
-            for (int k = 0; k < 128 / kStep; ++k)
-              mma<kE4m3>(tmem_o, a + ((k * kStep * 128) >> 4), kRowHi, q + ((k * kStep * S::kPRow) >> 4), desc_hi(S::kPRow),
-                         kDesc, j + k > 0);
-            mma_commit(bar(kEmpty + slot));
-            mma_commit(bar(kPvDone));
+            for (int i = 0; i < 4; ++i) o[i] = offs[(i0 + i) * kTok];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              cp16(dst1 + (i0 + i) * kTok * 128 + (((piece & 7) ^ (((i0 + i) * kTok + sub) & 7)) << 4),
+                   base + (o[i] < 0 ? 0 : o[i]), o[i] < 0 ? 0 : 16);
           }
         }
-        __syncwarp();
-        slot += 2;
-        if (slot >= S::kSlots) {
-          slot -= S::kSlots;
+        if (values || stall_tile != tile) cp_arrive(bar(kFull + slot));
+        if (++slot == S::kSlots) {
+          slot = 0;
           turn ^= 1;
         }
+        if (values) {
+          __syncwarp();
+          arrive_one(bar(kAEmpty + tile % kAddrRing), lane);
+          ++tile;
+          --left;
+        }
       }
-    }
-    if (!ok) {
-      if (lane == 0) fail();
-      // let the MMAs issued so far finish before TMEM is freed
-      const int drain = scores ? kDrain : kDrain + 1;
-      if (elect_one()) mma_commit(bar(drain));
-      const int never = 0;
-      wait_phase(bar(drain), 0, &never, limit);
-    }
-    __syncwarp();
-  } else {
-    // ---------------------------------------------------------- addresses
-    // One warp, four tokens a lane; the next tile's ids are on their way while this tile's pages are looked up.
-    const int shift = p.page_shift;
-    bool ok = true;
-    auto wait = [&](int b, uint32_t parity) {
-      ok = wait_phase(bar(b), parity, abort, limit);
-      return ok;
-    };
-    AttnSeg sg;
-    sg.ntiles = 0;
-    int seg = -1, j = 0;
-    int64_t ids_at = 0, head_at = 0;
-    const int32_t* table = nullptr;  // the row's block-table row, null if out of range
-    // the next tile of the work: its tokens' positions, -1 where there is none; false at the end
-    auto next_tile = [&](int32_t(&pos)[4]) {
-      if (++j >= sg.ntiles) {
+      if (!ok && lane == 0) fail();
+      cp_wait_all();
+    } else if (warp == 4) {
+      // ---------------------------------------------------------- scheduler
+      long long left = work;
+      int row = 0;
+      long long idx = 0;  // tile of the row, over its kv heads
+      if (work > 0 && p.token_ids) {
+        const long long per_row = row_tiles(0, p.num_ids) * p.kv_heads;
+        row = static_cast<int>(div_of(begin, per_row));
+        idx = begin - row * per_row;
+      } else if (work > 0) {
+        row = start_row;
+        idx = start_idx;
+      }
+      int4 info = make_int4(0, 0, 0, 0);
+      int base = -64, seg = 0;
+      int32_t first_l = 0, last_l = 0, table_l = 0;
+      bool ok = true;
+      while (ok) {
+        AttnSeg sg;
+        sg.ntiles = 0;
+        if (left > 0) {
+          if (row >= base + 32) {  // the next 32 rows' ranges, one per lane
+            base = row;
+            if (row + lane < p.rows) {
+              table_l = p.row_indices ? p.row_indices[row + lane] : row + lane;
+              if (table_l < 0 || table_l >= p.bt_rows) table_l = -1;
+              row_range(p, row + lane, false, first_l, last_l);
+            }
+          }
+          sg.table_row = __shfl_sync(0xffffffffu, table_l, row - base);
+          sg.first = __shfl_sync(0xffffffffu, first_l, row - base);
+          sg.last = __shfl_sync(0xffffffffu, last_l, row - base);
+          const long long t = row_tiles(sg.first, sg.last);
+          sg.row = row;
+          sg.kvh = p.kv_heads == 1 ? 0 : static_cast<int>(div_of(idx, t));
+          sg.tile0 = static_cast<int>(idx - sg.kvh * t);
+          const long long n = min(t - sg.tile0, left);
+          sg.ntiles = static_cast<int>(n);
+          const bool starts = sg.tile0 == 0, ends = sg.tile0 + n == t;
+          sg.slot = starts && ends ? -1 : 2 * static_cast<int>(blockIdx.x) + (starts ? 1 : 0);
+          if (starts && !ends) info = make_int4(row, sg.kvh, static_cast<int>(div_of(t - n + chunk - 1, chunk)), 0);
+          left -= n;
+          idx += n;
+          if (idx == t * p.kv_heads) {
+            ++row;
+            idx = 0;
+          }
+        }
+        if (seg >= kSegRing) ok = wait_phase(bar(kSegEmpty + seg % kSegRing), (seg / kSegRing - 1) & 1, abort, limit);
+        if (!ok) break;
+        if (lane == 0) {
+          segs[seg % kSegRing] = sg;
+          mbar_arrive(bar(kSegFull + seg % kSegRing));
+        }
         ++seg;
-        j = 0;
-        if (!wait(kSegFull + seg % kSegRing, (seg / kSegRing) & 1)) return false;
-        sg = segs[seg % kSegRing];
+        if (sg.ntiles == 0) break;
+      }
+      if (lane == 0) {
+        if (!ok) fail();
+        p.seg_info[blockIdx.x] = info;
+      }
+    } else if (warp != 6) {
+      // ---------------------------------------------------------------- MMA
+      // Warp 5 issues S = K Q^T, warp 7 O += V^T P: apart, so that S runs ahead of the softmax. The whole warp runs
+      // the loop, so that descriptors stay in uniform registers, and one elected thread issues.
+      constexpr uint32_t kRowHi = desc_hi(128);
+      const bool scores = warp == 5;
+      bool ok = true;
+      auto wait = [&](int b, uint32_t parity) {
+        ok = wait_phase(bar(b), parity, abort, limit);
+        return ok;
+      };
+      int slot = scores ? 0 : 1, it = 0;  // the tile's unit: K tiles are the even ones, V tiles the odd ones
+      uint32_t turn = 0;
+      for (int seg = 0; ok; ++seg) {
+        if (!wait(kSegFull + seg % kSegRing, (seg / kSegRing) & 1)) break;
+        const int n = segs[seg % kSegRing].ntiles;
         __syncwarp();
         arrive_one(bar(kSegEmpty + seg % kSegRing), lane);
-        if (sg.ntiles == 0) return false;
-        table = sg.table_row >= 0 ? p.block_table + static_cast<int64_t>(sg.table_row) * p.bt_stride : nullptr;
-        ids_at = static_cast<int64_t>(sg.row) * p.ids_ld;
-        head_at = static_cast<int64_t>(sg.kvh) * p.page_size;
-      }
+        if (n == 0) break;
+        const int qb = seg % S::kQBufs;
+        if (kE4m3 && scores && !wait(kQFull + qb, (seg / S::kQBufs) & 1)) break;
+        for (int j = 0; j < n; ++j, ++it) {
+          // the softmax reads the tile's mask and scales behind S: they are there before S is issued
+          if (scores && !wait((kE4m3 ? kScFull : kAFull) + it % kAddrRing, (it / kAddrRing) & 1)) break;
+          if (!wait(kFull + slot, turn)) break;
+          if (!wait(scores ? kSEmpty + (it & 1) : kPFull, scores ? ((it >> 1) + 1) & 1 : it & 1)) break;
+          fence_proxy_async_smem();
+          tc_fence_after();
+          const uint32_t unit_a = smem_addr(units) + slot * S::kUnit;
+          if (scores) {
+            constexpr uint32_t kDesc = mma_idesc(kE4m3, false, N);
+            const uint32_t a = desc_lo(unit_a, 16), q = desc_lo(smem_addr(q_s) + qb * S::kQBytes, 16);
+            if (elect_one()) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int64_t e = static_cast<int64_t>(sg.tile0 + j) * kAttnTile + k * 32 + lane;
-        pos[k] = -1;
-        if (p.token_ids) {
-          if (e < sg.last) pos[k] = p.token_ids[ids_at + e];
-        } else if (sg.first + e < sg.last) {
-          pos[k] = static_cast<int32_t>(sg.first + e);
-        }
-      }
-      return true;
-    };
-    int32_t ahead[4];
-    bool more = next_tile(ahead);
-    for (int it = 0; more; ++it) {
-      const int a = it % kAddrRing;
-      const int64_t head = head_at;
-      int32_t in_page[4], page[4];
-      bool asked[4];
+              for (int part = 0; part < S::kQParts; ++part)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        asked[k] = ahead[k] >= 0;
-        page[k] = -1;
-        in_page[k] = 0;
-        if (asked[k]) {
-          const int32_t col = shift >= 0 ? ahead[k] >> shift : ahead[k] / p.page_size;
-          in_page[k] = ahead[k] - col * p.page_size;
-          if (table && col < p.bt_stride) page[k] = table[col];
-        }
-      }
-      more = next_tile(ahead);
-      if (!ok || !wait(kAEmpty + a, (it / kAddrRing + 1) & 1)) break;
-      bool bad = false;
-      int64_t off[4];
+                for (int k = 0; k < S::kRow / 32; ++k)  // 32 bytes of K
+                  mma<kE4m3>(tmem_sc + (it & 1) * N, a + (((k >> 2) * 16384 + (k & 3) * 32) >> 4), kRowHi,
+                             q + ((part * S::kQPart + (k >> 2) * (N * 128) + (k & 3) * 32) >> 4), kRowHi, kDesc,
+                             part + k > 0);
+              mma_commit(bar(kEmpty + slot));
+              mma_commit(bar(kSFull + (it & 1)));
+              if (j == n - 1) mma_commit(bar(kQEmpty + qb));
+            }
+          } else {
+            constexpr uint32_t kDesc = mma_idesc(kE4m3, true, 2 * N);
+            constexpr int kStep = kE4m3 ? 32 : 16;  // tokens
+            const uint32_t a = desc_lo(unit_a, 16384), q = desc_lo(smem_addr(p_s), 128 * S::kPRow);
+            if (elect_one()) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        off[k] = -1;
-        float2* const scale = ring_scale + a * 128 + k * 32 + lane;
-        if (page[k] >= 0 && page[k] < p.num_pages) {
-          const int64_t vec = head + in_page[k];
-          off[k] = (page[k] * p.page_stride + vec * D) * (kE4m3 ? 1 : 2);
-          if (kE4m3) {
-            const int64_t at = page[k] * p.scale_page_stride + vec;
-            cp4(smem_addr(&scale->x), p.k_scales + at);
-            cp4(smem_addr(&scale->y), p.v_scales + at);
+              for (int k = 0; k < 128 / kStep; ++k)
+                mma<kE4m3>(tmem_o, a + ((k * kStep * 128) >> 4), kRowHi, q + ((k * kStep * S::kPRow) >> 4), desc_hi(S::kPRow),
+                           kDesc, j + k > 0);
+              mma_commit(bar(kEmpty + slot));
+              mma_commit(bar(kPvDone));
+            }
           }
-        } else {
-          if (kE4m3) *scale = make_float2(1.f, 1.f);
-          bad |= asked[k];
+          __syncwarp();
+          slot += 2;
+          if (slot >= S::kSlots) {
+            slot -= S::kSlots;
+            turn ^= 1;
+          }
         }
       }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        ring_off[a * 128 + k * 32 + lane] = off[k];
-        const uint32_t mask = __ballot_sync(0xffffffffu, off[k] >= 0);
-        if (lane == 0) ring_mask[a * 4 + k] = mask;
+      if (!ok) {
+        if (lane == 0) fail();
+        // let the MMAs issued so far finish before TMEM is freed
+        const int drain = scores ? kDrain : kDrain + 1;
+        if (elect_one()) mma_commit(bar(drain));
+        const int never = 0;
+        wait_phase(bar(drain), 0, &never, limit);
       }
-      if (kE4m3) {
-        cp_arrive(bar(kScFull + a));
-        mbar_arrive(bar(kScFull + a));
-      }
-      if (bad) atomicOr(p.status, kStatusBounds);
       __syncwarp();
-      arrive_one(bar(kAFull + a), lane);
+    } else {
+      // ---------------------------------------------------------- addresses
+      // One warp, four tokens a lane; the next tile's ids are on their way while this tile's pages are looked up.
+      const int shift = p.page_shift;
+      bool ok = true;
+      auto wait = [&](int b, uint32_t parity) {
+        ok = wait_phase(bar(b), parity, abort, limit);
+        return ok;
+      };
+      AttnSeg sg;
+      sg.ntiles = 0;
+      int seg = -1, j = 0;
+      int64_t ids_at = 0, head_at = 0;
+      const int32_t* table = nullptr;  // the row's block-table row, null if out of range
+      // the next tile of the work: its tokens' positions, -1 where there is none; false at the end
+      auto next_tile = [&](int32_t(&pos)[4]) {
+        if (++j >= sg.ntiles) {
+          ++seg;
+          j = 0;
+          if (!wait(kSegFull + seg % kSegRing, (seg / kSegRing) & 1)) return false;
+          sg = segs[seg % kSegRing];
+          __syncwarp();
+          arrive_one(bar(kSegEmpty + seg % kSegRing), lane);
+          if (sg.ntiles == 0) return false;
+          table = sg.table_row >= 0 ? p.block_table + static_cast<int64_t>(sg.table_row) * p.bt_stride : nullptr;
+          ids_at = static_cast<int64_t>(sg.row) * p.ids_ld;
+          head_at = static_cast<int64_t>(sg.kvh) * p.page_size;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int64_t e = static_cast<int64_t>(sg.tile0 + j) * kAttnTile + k * 32 + lane;
+          pos[k] = -1;
+          if (p.token_ids) {
+            if (e < sg.last) pos[k] = p.token_ids[ids_at + e];
+          } else if (sg.first + e < sg.last) {
+            pos[k] = static_cast<int32_t>(sg.first + e);
+          }
+        }
+        return true;
+      };
+      int32_t ahead[4];
+      bool more = next_tile(ahead);
+      for (int it = 0; more; ++it) {
+        const int a = it % kAddrRing;
+        const int64_t head = head_at;
+        int32_t in_page[4], page[4];
+        bool asked[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          asked[k] = ahead[k] >= 0;
+          page[k] = -1;
+          in_page[k] = 0;
+          if (asked[k]) {
+            const int32_t col = shift >= 0 ? ahead[k] >> shift : ahead[k] / p.page_size;
+            in_page[k] = ahead[k] - col * p.page_size;
+            if (table && col < p.bt_stride) page[k] = table[col];
+          }
+        }
+        more = next_tile(ahead);
+        if (!ok || !wait(kAEmpty + a, (it / kAddrRing + 1) & 1)) break;
+        bool bad = false;
+        int64_t off[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          off[k] = -1;
+          float2* const scale = ring_scale + a * 128 + k * 32 + lane;
+          if (page[k] >= 0 && page[k] < p.num_pages) {
+            const int64_t vec = head + in_page[k];
+            off[k] = (page[k] * p.page_stride + vec * D) * (kE4m3 ? 1 : 2);
+            if (kE4m3) {
+              const int64_t at = page[k] * p.scale_page_stride + vec;
+              cp4(smem_addr(&scale->x), p.k_scales + at);
+              cp4(smem_addr(&scale->y), p.v_scales + at);
+            }
+          } else {
+            if (kE4m3) *scale = make_float2(1.f, 1.f);
+            bad |= asked[k];
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          ring_off[a * 128 + k * 32 + lane] = off[k];
+          const uint32_t mask = __ballot_sync(0xffffffffu, off[k] >= 0);
+          if (lane == 0) ring_mask[a * 4 + k] = mask;
+        }
+        if (kE4m3) {
+          cp_arrive(bar(kScFull + a));
+          mbar_arrive(bar(kScFull + a));
+        }
+        if (bad) atomicOr(p.status, kStatusBounds);
+        __syncwarp();
+        arrive_one(bar(kAFull + a), lane);
+      }
+      if (!ok && lane == 0) fail();
+      cp_wait_all();
     }
-    if (!ok && lane == 0) fail();
-    cp_wait_all();
-  }
   } else {
     // ------------------------------------------------------------ softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
