@@ -98,8 +98,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     if (live) {
       const uint16_t* src = (is_q ? p.q + t * p.q_stride : is_v ? p.v + t * p.v_stride : p.k + t * p.k_stride) +
                             static_cast<int64_t>(head) * D;
-      a = *reinterpret_cast<const uint4*>(src + e0);
-      b = *reinterpret_cast<const uint4*>(src + e1);
+      a = __ldcs(reinterpret_cast<const uint4*>(src + e0));
+      b = __ldcs(reinterpret_cast<const uint4*>(src + e1));
     }
     const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
     float x[8], y[8];  // elements e0 .. e0 + 7 and e1 .. e1 + 7
