@@ -1107,21 +1107,21 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 
 // Join the partials of an item that CTA `first` of the attention kernel began
 // and others continued: out = sum_i w_i O_i / sum_i w_i l_i with
-// w_i = 2^(m_i - max m). blockIdx.x is that CTA, or, for few items, the item
-// (`by_item`: the block looks for the CTA, which keeps blocks without work few);
-// blockIdx.y picks heads_per_cta heads. With one head
-// the eight warps share the partials, with eight each warp has a head. Bound
-// by latency: the first partial outputs are loaded along with the maxima.
-template <int D>
-__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ AttnParams p, int ctas, int by_item,
-                                                      int heads_per_cta) {
-  constexpr int kPer = D / 32, kBatch = 8;
+// w_i = 2^(m_i - max m). Bound by latency, of its instructions too (a call runs
+// them once), so the two forms are compiled apart. kFew, for few items, whose
+// partials are many: a block per item and head, which looks for the item's
+// first CTA and shares the partials among its eight warps. Otherwise a block
+// per CTA and eight heads, a warp each. The first partial outputs are loaded
+// along with the maxima.
+template <int D, bool kFew>
+__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ AttnParams p, int ctas) {
+  constexpr int kPer = D / 32, kBatch = kFew ? 8 : 4;
   griddep_launch_dependents();
   griddep_wait();
-  __shared__ float acc_s[8][D], sum_s[8], max_s[8];
+  __shared__ float acc_s[kFew ? 8 : 1][D], sum_s[8], max_s[8];
   __shared__ int first_s;
   int first = blockIdx.x;
-  if (by_item) {
+  if (kFew) {
     if (threadIdx.x == 0) first_s = -1;
     __syncthreads();
     for (int c = threadIdx.x; c < ctas; c += 256) {
@@ -1136,9 +1136,9 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
   const int parts = info.z + 1;
   if (parts == 1) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int shares = heads_per_cta == 1 ? 8 : 1;  // warps per head
-  const int h = blockIdx.y * heads_per_cta + (shares == 1 ? warp : 0);
-  const int i0 = shares == 1 ? 0 : warp;
+  constexpr int shares = kFew ? 8 : 1;  // warps per head
+  const int h = kFew ? blockIdx.y : blockIdx.y * 8 + warp;
+  const int i0 = kFew ? warp : 0;
   const int n = h < p.group && i0 < parts ? (parts - i0 + shares - 1) / shares : 0;  // partials of this warp
   auto slot = [&](int k) {
     const int i = i0 + k * shares;
@@ -1147,11 +1147,13 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
   float m = kUnset, l = 0.f, acc[kPer];
 #pragma unroll
   for (int j = 0; j < kPer; ++j) acc[j] = 0.f;
+#pragma unroll 1
   for (int base = 0; base < n; base += 32) {
     const int count = min(32, n - base);
     float2 ml = make_float2(kUnset, 0.f);
     if (lane < count) ml = p.part_ml[slot(base + lane)];
     float w = 0.f;
+#pragma unroll 1
     for (int k0 = 0; k0 < count; k0 += kBatch) {
       using Vec = typename std::conditional<kPer == 4, float4, float2>::type;
       union {
@@ -1184,7 +1186,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
       }
     }
   }
-  if (shares > 1) {
+  if (kFew) {
 #pragma unroll
     for (int j = 0; j < kPer; ++j) acc_s[warp][lane * kPer + j] = acc[j];
     if (lane == 0) {
@@ -1277,11 +1279,11 @@ cudaError_t launch_attention(const AttnParams& p, bool e4m3, int grid, cudaStrea
   if (tiles == 1 || (p.token_ids && chunk % tiles == 0)) return cudaSuccess;
   // few items: an item has many partials, shared by a CTA per head
   const int64_t items = static_cast<int64_t>(p.rows) * p.kv_heads;
-  const int heads_per_cta = items * 4 >= grid ? 8 : 1;
-  const int by_item = heads_per_cta == 1;
-  return launch(p.head_dim == 128 ? combine_kernel<128> : combine_kernel<64>,
-                dim3(by_item ? static_cast<unsigned>(items) : grid, (p.group + heads_per_cta - 1) / heads_per_cta), 256, 0, stream, p, grid,
-                by_item, heads_per_cta);
+  if (items * 4 < grid)
+    return launch(p.head_dim == 128 ? combine_kernel<128, true> : combine_kernel<64, true>,
+                  dim3(static_cast<unsigned>(items), p.group), 256, 0, stream, p, grid);
+  return launch(p.head_dim == 128 ? combine_kernel<128, false> : combine_kernel<64, false>, dim3(grid, (p.group + 7) / 8), 256,
+                0, stream, p, grid);
 }
 
 }  // namespace smq
