@@ -416,34 +416,23 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   const uint64_t limit = static_cast<uint64_t>(p.wait_ns);
   griddep_launch_dependents();
 
+  if (tid < kBars) {  // a barrier a thread
+    const int i = tid;
+    const int count = i < kEmpty ? kLoaders                                   // K and V units: each loader thread's copies
+                      : i < kSEmpty ? 1                                       // freed by the MMAs; S
+                      : i < kPvDone ? kSoftmax / 32                           // S read, P written: each softmax warp
+                      : i < kQFull ? 1                                        // O; queries freed by the MMAs
+                      : i < kSegFull ? kLoaders                               // 8-bit queries
+                      : i < kSegEmpty ? 1 : i < kAFull ? kSegReaders          // segments
+                      : i < kAEmpty ? 1 : i < kDrain ? kAddrReaders           // addresses
+                      : i < kScFull ? 1 : 64;                                 // drains; scales: each lane's copies, and its stores
+    mbar_init(bar(i), count);
+  }
   if (tid == 0) {
-    for (int i = 0; i < S::kSlots; ++i) {
-      mbar_init(bar(kFull + i), kLoaders);
-      mbar_init(bar(kEmpty + i), 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(kSFull + i), 1);
-      mbar_init(bar(kSEmpty + i), kSoftmax / 32);
-      mbar_init(bar(kQEmpty + i), 1);
-      mbar_init(bar(kQFull + i), kLoaders);
-    }
-    mbar_init(bar(kPFull), kSoftmax / 32);
-    mbar_init(bar(kPvDone), 1);
-    for (int i = 0; i < kSegRing; ++i) {
-      mbar_init(bar(kSegFull + i), 1);
-      mbar_init(bar(kSegEmpty + i), kSegReaders);
-    }
-    for (int i = 0; i < kAddrRing; ++i) {
-      mbar_init(bar(kAFull + i), 1);
-      mbar_init(bar(kAEmpty + i), kAddrReaders);
-      if (kE4m3) mbar_init(bar(kScFull + i), 64);  // each lane's copies, and its stores
-    }
-    mbar_init(bar(kDrain), 1);
-    mbar_init(bar(kDrain + 1), 1);
-    mbar_init_fence();
     abort_flag = 0;
     start_row = -1;
   }
+  if (tid < kBars) mbar_init_fence();
   if (tid < N) nm_s[tid] = 0.f;
   if (warp == 5) tmem_alloc(smem_addr(&tmem_slot), S::kTmem);
   griddep_wait();
@@ -898,7 +887,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         pin<kStep>(o2);
         if (t >= D) continue;  // whole warps
         if (w.slot >= 0) {
-          float* const dst = p.part_o + (static_cast<int64_t>(w.slot) * p.group + c0 + c) * D + t;
+          float* const dst = p.part_o + (w.slot * p.group + c0 + c) * D + t;
 #pragma unroll
           for (int i = 0; i < kStep; ++i)
             if (c0 + c + i < p.group) dst[i * D] = o[i] + (kE4m3 ? o2[i] * (1.f / kLift) : o2[i]);
@@ -1085,13 +1074,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         const float sum = red[wt] + red[C + wt] + red[2 * C + wt] + red[3 * C + wt];
         const float m = fresh ? kUnset : -nm_s[h];
         nm_s[h] = 0.f;
-        inv_s[h] = sum == 0.f ? 0.f : 1.f / sum;
+        inv_s[h] = sum == 0.f ? 0.f : __fdividef(1.f, sum);
         if (h < p.group) {
           if (sg.slot >= 0)
-            p.part_ml[static_cast<int64_t>(sg.slot) * p.group + h] = make_float2(m, sum);
+            p.part_ml[sg.slot * p.group + h] = make_float2(m, sum);
           else if (p.lse)
             p.lse[static_cast<int64_t>(sg.row) * p.kv_heads * p.group + sg.kvh * p.group + h] =
-                (m + log2f(sum)) * 0.69314718055994531f;
+                (m + lg2(sum)) * 0.69314718055994531f;
         }
       }
       done = sg;
@@ -1142,7 +1131,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
   const int n = h < p.group && i0 < parts ? (parts - i0 + shares - 1) / shares : 0;  // partials of this warp
   auto slot = [&](int k) {
     const int i = i0 + k * shares;
-    return (static_cast<int64_t>(i == 0 ? 2 * first + 1 : 2 * (first + i)) * p.group + h);
+    return (i == 0 ? 2 * first + 1 : 2 * (first + i)) * p.group + h;  // below 2^20: two partials an SM, 128 heads
   };
   float m = kUnset, l = 0.f, acc[kPer];
 #pragma unroll
@@ -1208,12 +1197,12 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
     }
   }
   if (h >= p.group) return;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float inv = l == 0.f ? 0.f : __fdividef(1.f, l);
   const int64_t out_row = (static_cast<int64_t>(info.x) * p.kv_heads + info.y) * p.group + h;
 #pragma unroll
   for (int j = 0; j < kPer; j += 2)
     *reinterpret_cast<uint32_t*>(p.out + out_row * D + lane * kPer + j) = bf16x2(acc[j] * inv, acc[j + 1] * inv);
-  if (p.lse && lane == 0) p.lse[out_row] = (m + log2f(l)) * 0.69314718055994531f;
+  if (p.lse && lane == 0) p.lse[out_row] = (m + lg2(l)) * 0.69314718055994531f;
 }
 
 namespace {
