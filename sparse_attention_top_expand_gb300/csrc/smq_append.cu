@@ -9,7 +9,11 @@
 // row is read once per warp, not once per head.
 //
 // The kernel moves bytes only (about 3 operations for every 4 bytes), so it is
-// bound by DRAM for a chunk and by launch and load latency for a step.
+// bound by DRAM for a chunk and by launch and load latency for a step: 4096
+// tokens of 64 + 16 heads of 128 in bf16 take 32.6 us, 5.2 TB/s; 4093 tokens of
+// 32 + 8 heads of 64 into an E4M3 cache 9.6 us (10.9 before the loads streamed;
+// 14.5 with the next pass loaded ahead); 64 tokens 3.7 us; one token's call is
+// the host's launch, 2.8 us.
 // Rounding: products and sums round to fp32 one by one (no fused
 // multiply-add), so a result does not depend on how the compiler contracts
 // them; then once to bf16, or to E4M3 with scale amax / 448.
@@ -176,7 +180,9 @@ cudaError_t launch_append(const AppendParams& p, int head_dim, bool e4m3, int nu
   const int per_pass = 32 / (head_dim / 16);
   const int passes = ((p.q ? p.heads : 0) + 2 * p.kv_heads + per_pass - 1) / per_pass;
   // A warp keeps the token's table row over its passes; with too few tokens to
-  // fill the SMs the passes are spread over more warps instead.
+  // fill the SMs the passes are spread over more warps instead, up to 16 warps
+  // an SM (48 measured 31.6 against 32.3 us on the bf16 chunk, but 13.0 against
+  // 10.9 on the 8-bit one).
   int64_t parts = (static_cast<int64_t>(num_sms) * 16 + p.rows - 1) / p.rows;
   parts = parts < 1 ? 1 : parts > passes ? passes : parts;
   const int64_t warps = static_cast<int64_t>(p.rows) * parts;

@@ -42,14 +42,14 @@
 //
 // Bounds, measured (MEASURED: 6790 GB/s copy):
 //  - contexts of 4096 to 32768, 64 rows, 8 heads on each of 8 kv heads, bf16:
-//    707 us for 4.83 GB, 6830 GB/s: DRAM.
-//  - 4096 rows of 2048 selected tokens, 64 heads on one kv head, bf16: 605 us.
+//    700 us for 4.83 GB, 6900 GB/s: DRAM.
+//  - 4096 rows of 2048 selected tokens, 64 heads on one kv head, bf16: 603 us.
 //    Each tile's 64 KB come from L2 in 256-byte rows: 7.1 TB/s, where a kernel
 //    that only copies such rows into shared memory reaches 7.2 to 7.6.
-//  - the first batch with one kv head and an E4M3 cache: 94 us for 312 MB,
+//  - the first batch with one kv head and an E4M3 cache: 95 us for 314 MB,
 //    3.3 TB/s: about 6500 warp instructions a tile, at half of the issue slots.
 //  - small calls: start-up (launch, three dependent loads to the first key, a
-//    tile's chain of copy, two products and softmax) and the join, 6 to 26 us.
+//    tile's chain of copy, two products and softmax) and the join, 6 to 25 us.
 #include "smq_attn.cuh"
 #include "smq_kernels.cuh"
 #include "smq_ptx.cuh"
@@ -1253,6 +1253,11 @@ cudaError_t with_kernel(int head_dim, bool e4m3, int group, F f) {
 
 cudaError_t prepare_attention(int head_dim, bool e4m3, int group) {
   return with_kernel(head_dim, e4m3, group, [](auto kernel, size_t smem) {
+    // the register split waits for ever on a launch with fewer registers than it hands out
+    cudaFuncAttributes a;
+    const cudaError_t rc = cudaFuncGetAttributes(&a, kernel);
+    if (rc != cudaSuccess) return rc;
+    if (a.numRegs != 128) return cudaErrorInvalidKernelImage;
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   });
 }
