@@ -42,11 +42,11 @@
 //
 // Bounds, measured (MEASURED: 6790 GB/s copy):
 //  - contexts of 4096 to 32768, 64 rows, 8 heads on each of 8 kv heads, bf16:
-//    700 us for 4.83 GB, 6900 GB/s: DRAM.
-//  - 4096 rows of 2048 selected tokens, 64 heads on one kv head, bf16: 603 us.
-//    Each tile's 64 KB come from L2 in 256-byte rows: 7.1 TB/s, where a kernel
+//    700 to 708 us for 4.83 GB, 6.8 to 6.9 TB/s: DRAM.
+//  - 4096 rows of 2048 selected tokens, 64 heads on one kv head, bf16: 587 us.
+//    Each tile's 64 KB come from L2 in 256-byte rows: 7.3 TB/s, where a kernel
 //    that only copies such rows into shared memory reaches 7.2 to 7.6.
-//  - the first batch with one kv head and an E4M3 cache: 95 us for 314 MB,
+//  - the first batch with one kv head and an E4M3 cache: 96 us for 314 MB,
 //    3.3 TB/s: about 6500 warp instructions a tile, at half of the issue slots.
 //  - small calls: start-up (launch, three dependent loads to the first key, a
 //    tile's chain of copy, two products and softmax) and the join, 6 to 25 us.
@@ -932,54 +932,52 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       bool fresh = true;  // no token so far
       for (int j = 0; j < sg.ntiles; ++j, ++it) {
         const int a = it % kAddrRing;
-        if (!s_ready) wait(kSFull + (it & 1), (it >> 1) & 1);
+        if (__builtin_expect(!s_ready, 0)) wait(kSFull + (it & 1), (it >> 1) & 1);
         float s[C];  // scores, less the running maxima, then P
-        bool over = failed, first = false;
+        bool over = failed;
         float inv_vs = 1.f;
-        if (!failed) {
-          tc_fence_after();
-          const uint32_t s_col = tmem_sc + lanes + (it & 1) * N + c0;
-          constexpr int kLd = C > 32 ? 32 : C;
+        tc_fence_after();  // (after a failed wait the scores are of no use, and do no harm)
+        const uint32_t s_col = tmem_sc + lanes + (it & 1) * N + c0;
+        constexpr int kLd = C > 32 ? 32 : C;
 #pragma unroll
-          for (int c = 0; c < C; c += kLd) tmem_ld<kLd>(s_col + c, s + c);
-          float mul = p.scale_log2, add = 0.f;
-          const uint4 mask = *reinterpret_cast<const uint4*>(ring_mask + a * 4);
-          const bool valid = ((quarter == 0 ? mask.x : quarter == 1 ? mask.y : quarter == 2 ? mask.z : mask.w) >> lane) & 1;
-          first = fresh && (mask.x | mask.y | mask.z | mask.w) != 0;
-          if (kE4m3) {
-            const float2 sc = ring_scale[a * 128 + t];
-            mul *= sc.x;
-            add = lg2(sc.y);
-            inv_vs = __fdividef(1.f, sc.y);
-          }
-          tmem_wait_ld();
-          pin<C>(s);
-          tc_fence_before();
-          __syncwarp();
-          arrive_one(bar(kSEmpty + (it & 1)), lane);
-          arrive_one(bar(kAEmpty + a), lane);
-          float most = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < C; c += 4) {
-            float4 a4 = *reinterpret_cast<const float4*>(nm_s + c0 + c), f4 = make_float4(mul, mul, mul, mul);
-            if (kE4m3) {
-              const float4 q4 = *reinterpret_cast<const float4*>(qscale + c);
-              mul2(f4.x, f4.y, q4.x, q4.y);
-              mul2(f4.z, f4.w, q4.z, q4.w);
-              add2(a4.x, a4.y, add, add);
-              add2(a4.z, a4.w, add, add);
-            }
-            fma2(s[c], s[c + 1], f4.x, f4.y, a4.x, a4.y);
-            fma2(s[c + 2], s[c + 3], f4.z, f4.w, a4.z, a4.w);
-            most = fmaxf(fmaxf(most, fmaxf(s[c], s[c + 1])), fmaxf(s[c + 2], s[c + 3]));
-          }
-          if (!valid) {
-#pragma unroll
-            for (int c = 0; c < C; ++c) s[c] = -INFINITY;
-            most = -INFINITY;
-          }
-          over = most > S::kTau || first;
+        for (int c = 0; c < C; c += kLd) tmem_ld<kLd>(s_col + c, s + c);
+        float mul = p.scale_log2, add = 0.f;
+        const uint4 mask = *reinterpret_cast<const uint4*>(ring_mask + a * 4);
+        const bool valid = ((quarter == 0 ? mask.x : quarter == 1 ? mask.y : quarter == 2 ? mask.z : mask.w) >> lane) & 1;
+        const bool first = fresh && (mask.x | mask.y | mask.z | mask.w) != 0;
+        if (kE4m3) {
+          const float2 sc = ring_scale[a * 128 + t];
+          mul *= sc.x;
+          add = lg2(sc.y);
+          inv_vs = __fdividef(1.f, sc.y);
         }
+        tmem_wait_ld();
+        pin<C>(s);
+        tc_fence_before();
+        __syncwarp();
+        arrive_one(bar(kSEmpty + (it & 1)), lane);
+        arrive_one(bar(kAEmpty + a), lane);
+        float most = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < C; c += 4) {
+          float4 a4 = *reinterpret_cast<const float4*>(nm_s + c0 + c), f4 = make_float4(mul, mul, mul, mul);
+          if (kE4m3) {
+            const float4 q4 = *reinterpret_cast<const float4*>(qscale + c);
+            mul2(f4.x, f4.y, q4.x, q4.y);
+            mul2(f4.z, f4.w, q4.z, q4.w);
+            add2(a4.x, a4.y, add, add);
+            add2(a4.z, a4.w, add, add);
+          }
+          fma2(s[c], s[c + 1], f4.x, f4.y, a4.x, a4.y);
+          fma2(s[c + 2], s[c + 3], f4.z, f4.w, a4.z, a4.w);
+          most = fmaxf(fmaxf(most, fmaxf(s[c], s[c + 1])), fmaxf(s[c + 2], s[c + 3]));
+        }
+        if (!valid) {
+#pragma unroll
+          for (int c = 0; c < C; ++c) s[c] = -INFINITY;
+          most = -INFINITY;
+        }
+        over |= most > S::kTau || first;
         const bool raise = bar_or(bar_id, 128, over);
         // asked early, as an answer takes its time behind the copies in the load-store queue
         const bool pv_ready = it == 0 || __all_sync(0xffffffffu, mbar_test_wait(bar(kPvDone), (it - 1) & 1));
@@ -1034,9 +1032,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 #pragma unroll
         for (int i = 0; i < kWords; ++i) asm volatile("" : "+r"(hi[i]), "+r"(lo[i]));
         s_ready = __all_sync(0xffffffffu, mbar_test_wait(bar(kSFull + ((it + 1) & 1)), ((it + 1) >> 1) & 1));
-        if (!pv_ready) wait(kPvDone, (it - 1) & 1);  // O is final up to the previous tile, and P is free
-        if (j == 0 && done.ntiles > 0) write_out(done);
-        if (raise && j > 0) {
+        if (__builtin_expect(!pv_ready, 0)) wait(kPvDone, (it - 1) & 1);  // O is final up to the previous tile, and P is free
+        if (__builtin_expect(j == 0 && done.ntiles > 0, 0)) write_out(done);
+        if (__builtin_expect(raise && j > 0, 0)) {
           tc_fence_after();
 #pragma unroll
           for (int part = 0; part < 2; ++part)
