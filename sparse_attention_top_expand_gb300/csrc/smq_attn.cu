@@ -40,7 +40,7 @@
 // and cold parts rolled (unrolled copies of the role loops cost 893 against
 // 648 us on the selected chunk).
 //
-// Bounds, measured (MEASURED: 6790 GB/s copy):
+// Bounds (a plain copy reaches 6790 GB/s):
 //  - contexts of 4096 to 32768, 64 rows, 8 heads on each of 8 kv heads, bf16:
 //    700 to 708 us for 4.83 GB, 6.8 to 6.9 TB/s: DRAM.
 //  - 4096 rows of 2048 selected tokens, 64 heads on one kv head, bf16: 587 us.
