@@ -746,13 +746,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           }
         }
       }
-      if (!ok) {
-        if (lane == 0) fail();
-        // let the MMAs issued so far finish before TMEM is freed
+      if (!ok && lane == 0) fail();
+      // The MMAs issued so far read shared memory and write TMEM, which a softmax whose waits ran out would free under
+      // them: they end by themselves, so this wait has a limit of its own and not the plan's.
+      if (it > 0) {
         const int drain = scores ? kDrain : kDrain + 1;
         if (elect_one()) mma_commit(bar(drain));
         const int never = 0;
-        wait_phase(bar(drain), 0, &never, limit);
+        wait_phase(bar(drain), 0, &never, 2000000000ull);
       }
       __syncwarp();
     } else {
