@@ -13,17 +13,21 @@
 // kTau (in log2), which keeps the rescale of O out of the common path; P stays
 // below 2^kTau, and sums in fp32 do not mind.
 //
-// Rounding. S, m, l and O are fp32. P goes to the tensor core in two numbers
-// of the cache's type, hi + lo, as one operand of 2 N columns with an
-// accumulator for each half, so V is read once for both. bf16: 16 bits
-// together (one bf16 alone moved results by up to 2^-9 of the weights and
-// measured 870 against 893 us on the selected chunk of its day: the second
-// number costs little). E4M3: kind::f8f6f4 wants both operands in 8 bits, so
-// the cache is never widened; P's two E4M3 numbers hold 9 bits, lo lifted by
-// 16 (undone at the end), so that what is lost of a small weight is below
-// 2^-18 of the largest; Q too is hi + lo (8 bits, what its bf16 has), two
-// chains into one accumulator. The token's key scale multiplies its scores; its value scale
-// joins P (as log2 in the exponent), and l adds P / value scale.
+// Rounding. Queries, keys and values go to the tensor core as the cache and the
+// caller hold them: bf16, and E4M3 codes widened to bf16, which is exact. S, m,
+// l and O are fp32. P goes to the tensor core in two bf16 numbers, hi + lo (16
+// bits), as one operand of 2 N columns with an accumulator for each half, so V
+// is read once for both. One bf16 alone moved results by up to 2^-9 of the
+// weights and measured 870 against 893 us on the selected chunk of its day: the
+// second number costs little. Over an E4M3 cache the token's key scale
+// multiplies its scores, and its value scale multiplies P after l has taken it:
+// m follows the scores alone, and a bf16 has the exponents of fp32, so neither
+// a token of zeros nor one of large values costs the others' weights any bits.
+// (kind::f8f6f4 reads the codes as they are, but wants P and Q in 8 bits too.
+// Two E4M3 numbers for each lost what was below 2^-18 of the largest weight
+// times scale: a token of zero values, whose scale is 1, beside values of 1
+// then took 10 to 60 % of the result. It measured 97 against 127 us on 64 rows
+// of 4096 to 32768 tokens, and 60 against 69 us on 256 rows of 2048 selected.)
 //
 // Split. The tiles of all items form one list, cut into equal ranges, one per
 // CTA and SM, whatever the rows' lengths are. A range that starts or ends
@@ -33,12 +37,14 @@
 // the last CTAs to arrive, measured 31.4 against 26.5 us on 64 rows of 2048
 // selected tokens: the code it adds costs more than the second launch.
 //
-// Roles (512 threads): warps 0-3 copy K, V and Q tiles (cp.async), warp 4
-// cuts the work into segments, warps 5 and 7 issue the MMAs, warp 6 looks up
-// addresses, warps 8-15 are two softmax groups of 128 threads, each with half
-// of the heads. All roles run from one instruction cache: loops are kept short
-// and cold parts rolled (unrolled copies of the role loops cost 893 against
-// 648 us on the selected chunk).
+// Roles: warps 0-3 copy K, V and Q tiles (cp.async), warp 4 cuts the work into
+// segments, warps 5 and 7 issue the MMAs, warp 6 looks up addresses, warps 8-15
+// are two softmax groups of 128 threads, each with half of the heads. Over an
+// E4M3 cache warps 0-3 copy and widen keys and warps 16-19 values. All roles
+// run from one instruction cache: loops are kept short and cold parts rolled
+// (unrolled copies of the role loops cost 893 against 648 us on the selected
+// chunk; widening four pieces at a time instead of two 667 against 653 us on a
+// batch of 8-bit contexts).
 //
 // Bounds (a plain copy reaches 6790 GB/s):
 //  - contexts of 4096 to 32768, 64 rows, 8 heads on each of 8 kv heads, bf16:
@@ -46,8 +52,11 @@
 //  - 4096 rows of 2048 selected tokens, 64 heads on one kv head, bf16: 587 us.
 //    Each tile's 64 KB come from L2 in 256-byte rows: 7.3 TB/s, where a kernel
 //    that only copies such rows into shared memory reaches 7.2 to 7.6.
-//  - the first batch with one kv head and an E4M3 cache: 96 us for 314 MB,
-//    3.3 TB/s: about 6500 warp instructions a tile, at half of the issue slots.
+//  - 64 rows of such contexts, E4M3, 64 heads on one kv head: 127 us for 314 MB,
+//    2.5 TB/s; with 64 heads on 8 kv heads 653 us for 2.5 GB. A tile costs some
+//    7300 warp instructions at half of the issue slots and 128 KB of
+//    shared-memory traffic for the widening alone; without any loading or
+//    widening the rest of the first would still take 116 us, of the second 500.
 //  - small calls: start-up (launch, three dependent loads to the first key, a
 //    tile's chain of copy, two products and softmax) and the join, 6 to 25 us.
 #include "smq_attn.cuh"
@@ -62,16 +71,9 @@ namespace smq {
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kLoaders = 128;
+constexpr int kLoaders = 128;   // threads; over an E4M3 cache as many again, a group for keys and one for values
 constexpr int kSoftmax = 256;
-constexpr int kAddrRing = 8;    // tiles whose addresses, masks and scales may be ahead of the softmax
 constexpr int kSegRing = 8;     // segments published ahead
-// Query scales of E4M3 segments: the loader is at most four segments ahead of the softmax (its
-// buffers free with the MMA, the MMA runs up to two tiles ahead), so eight sets never collide.
-constexpr int kQScales = 8;
-constexpr int kSegReaders = 4 + 2 + 1 + 8;   // loader, MMA, address and softmax warps
-constexpr int kAddrReaders = 4 + 8;          // loader and softmax warps
 constexpr float kUnset = -3.0e38f;           // the running maximum of a partial without tokens
 constexpr int kSmemLimit = 232448 - 1024;  // less the static part
 
@@ -85,36 +87,47 @@ struct AttnSeg {
 };
 static_assert(sizeof(AttnSeg) == 32, "");
 
-// A kernel's shapes. N is the group of query heads rounded up to 16 (32 with an E4M3 cache, whose P rows would be
-// shorter than a swizzle), 32, 64 or 128. Shared memory holds kSlots tiles of K or V (16 or 32 KB each), Q, P and the
+// A kernel's shapes. N is the group of query heads rounded up to 16, 32, 64 or 128. Shared memory holds kSlots tiles of
+// K or V as the tensor core reads them (16 or 32 KB each), over an E4M3 cache kRaws tiles of codes of each side, Q, P and the
 // rings; what is left over after those goes to the tiles in flight.
 template <int D, bool kE4m3, int N>
 struct Shape {
-  static constexpr int kRow = D * (kE4m3 ? 1 : 2);               // bytes per token
+  static constexpr int kRow = 2 * D;                             // bytes per token, in bf16
   static constexpr int kBlocks = kRow > 128 ? 2 : 1;             // 128-byte columns
   static constexpr int kUnit = kBlocks * 128 * 128;              // bytes of a K or V tile
-  static constexpr int kQParts = kE4m3 ? 2 : 1;                  // hi and lo of Q
-  static constexpr int kQPart = kBlocks * N * 128;
-  static constexpr int kQBytes = kQParts * kQPart;
+  static constexpr int kRaw = kE4m3 ? 128 * D : 0;               // bytes of its codes
+  static constexpr int kQBytes = kBlocks * N * 128;
   static constexpr int kQBufs = N >= 64 ? 1 : 2;
-  static constexpr int kPRow = N * (kE4m3 ? 1 : 2) > 128 ? 128 : N * (kE4m3 ? 1 : 2);  // bytes of a P row in a block
-  static constexpr int kPPart = 128 * N * (kE4m3 ? 1 : 2);
+  static constexpr int kPRow = N * 2 > 128 ? 128 : N * 2;        // bytes of a P row in a block
+  static constexpr int kPPart = 128 * N * 2;
   static constexpr int kPBytes = 2 * kPPart;                     // hi and lo of P
   static constexpr int kCols = N / 2;                            // heads per softmax thread
-  static constexpr int kRingBytes = kAddrRing * 128 * (8 + (kE4m3 ? 8 : 0));
-  static constexpr int kMisc = kRingBytes + kAddrRing * 16 + kSegRing * 32 + 640 /*barriers*/ + N * 16 /*m, alpha, raise, 1 / l*/ +
-                               (kE4m3 ? kQScales * N * 4 : 0) + 8 * kCols * 4 /*scratch*/ + 64;
+  static constexpr int kThreads = kE4m3 ? 640 : 512;
+  // registers of a thread: at launch all of an SM's, then most for the 256 softmax threads (of the widest group, which
+  // hold twice the heads: 168 against 152 measured 173 and 230 us on 64 rows of 128 heads on one 8-bit kv head)
+  static constexpr int kRegs = kE4m3 ? 96 : 128;
+  static constexpr int kSoftmaxRegs = !kE4m3 ? 184 : N == 128 ? 168 : 152;
+  static constexpr int kOtherRegs = !kE4m3 ? 72 : N == 128 ? 48 : 56;
+  static_assert(kSoftmax * kSoftmaxRegs + (kThreads - kSoftmax) * kOtherRegs <= kThreads * kRegs, "");
+  static constexpr int kAddrReaders = (kE4m3 ? 8 : 4) + 8;       // loader and softmax warps
+  static constexpr int kSegReaders = kAddrReaders + 2 + 1;       // and MMA and address warps
+  static constexpr int kRing = 8;                                // tiles whose addresses, masks and scales may be ahead of the softmax
+  static constexpr int kRingBytes = kRing * 128 * (8 + (kE4m3 ? 8 : 0));
+  static constexpr int kMisc = kRingBytes + kRing * 16 + kSegRing * 32 + 640 /*barriers*/ + N * 16 /*m, alpha, raise, 1 / l*/ +
+                               8 * kCols * 4 /*scratch*/ + 64;
   static constexpr int kFixed = kQBufs * kQBytes + kPBytes + kMisc;
-  static constexpr int kFit = (kSmemLimit - kFixed) / kUnit;
+  static constexpr int kFree = kSmemLimit - kFixed;
+  // over an E4M3 cache one or two units of each side, so that what is left over goes to the copies ahead
+  static constexpr int kFit = kE4m3 ? (kFree >= 4 * kUnit + 4 * kRaw ? 4 : 2) : kFree / kUnit;
   static constexpr int kSlots = kFit > 12 ? 12 : kFit;
-  static constexpr int kSmem = kSlots * kUnit + kFixed;
+  static constexpr int kRawFit = kE4m3 ? (kFree - kSlots * kUnit) / (kE4m3 ? 2 * kRaw : 1) : 0;
+  static constexpr int kRaws = kRawFit > 4 ? 4 : kRawFit;        // of each side
+  static constexpr int kSmem = kSlots * kUnit + 2 * kRaws * kRaw + kFixed;
   static constexpr int kTmem = 4 * N;                            // O from hi and from lo, two buffers of S
-  static constexpr float kTop = kE4m3 ? 4.f : 0.f;               // log2 of P at the maximum
-  static constexpr float kTau = kE4m3 ? 8.8f : 8.f;              // log2 of the largest P: 2^8.8 < 448
-  static_assert(kSlots >= 3 && kSmem <= kSmemLimit, "");
-  static_assert(!kE4m3 || N >= 32, "");
-  static_assert(kBlocks == 2 || kFixed >= 16384, "an M = 128 operand of a 64-wide bf16 head reads past its unit");
+  static_assert((kE4m3 ? kSlots % 2 == 0 && kRaws >= 1 : kSlots >= 3) && kSmem <= kSmemLimit, "");
+  static_assert(kBlocks == 2 || kFixed >= 16384, "an M = 128 operand of a 64-wide head reads past its unit");
 };
+constexpr float kTau = 8.f;  // log2 of the largest P
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -133,13 +146,6 @@ __device__ __forceinline__ void fma2(float& x0, float& x1, float f0, float f1, f
       " fma.rn.f32x2 x, x, f, a;\n mov.b64 {%0, %1}, x;\n}"
       : "+f"(x0), "+f"(x1)
       : "f"(f0), "f"(f1), "f"(a0), "f"(a1));
-}
-// a += x * f
-__device__ __forceinline__ void fma2acc(float& a0, float& a1, float x0, float x1, float f) {
-  asm("{\n .reg .b64 x, f, a;\n mov.b64 x, {%2, %3};\n mov.b64 f, {%4, %4};\n mov.b64 a, {%0, %1};\n"
-      " fma.rn.f32x2 a, x, f, a;\n mov.b64 {%0, %1}, a;\n}"
-      : "+f"(a0), "+f"(a1)
-      : "f"(x0), "f"(x1), "f"(f));
 }
 __device__ __forceinline__ void mul2(float& x0, float& x1, float y0, float y1) {
   asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
@@ -179,6 +185,11 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
 }
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void cp_wait() {  // all but the newest kLeft groups
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 __device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // 4-byte asynchronous copy.
@@ -258,29 +269,20 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-// Instruction descriptor: fp32 accumulation; kind::f16 with bf16 operands or
-// kind::f8f6f4 with E4M3 operands; `mn` for M-major A and N-major B.
-__host__ __device__ constexpr uint32_t mma_idesc(bool e4m3, bool mn, int n) {
-  return (1u << 4) | ((e4m3 ? 0u : 1u) << 7) | ((e4m3 ? 0u : 1u) << 10) | ((mn ? 3u : 0u) << 15) |
-         (static_cast<uint32_t>(n >> 3) << 17) | ((128u >> 4) << 24);
+// Instruction descriptor of kind::f16: fp32 accumulation, bf16 operands; `mn` for M-major A and N-major B.
+__host__ __device__ constexpr uint32_t mma_idesc(bool mn, int n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((mn ? 3u : 0u) << 15) | (static_cast<uint32_t>(n >> 3) << 17) |
+         ((128u >> 4) << 24);
 }
 
 // D[tmem] (+)= A x B; a and b are descriptors' low words.
-template <bool kE4m3>
 __device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t a_hi, uint32_t b, uint32_t b_hi, uint32_t idesc,
                                     uint32_t accumulate) {
-  if (kE4m3)
-    asm volatile(
-        "{\n .reg .pred p;\n .reg .b64 x, y;\n mov.b64 x, {%1, %2};\n mov.b64 y, {%3, %4};\n setp.ne.b32 p, %6, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %5, p;\n}" ::"r"(d),
-        "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "r"(accumulate)
-        : "memory");
-  else
-    asm volatile(
-        "{\n .reg .pred p;\n .reg .b64 x, y;\n mov.b64 x, {%1, %2};\n mov.b64 y, {%3, %4};\n setp.ne.b32 p, %6, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n}" ::"r"(d),
-        "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "r"(accumulate)
-        : "memory");
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 x, y;\n mov.b64 x, {%1, %2};\n mov.b64 y, {%3, %4};\n setp.ne.b32 p, %6, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n}" ::"r"(d),
+      "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
@@ -297,27 +299,22 @@ __device__ __forceinline__ void split_bf16x2(float x0, float x1, uint32_t& hi, u
   lo = bf16x2(r0, r1);
 }
 
-// x0 .. x3 as E4M3 numbers hi + lo / kLift: hi is x rounded, lo the rest times kLift rounded (9 bits together).
-constexpr float kLift = 16.f;  // hi's rest is at most 1/16 of 448 / 2, so 16 times that still fits
-template <bool kLifted>
-__device__ __forceinline__ void split_e4m3x4(float x0, float x1, float x2, float x3, uint32_t& hi, uint32_t& lo) {
-  asm("{\n .reg .b32 f, g, h, i;\n .reg .b16 a, b, c, d;\n"
-      " cvt.rn.f16x2.f32 f, %3, %2;\n"
-      " cvt.rn.f16x2.f32 g, %5, %4;\n"
-      " cvt.rn.satfinite.e4m3x2.f16x2 a, f;\n"
-      " cvt.rn.satfinite.e4m3x2.f16x2 b, g;\n"
-      " mov.b32 %0, {a, b};\n"
-      " cvt.rn.f16x2.e4m3x2 h, a;\n"
-      " cvt.rn.f16x2.e4m3x2 i, b;\n"
-      " sub.rn.f16x2 f, f, h;\n"
-      " sub.rn.f16x2 g, g, i;\n"
-      " mul.rn.f16x2 f, f, %6;\n"
-      " mul.rn.f16x2 g, g, %6;\n"
-      " cvt.rn.satfinite.e4m3x2.f16x2 c, f;\n"
-      " cvt.rn.satfinite.e4m3x2.f16x2 d, g;\n"
-      " mov.b32 %1, {c, d};\n}"
-      : "=r"(hi), "=r"(lo)
-      : "f"(x0), "f"(x1), "f"(x2), "f"(x3), "r"(kLifted ? 0x4c004c00u : 0x3c003c00u));
+// Four E4M3 codes as two pairs of bf16. Through fp16 and fp32, all of it exact: a value has 4 bits, NaN stays NaN.
+__device__ __forceinline__ void widen4(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 a, b, c, d;\n .reg .b32 f, g, x, y;\n"
+      " mov.b32 {a, b}, %2;\n"
+      " cvt.rn.f16x2.e4m3x2 f, a;\n"
+      " cvt.rn.f16x2.e4m3x2 g, b;\n"
+      " mov.b32 {a, b}, f;\n"
+      " mov.b32 {c, d}, g;\n"
+      " cvt.f32.f16 x, a;\n"
+      " cvt.f32.f16 y, b;\n"
+      " prmt.b32 %0, x, y, 0x7632;\n"
+      " cvt.f32.f16 x, c;\n"
+      " cvt.f32.f16 y, d;\n"
+      " prmt.b32 %1, x, y, 0x7632;\n}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(codes));
 }
 
 // Reduce kN values over the 32 lanes of a warp, halving the values a lane
@@ -378,31 +375,31 @@ __device__ __forceinline__ long long div_of(long long a, long long b) {
 }  // namespace
 
 template <int D, bool kE4m3, int N>
-__global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(Shape<D, kE4m3, N>::kThreads, 1) attention_kernel(const __grid_constant__ AttnParams p) {
   using S = Shape<D, kE4m3, N>;
-  constexpr int C = S::kCols;
+  constexpr int C = S::kCols, kThreads = S::kThreads;
   extern __shared__ __align__(1024) uint8_t smem[];
   // operands first (1024-byte aligned), then rings, state and barriers
   uint8_t* const units = smem;
-  uint8_t* const q_s = units + S::kSlots * S::kUnit;
+  uint8_t* const raws = units + S::kSlots * S::kUnit;  // E4M3
+  uint8_t* const q_s = raws + 2 * S::kRaws * S::kRaw;
   uint8_t* const p_s = q_s + S::kQBufs * S::kQBytes;
   int64_t* const ring_off = reinterpret_cast<int64_t*>(p_s + S::kPBytes);          // [ring][128]
-  float2* const ring_scale = reinterpret_cast<float2*>(ring_off + kAddrRing * 128);  // [ring][128], E4M3
+  float2* const ring_scale = reinterpret_cast<float2*>(ring_off + S::kRing * 128);  // [ring][128], E4M3
   uint32_t* const ring_mask = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(ring_off) + S::kRingBytes);
-  AttnSeg* const segs = reinterpret_cast<AttnSeg*>(ring_mask + kAddrRing * 4);
+  AttnSeg* const segs = reinterpret_cast<AttnSeg*>(ring_mask + S::kRing * 4);
   float* const nm_s = reinterpret_cast<float*>(segs + kSegRing);  // [N] running maxima, negated
   float* const alpha_s = nm_s + N;                               // [N] rescale factors
   float* const up_s = alpha_s + N;                               // [N] the last raise of each maximum
   float* const inv_s = up_s + N;                                 // [N] 1 / l of the segment being written
-  float* const qscale_s = inv_s + N;                             // [kQScales][N], E4M3: 1 / the scale Q was stored with
-  float* const scratch = qscale_s + (kE4m3 ? kQScales * N : 0);                       // [2][4][C]
+  float* const scratch = inv_s + N;                              // [2][4][C]
   uint64_t* const bars = reinterpret_cast<uint64_t*>(scratch + 8 * C);
   // barriers
   constexpr int kFull = 0, kEmpty = kFull + S::kSlots, kSFull = kEmpty + S::kSlots, kSEmpty = kSFull + 2, kPFull = kSEmpty + 2,
                 kPvDone = kPFull + 1, kQEmpty = kPvDone + 1, kQFull = kQEmpty + 2, kSegFull = kQFull + 2,
                 kSegEmpty = kSegFull + kSegRing,
-                kAFull = kSegEmpty + kSegRing, kAEmpty = kAFull + kAddrRing, kDrain = kAEmpty + kAddrRing, kScFull = kDrain + 2,
-                kBars = kScFull + (kE4m3 ? kAddrRing : 0);
+                kAFull = kSegEmpty + kSegRing, kAEmpty = kAFull + S::kRing, kDrain = kAEmpty + S::kRing, kScFull = kDrain + 2,
+                kBars = kScFull + (kE4m3 ? S::kRing : 0);
   static_assert(kBars * 8 <= 640, "");
   auto bar = [&](int i) { return smem_addr(bars + i); };
 
@@ -418,13 +415,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 
   if (tid < kBars) {  // a barrier a thread
     const int i = tid;
-    const int count = i < kEmpty ? kLoaders                                   // K and V units: each loader thread's copies
+    const int count = i < kEmpty ? (kE4m3 ? kLoaders / 32 : kLoaders)         // K and V units: loader warps, or each thread's copies
                       : i < kSEmpty ? 1                                       // freed by the MMAs; S
                       : i < kPvDone ? kSoftmax / 32                           // S read, P written: each softmax warp
                       : i < kQFull ? 1                                        // O; queries freed by the MMAs
-                      : i < kSegFull ? kLoaders                               // 8-bit queries
-                      : i < kSegEmpty ? 1 : i < kAFull ? kSegReaders          // segments
-                      : i < kAEmpty ? 1 : i < kDrain ? kAddrReaders           // addresses
+                      : i < kSegFull ? kLoaders                               // queries over an 8-bit cache: each thread's copies
+                      : i < kSegEmpty ? 1 : i < kAFull ? S::kSegReaders          // segments
+                      : i < kAEmpty ? 1 : i < kDrain ? S::kAddrReaders           // addresses
                       : i < kScFull ? 1 : 64;                                 // drains; scales: each lane's copies, and its stores
     mbar_init(bar(i), count);
   }
@@ -493,129 +490,218 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   const volatile int* const abort = &abort_flag;
   auto fail = [&] { *reinterpret_cast<volatile int*>(&abort_flag) = 1; };  // reported at the end
 
-  // the softmax threads take registers that the others do not need: 256 x 72 + 256 x 184 = 512 x 128
-  if (warp < 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp < 4) {
+  // the softmax threads take registers that the others do not need
+  if (warp < 8 || warp >= 16) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kOtherRegs));
+    if (warp < 4 || warp >= 16) {
       // ------------------------------------------------------------ loaders
       const int stall_tile = blockIdx.x == 0 ? p.stall_tile : -1;  // tests: its keys are not handed over
-      constexpr int kChunks = S::kRow / 16;         // 16-byte pieces of a token
-      constexpr int kTok = 32 / kChunks;            // tokens per warp instruction
-      const int piece = lane % kChunks, sub = lane / kChunks;
       const uint32_t units_a = smem_addr(units);
       bool ok = true;
       auto wait = [&](int b, uint32_t parity) {
         ok = wait_phase(bar(b), parity, abort, limit);
         return ok;
       };
-      // Units: K 0, V 0, K 1, V 1, ... The unit's barrier counts each thread's copies when they land; the MMA warps'
-      // proxy fence, after their wait, orders them before the tensor core's reads.
-      int slot = 0, seg = 0, left = 0, tile = 0;  // left: tiles of this segment
-      uint32_t turn = 1;                          // parity that says that the slot is free
-      for (bool values = false; ok; values = !values) {
-        if (!values) {
-          if (left == 0) {
-            if (!wait(kSegFull + seg % kSegRing, (seg / kSegRing) & 1)) break;
-            const AttnSeg sg = segs[seg % kSegRing];
-            left = sg.ntiles;
-            if (left == 0) break;
-            // the segment's queries: in bf16 its first K tile's barrier covers them, split in E4M3 they have one
-            const int qb = seg % S::kQBufs;
-            if (!wait(kQEmpty + qb, (seg / S::kQBufs + 1) & 1)) break;
-            const uint16_t* qrow = p.q + sg.row * p.q_stride + static_cast<int64_t>(sg.kvh) * p.group * D;
-            uint8_t* const qdst = q_s + qb * S::kQBytes;
-            if (!kE4m3) {
-              constexpr int kQChunks = D * 2 / 16, kQTok = 32 / kQChunks;
-              const int c = lane % kQChunks;
-              for (int i = warp * kQTok + lane / kQChunks; i < N; i += 4 * kQTok)
-                cp16(smem_addr(qdst) + (c >> 3) * (N * 128) + i * 128 + (((c & 7) ^ (i & 7)) << 4),
-                     qrow + (i < p.group ? i * D + c * 8 : 0), i < p.group ? 16 : 0);
-            } else {
-              // A head per D / 8 lanes, fetched with all loads in flight into the rows where it is then stored, as hi + lo
-              // times a power of two that brings its amax to (224, 448].
-              constexpr int kL = D / 8;
-              const int c = lane % kL, i0 = warp * (32 / kL) + lane / kL;
-              uint8_t* const piece_q = qdst + (c >> 3) * S::kQPart + (c & 7) * 16;
-              for (int i = i0; i < N; i += 4 * (32 / kL))
-                cp16(smem_addr(piece_q + i * 128), qrow + (i < p.group ? i * D + c * 8 : 0), i < p.group ? 16 : 0);
-              cp_wait_all();
-              __syncwarp();
-#pragma unroll 1
-              for (int i = i0; i < N; i += 4 * (32 / kL)) {
-                const uint4 w = *reinterpret_cast<const uint4*>(piece_q + i * 128);
-                __syncwarp();
-                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-                float x[8], amax = 0.f;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  x[2 * k] = __uint_as_float(ws[k] << 16);
-                  x[2 * k + 1] = __uint_as_float(ws[k] & 0xffff0000u);
-                  amax = fmaxf(amax, fmaxf(fabsf(x[2 * k]), fabsf(x[2 * k + 1])));
+      auto fetch_queries = [&](const AttnSeg& sg, int qb) {
+        const uint16_t* const qrow = p.q + sg.row * p.q_stride + static_cast<int64_t>(sg.kvh) * p.group * D;
+        constexpr int kQChunks = D * 2 / 16, kQTok = 32 / kQChunks;
+        const int c = lane % kQChunks;
+        for (int i = warp * kQTok + lane / kQChunks; i < N; i += 4 * kQTok)
+          cp16(smem_addr(q_s + qb * S::kQBytes) + (c >> 3) * (N * 128) + i * 128 + (((c & 7) ^ (i & 7)) << 4),
+               qrow + (i < p.group ? i * D + c * 8 : 0), i < p.group ? 16 : 0);
+      };
+      if constexpr (kE4m3) {
+        // Warps 0-3 bring keys, warps 16-19 values. Each lane copies pieces of 16 codes into a place of its own and widens
+        // them later into the unit that the tensor core reads, so the copies need no barrier. Two cursors go over the
+        // tiles: one copies, up to kRaws tiles ahead of the one that widens.
+        constexpr int kPieces = D / 16;                             // of a token
+        constexpr int kTok = 32 / kPieces, kPer = 32 / kTok;        // tokens per warp instruction, pieces per lane and unit
+        // Eight lanes have two neighbouring tokens' pieces of one 128-byte column, so that their stores, two 16-byte
+        // chunks apart within a token and swizzled by the token, meet every bank once.
+        const int piece = (lane & 3) | (kPieces == 8 ? (lane >> 1) & 4 : 0);
+        const int sub = kPieces == 8 ? ((lane >> 2) & 1) | ((lane >> 3) & 2) : lane >> 2;
+        const bool values = warp >= 16;
+        const int w0 = (warp & 3) * 32;                             // the warp's first token
+        uint8_t* const mine = raws + (values ? S::kRaws * S::kRaw : 0) + w0 * D + lane * 16;
+        const uint8_t* const base = static_cast<const uint8_t*>(values ? p.v_cache : p.k_cache) + piece * 16;
+        int ahead = 0;                                              // tiles copied and not yet widened
+        int cseg = 0, cleft = 0, ctile = 0, craw = 0, qseg = 0;     // copying; segments whose queries are asked for
+        int seg = 0, left = 0, tile = 0, raw = 0;                   // widening
+        int slot = values ? 1 : 0;                                  // keys in the even units, values in the odd ones
+        uint32_t turn = 1;
+        bool more = true;
+        auto ready = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test_wait(bar(b), parity)); };
+        while (true) {
+          if (more && ahead < S::kRaws) {
+            // copy the next tile; as long as there is something to widen, only if its segment and addresses are there
+            bool there = true;
+            if (cleft == 0) {
+              const int at = kSegFull + cseg % kSegRing, parity = (cseg / kSegRing) & 1;
+              there = ahead > 0 ? ready(at, parity) : wait(at, parity);
+              if (there) {
+                const AttnSeg& sg = segs[cseg % kSegRing];
+                cleft = sg.ntiles;
+                more = there = cleft > 0;
+                const int qb = cseg % S::kQBufs;
+                if (more && !values && qseg == cseg && ready(kQEmpty + qb, (cseg / S::kQBufs + 1) & 1)) {
+                  fetch_queries(sg, qb);
+                  cp_arrive(bar(kQFull + qb));
+                  ++qseg;
                 }
-#pragma unroll
-                for (int o = kL / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                // amax = f * 2^e with f in [1, 2): the factor 2^(7 - e), or 2^(8 - e) where f <= 1.75
-                const uint32_t bits = __float_as_uint(amax);
-                int e = static_cast<int>(bits >> 23) - 127;
-                e = e < -100 ? -100 : e;
-                const int up = 7 - e + ((bits & 0x7fffffu) <= 0x600000u ? 1 : 0);
-                const float mul = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
-                uint32_t hi[2], lo[2];
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                  split_e4m3x4<false>(x[4 * k] * mul, x[4 * k + 1] * mul, x[4 * k + 2] * mul, x[4 * k + 3] * mul, hi[k], lo[k]);
-                uint8_t* dst = qdst + i * 128 + (((c >> 1) ^ (i & 7)) << 4) + (c & 1) * 8;
-                *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
-                *reinterpret_cast<uint2*>(dst + S::kQPart) = make_uint2(lo[0], lo[1]);
-                if (c == 0) qscale_s[(seg % kQScales) * N + i] = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+                ++cseg;
               }
-              mbar_arrive(bar(kQFull + qb));
+            }
+            if (there) {
+              const int at = kAFull + ctile % S::kRing, parity = (ctile / S::kRing) & 1;
+              there = ahead > 0 ? ready(at, parity) : wait(at, parity);
+            }
+            if (!ok) break;
+            if (there) {
+              const int64_t* const offs = ring_off + ctile % S::kRing * 128 + w0 + sub;
+              const uint32_t dst = smem_addr(mine) + craw * S::kRaw;
+              const bool whole = ring_mask[ctile % S::kRing * 4 + (warp & 3)] == 0xffffffffu;  // every token is there
+              if (__builtin_expect(whole, 1)) {
+#pragma unroll
+                for (int i0 = 0; i0 < kPer; i0 += 4) {
+                  const uint8_t* src[4];
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) src[i] = base + offs[(i0 + i) * kTok];
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) cp16(dst + (i0 + i) * 512, src[i]);
+                }
+              } else {
+#pragma unroll 1
+                for (int i = 0; i < kPer; ++i) {
+                  const int64_t o = offs[i * kTok];
+                  cp16(dst + i * 512, base + (o < 0 ? 0 : o), o < 0 ? 0 : 16);
+                }
+              }
+              cp_commit();
+              __syncwarp();
+              arrive_one(bar(kAEmpty + ctile % S::kRing), lane);
+              ++ctile;
+              --cleft;
+              if (++craw == S::kRaws) craw = 0;
+              ++ahead;
+              continue;
+            }
+          }
+          if (ahead == 0) break;
+          if (left == 0) {
+            left = segs[seg % kSegRing].ntiles;
+            if (!values && qseg == seg) {
+              const int qb = seg % S::kQBufs;
+              if (!wait(kQEmpty + qb, (seg / S::kQBufs + 1) & 1)) break;
+              fetch_queries(segs[seg % kSegRing], qb);
+              cp_arrive(bar(kQFull + qb));
+              ++qseg;
             }
             __syncwarp();
             arrive_one(bar(kSegEmpty + seg % kSegRing), lane);
             ++seg;
           }
-          if (!wait(kAFull + tile % kAddrRing, (tile / kAddrRing) & 1)) break;
-        }
-        if (!wait(kEmpty + slot, turn)) break;
-        const uint8_t* const base = static_cast<const uint8_t*>(values ? p.v_cache : p.k_cache) + piece * 16;
-        const uint32_t dst0 = units_a + slot * S::kUnit + (piece >> 3) * 16384;
-        const int64_t* const offs = ring_off + tile % kAddrRing * 128 + warp * 32 + sub;
-        constexpr int kBatch = 32 / kTok < 8 ? 32 / kTok : 8;  // addresses first, so that the copies issue back to back
-        const uint32_t dst1 = dst0 + (warp * 32 + sub) * 128;
-        const bool whole = ring_mask[tile % kAddrRing * 4 + warp] == 0xffffffffu;  // every token of the warp is there
-        if (__builtin_expect(whole, 1)) {
-#pragma unroll
-          for (int i0 = 0; i0 < 32 / kTok; i0 += kBatch) {
-            const uint8_t* src[kBatch];
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) src[i] = base + offs[(i0 + i) * kTok];
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-              cp16(dst1 + (i0 + i) * kTok * 128 + (((piece & 7) ^ (((i0 + i) * kTok + sub) & 7)) << 4), src[i]);
-          }
-        } else {
+          if (!wait(kEmpty + slot, turn)) break;
+          if (ahead == S::kRaws)
+            cp_wait<S::kRaws - 1>();  // the oldest tile has landed
+          else
+            cp_wait_all();
+          const uint8_t* const src = mine + raw * S::kRaw;
+          const uint32_t dst = units_a + slot * S::kUnit + (piece >> 2) * 16384 + (w0 + sub) * 128;
 #pragma unroll 1
-          for (int i0 = 0; i0 < 32 / kTok; i0 += 4) {
-            int64_t o[4];
+          for (int i0 = 0; i0 < kPer; i0 += 2) {
+            uint4 w[2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = offs[(i0 + i) * kTok];
+            for (int i = 0; i < 2; ++i) w[i] = *reinterpret_cast<const uint4*>(src + (i0 + i) * 512);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              cp16(dst1 + (i0 + i) * kTok * 128 + (((piece & 7) ^ (((i0 + i) * kTok + sub) & 7)) << 4),
-                   base + (o[i] < 0 ? 0 : o[i]), o[i] < 0 ? 0 : 16);
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t row = dst + (i0 + i) * (kTok * 128), t = (i * kTok + sub) & 7;  // i0 * kTok is a multiple of 8
+              uint32_t x[4];
+              widen4(w[i].x, x[0], x[1]);
+              widen4(w[i].y, x[2], x[3]);
+              sts16(row + (((piece & 3) * 2 ^ t) << 4), x[0], x[1], x[2], x[3]);
+              widen4(w[i].z, x[0], x[1]);
+              widen4(w[i].w, x[2], x[3]);
+              sts16(row + (((piece & 3) * 2 + 1 ^ t) << 4), x[0], x[1], x[2], x[3]);
+            }
           }
-        }
-        if (values || stall_tile != tile) cp_arrive(bar(kFull + slot));
-        if (++slot == S::kSlots) {
-          slot = 0;
-          turn ^= 1;
-        }
-        if (values) {
+          fence_proxy_async_smem();
           __syncwarp();
-          arrive_one(bar(kAEmpty + tile % kAddrRing), lane);
+          if (values || stall_tile != tile) arrive_one(bar(kFull + slot), lane);
+          slot += 2;
+          if (slot >= S::kSlots) {
+            slot -= S::kSlots;
+            turn ^= 1;
+          }
+          if (++raw == S::kRaws) raw = 0;
+          --ahead;
           ++tile;
           --left;
+        }
+      } else {
+        constexpr int kChunks = S::kRow / 16;         // 16-byte pieces of a token
+        constexpr int kTok = 32 / kChunks;            // tokens per warp instruction
+        const int piece = lane % kChunks, sub = lane / kChunks;
+        // Units: K 0, V 0, K 1, V 1, ... The unit's barrier counts each thread's copies when they land; the MMA warps'
+        // proxy fence, after their wait, orders them before the tensor core's reads.
+        int slot = 0, seg = 0, left = 0, tile = 0;  // left: tiles of this segment
+        uint32_t turn = 1;                          // parity that says that the slot is free
+        for (bool values = false; ok; values = !values) {
+          if (!values) {
+            if (left == 0) {
+              if (!wait(kSegFull + seg % kSegRing, (seg / kSegRing) & 1)) break;
+              const AttnSeg sg = segs[seg % kSegRing];
+              left = sg.ntiles;
+              if (left == 0) break;
+              // the segment's queries: its first K tile's barrier covers them
+              const int qb = seg % S::kQBufs;
+              if (!wait(kQEmpty + qb, (seg / S::kQBufs + 1) & 1)) break;
+              fetch_queries(sg, qb);
+              __syncwarp();
+              arrive_one(bar(kSegEmpty + seg % kSegRing), lane);
+              ++seg;
+            }
+            if (!wait(kAFull + tile % S::kRing, (tile / S::kRing) & 1)) break;
+          }
+          if (!wait(kEmpty + slot, turn)) break;
+          const uint8_t* const base = static_cast<const uint8_t*>(values ? p.v_cache : p.k_cache) + piece * 16;
+          const uint32_t dst0 = units_a + slot * S::kUnit + (piece >> 3) * 16384;
+          const int64_t* const offs = ring_off + tile % S::kRing * 128 + warp * 32 + sub;
+          constexpr int kBatch = 32 / kTok < 8 ? 32 / kTok : 8;  // addresses first, so that the copies issue back to back
+          const uint32_t dst1 = dst0 + (warp * 32 + sub) * 128;
+          const bool whole = ring_mask[tile % S::kRing * 4 + warp] == 0xffffffffu;  // every token of the warp is there
+          if (__builtin_expect(whole, 1)) {
+#pragma unroll
+            for (int i0 = 0; i0 < 32 / kTok; i0 += kBatch) {
+              const uint8_t* src[kBatch];
+#pragma unroll
+              for (int i = 0; i < kBatch; ++i) src[i] = base + offs[(i0 + i) * kTok];
+#pragma unroll
+              for (int i = 0; i < kBatch; ++i)
+                cp16(dst1 + (i0 + i) * kTok * 128 + (((piece & 7) ^ (((i0 + i) * kTok + sub) & 7)) << 4), src[i]);
+            }
+          } else {
+#pragma unroll 1
+            for (int i0 = 0; i0 < 32 / kTok; i0 += 4) {
+              int64_t o[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[i] = offs[(i0 + i) * kTok];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                cp16(dst1 + (i0 + i) * kTok * 128 + (((piece & 7) ^ (((i0 + i) * kTok + sub) & 7)) << 4),
+                     base + (o[i] < 0 ? 0 : o[i]), o[i] < 0 ? 0 : 16);
+            }
+          }
+          if (values || stall_tile != tile) cp_arrive(bar(kFull + slot));
+          if (++slot == S::kSlots) {
+            slot = 0;
+            turn ^= 1;
+          }
+          if (values) {
+            __syncwarp();
+            arrive_one(bar(kAEmpty + tile % S::kRing), lane);
+            ++tile;
+            --left;
+          }
         }
       }
       if (!ok && lane == 0) fail();
@@ -704,36 +790,32 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         if (kE4m3 && scores && !wait(kQFull + qb, (seg / S::kQBufs) & 1)) break;
         for (int j = 0; j < n; ++j, ++it) {
           // the softmax reads the tile's mask and scales behind S: they are there before S is issued
-          if (scores && !wait((kE4m3 ? kScFull : kAFull) + it % kAddrRing, (it / kAddrRing) & 1)) break;
+          if (scores && !wait((kE4m3 ? kScFull : kAFull) + it % S::kRing, (it / S::kRing) & 1)) break;
           if (!wait(kFull + slot, turn)) break;
           if (!wait(scores ? kSEmpty + (it & 1) : kPFull, scores ? ((it >> 1) + 1) & 1 : it & 1)) break;
           fence_proxy_async_smem();
           tc_fence_after();
           const uint32_t unit_a = smem_addr(units) + slot * S::kUnit;
           if (scores) {
-            constexpr uint32_t kDesc = mma_idesc(kE4m3, false, N);
+            constexpr uint32_t kDesc = mma_idesc(false, N);
             const uint32_t a = desc_lo(unit_a, 16), q = desc_lo(smem_addr(q_s) + qb * S::kQBytes, 16);
             if (elect_one()) {
 #pragma unroll
-              for (int part = 0; part < S::kQParts; ++part)
-#pragma unroll
-                for (int k = 0; k < S::kRow / 32; ++k)  // 32 bytes of K
-                  mma<kE4m3>(tmem_sc + (it & 1) * N, a + (((k >> 2) * 16384 + (k & 3) * 32) >> 4), kRowHi,
-                             q + ((part * S::kQPart + (k >> 2) * (N * 128) + (k & 3) * 32) >> 4), kRowHi, kDesc,
-                             part + k > 0);
+              for (int k = 0; k < S::kRow / 32; ++k)  // 32 bytes of K
+                mma(tmem_sc + (it & 1) * N, a + (((k >> 2) * 16384 + (k & 3) * 32) >> 4), kRowHi,
+                    q + (((k >> 2) * (N * 128) + (k & 3) * 32) >> 4), kRowHi, kDesc, k > 0);
               mma_commit(bar(kEmpty + slot));
               mma_commit(bar(kSFull + (it & 1)));
               if (j == n - 1) mma_commit(bar(kQEmpty + qb));
             }
           } else {
-            constexpr uint32_t kDesc = mma_idesc(kE4m3, true, 2 * N);
-            constexpr int kStep = kE4m3 ? 32 : 16;  // tokens
+            constexpr uint32_t kDesc = mma_idesc(true, 2 * N);
             const uint32_t a = desc_lo(unit_a, 16384), q = desc_lo(smem_addr(p_s), 128 * S::kPRow);
             if (elect_one()) {
 #pragma unroll
-              for (int k = 0; k < 128 / kStep; ++k)
-                mma<kE4m3>(tmem_o, a + ((k * kStep * 128) >> 4), kRowHi, q + ((k * kStep * S::kPRow) >> 4), desc_hi(S::kPRow),
-                           kDesc, j + k > 0);
+              for (int k = 0; k < 8; ++k)  // 16 tokens
+                mma(tmem_o, a + ((k * 16 * 128) >> 4), kRowHi, q + ((k * 16 * S::kPRow) >> 4), desc_hi(S::kPRow), kDesc,
+                    j + k > 0);
               mma_commit(bar(kEmpty + slot));
               mma_commit(bar(kPvDone));
             }
@@ -799,7 +881,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       int32_t ahead[4];
       bool more = next_tile(ahead);
       for (int it = 0; more; ++it) {
-        const int a = it % kAddrRing;
+        const int a = it % S::kRing;
         const int64_t head = head_at;
         int32_t in_page[4], page[4];
         bool asked[4];
@@ -815,7 +897,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           }
         }
         more = next_tile(ahead);
-        if (!ok || !wait(kAEmpty + a, (it / kAddrRing + 1) & 1)) break;
+        if (!ok || !wait(kAEmpty + a, (it / S::kRing + 1) & 1)) break;
         bool bad = false;
         int64_t off[4];
 #pragma unroll
@@ -854,7 +936,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     }
   } else {
     // ------------------------------------------------------------ softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kSoftmaxRegs));
     const int wg = (warp - 8) >> 2, quarter = warp & 3;
     const int t = quarter * 32 + lane;          // this thread's token, and its row of O^T
     const int c0 = wg * C;                      // its first head
@@ -863,8 +945,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     const uint32_t o_col = tmem_o + lanes + c0;
     float* const red = scratch + wg * 4 * C;
     // this thread's row of P: the 16-byte pieces of its heads, swizzled (its first piece is a multiple of their number)
-    constexpr int kWords = kE4m3 ? C / 4 : C / 2;
-    constexpr bool kWide = N == 128 && !kE4m3;  // a block of 64 heads for each group
+    constexpr int kWords = C / 2;
+    constexpr bool kWide = N == 128;  // a block of 64 heads for each group
     const int p_swz = (S::kPRow == 128 ? (t & 7) : S::kPRow == 64 ? ((t >> 1) & 3) : ((t >> 2) & 1)) ^
                       (kWide ? 0 : wg * (kWords / 4));
     const uint32_t p_row = smem_addr(p_s) + t * S::kPRow + (kWide ? wg * 128 * S::kPRow : 0);
@@ -876,8 +958,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     // Write the result of segment w, whose O is final: normalised by inv_s, or as a partial.
     auto write_out = [&](const AttnSeg& w) {
       tc_fence_after();
-      constexpr int kStep = !kE4m3 && C <= 32 && C >= 16 ? 16 : 8;
-#pragma unroll (kE4m3 || C > 32 ? 1 : 2)
+      constexpr int kStep = C <= 32 && C >= 16 ? 16 : 8;
+#pragma unroll (C > 32 ? 1 : 2)
       for (int c = 0; c < C; c += kStep) {
         if (c0 + c >= p.group) break;
         float o[kStep], o2[kStep];
@@ -891,7 +973,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           float* const dst = p.part_o + (w.slot * p.group + c0 + c) * D + t;
 #pragma unroll
           for (int i = 0; i < kStep; ++i)
-            if (c0 + c + i < p.group) dst[i * D] = o[i] + (kE4m3 ? o2[i] * (1.f / kLift) : o2[i]);
+            if (c0 + c + i < p.group) dst[i * D] = o[i] + o2[i];
         } else {
           // lanes 2 i and 2 i + 1 exchange, so that each writes two elements of every other head
           uint16_t* const dst = p.out +
@@ -899,8 +981,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                                 (t & ~1);
 #pragma unroll
           for (int i = 0; i < kStep; i += 2) {
-            const float x = (o[i] + (kE4m3 ? o2[i] * (1.f / kLift) : o2[i])) * inv_s[c0 + c + i];
-            const float y = (o[i + 1] + (kE4m3 ? o2[i + 1] * (1.f / kLift) : o2[i + 1])) * inv_s[c0 + c + i + 1];
+            const float x = (o[i] + o2[i]) * inv_s[c0 + c + i];
+            const float y = (o[i + 1] + o2[i + 1]) * inv_s[c0 + c + i + 1];
             const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? x : y, 1);
             if (c0 + c + i + (lane & 1) < p.group)
               *reinterpret_cast<uint32_t*>(dst + i * D) = lane & 1 ? bf16x2(got, y) : bf16x2(x, got);
@@ -929,28 +1011,25 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       }
 #pragma unroll
       for (int c = 0; c < C; ++c) l[c] = 0.f;
-      const float* const qscale = qscale_s + (seg % kQScales) * N + c0;
       bool fresh = true;  // no token so far
       for (int j = 0; j < sg.ntiles; ++j, ++it) {
-        const int a = it % kAddrRing;
+        const int a = it % S::kRing;
         if (__builtin_expect(!s_ready, 0)) wait(kSFull + (it & 1), (it >> 1) & 1);
         float s[C];  // scores, less the running maxima, then P
         bool over = failed;
-        float inv_vs = 1.f;
         tc_fence_after();  // (after a failed wait the scores are of no use, and do no harm)
         const uint32_t s_col = tmem_sc + lanes + (it & 1) * N + c0;
         constexpr int kLd = C > 32 ? 32 : C;
 #pragma unroll
         for (int c = 0; c < C; c += kLd) tmem_ld<kLd>(s_col + c, s + c);
-        float mul = p.scale_log2, add = 0.f;
+        float mul = p.scale_log2, vs = 1.f;
         const uint4 mask = *reinterpret_cast<const uint4*>(ring_mask + a * 4);
         const bool valid = ((quarter == 0 ? mask.x : quarter == 1 ? mask.y : quarter == 2 ? mask.z : mask.w) >> lane) & 1;
         const bool first = fresh && (mask.x | mask.y | mask.z | mask.w) != 0;
         if (kE4m3) {
           const float2 sc = ring_scale[a * 128 + t];
           mul *= sc.x;
-          add = lg2(sc.y);
-          inv_vs = __fdividef(1.f, sc.y);
+          vs = sc.y;
         }
         tmem_wait_ld();
         pin<C>(s);
@@ -961,16 +1040,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         float most = -INFINITY;
 #pragma unroll
         for (int c = 0; c < C; c += 4) {
-          float4 a4 = *reinterpret_cast<const float4*>(nm_s + c0 + c), f4 = make_float4(mul, mul, mul, mul);
-          if (kE4m3) {
-            const float4 q4 = *reinterpret_cast<const float4*>(qscale + c);
-            mul2(f4.x, f4.y, q4.x, q4.y);
-            mul2(f4.z, f4.w, q4.z, q4.w);
-            add2(a4.x, a4.y, add, add);
-            add2(a4.z, a4.w, add, add);
-          }
-          fma2(s[c], s[c + 1], f4.x, f4.y, a4.x, a4.y);
-          fma2(s[c + 2], s[c + 3], f4.z, f4.w, a4.z, a4.w);
+          const float4 a4 = *reinterpret_cast<const float4*>(nm_s + c0 + c);
+          fma2(s[c], s[c + 1], mul, mul, a4.x, a4.y);
+          fma2(s[c + 2], s[c + 3], mul, mul, a4.z, a4.w);
           most = fmaxf(fmaxf(most, fmaxf(s[c], s[c + 1])), fmaxf(s[c + 2], s[c + 3]));
         }
         if (!valid) {
@@ -978,7 +1050,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           for (int c = 0; c < C; ++c) s[c] = -INFINITY;
           most = -INFINITY;
         }
-        over |= most > S::kTau || first;
+        over |= most > kTau || first;
         const bool raise = bar_or(bar_id, 128, over);
         // asked early, as an answer takes its time behind the copies in the load-store queue
         const bool pv_ready = it == 0 || __all_sync(0xffffffffu, mbar_test_wait(bar(kPvDone), (it - 1) & 1));
@@ -998,7 +1070,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             break;
           }
           if (wt < C) {
-            const float top = fmaxf(fmaxf(red[wt], red[C + wt]), fmaxf(red[2 * C + wt], red[3 * C + wt])) - S::kTop;
+            const float top = fmaxf(fmaxf(red[wt], red[C + wt]), fmaxf(red[2 * C + wt], red[3 * C + wt]));
             const float up = top == -INFINITY ? 0.f : first ? top : fmaxf(top, 0.f);
             nm_s[c0 + wt] -= up;
             up_s[c0 + wt] = up;
@@ -1020,14 +1092,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         for (int c = 0; c < C; ++c) s[c] = ex2(s[c]);
 #pragma unroll
         for (int i = 0; i < kWords; ++i) {
-          if (kE4m3) {
-            fma2acc(l[(4 * i) % C], l[(4 * i + 1) % C], s[(4 * i) % C], s[(4 * i + 1) % C], inv_vs);
-            fma2acc(l[(4 * i + 2) % C], l[(4 * i + 3) % C], s[(4 * i + 2) % C], s[(4 * i + 3) % C], inv_vs);
-            split_e4m3x4<true>(s[(4 * i) % C], s[(4 * i + 1) % C], s[(4 * i + 2) % C], s[(4 * i + 3) % C], hi[i], lo[i]);
-          } else {
-            add2(l[(2 * i) % C], l[(2 * i + 1) % C], s[(2 * i) % C], s[(2 * i + 1) % C]);
-            split_bf16x2(s[(2 * i) % C], s[(2 * i + 1) % C], hi[i], lo[i]);
-          }
+          add2(l[2 * i], l[2 * i + 1], s[2 * i], s[2 * i + 1]);
+          if (kE4m3) mul2(s[2 * i], s[2 * i + 1], vs, vs);
+          split_bf16x2(s[2 * i], s[2 * i + 1], hi[i], lo[i]);
         }
         // computed here, not behind the wait, where the compiler would move it
 #pragma unroll
@@ -1221,49 +1288,45 @@ cudaError_t launch(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t s
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Calls f with the kernel of a geometry and its shared-memory bytes.
+// Calls f with the kernel of a geometry and its shape.
 template <typename F>
 cudaError_t with_kernel(int head_dim, bool e4m3, int group, F f) {
-#define SMQ_ATTN(D, E, N) return f(attention_kernel<D, E, N>, static_cast<size_t>(Shape<D, E, N>::kSmem))
+#define SMQ_ATTN(D, E, N) return f(attention_kernel<D, E, N>, Shape<D, E, N>())
+#define SMQ_ATTN_GROUPS(D, E)         \
+  if (group <= 16) SMQ_ATTN(D, E, 16); \
+  if (group <= 32) SMQ_ATTN(D, E, 32); \
+  if (group <= 64) SMQ_ATTN(D, E, 64); \
+  SMQ_ATTN(D, E, 128)
   if (head_dim == 128) {
     if (e4m3) {
-      if (group <= 32) SMQ_ATTN(128, true, 32);
-      if (group <= 64) SMQ_ATTN(128, true, 64);
-      SMQ_ATTN(128, true, 128);
+      SMQ_ATTN_GROUPS(128, true);
     }
-    if (group <= 16) SMQ_ATTN(128, false, 16);
-    if (group <= 32) SMQ_ATTN(128, false, 32);
-    if (group <= 64) SMQ_ATTN(128, false, 64);
-    SMQ_ATTN(128, false, 128);
+    SMQ_ATTN_GROUPS(128, false);
   }
   if (e4m3) {
-    if (group <= 32) SMQ_ATTN(64, true, 32);
-    if (group <= 64) SMQ_ATTN(64, true, 64);
-    SMQ_ATTN(64, true, 128);
+    SMQ_ATTN_GROUPS(64, true);
   }
-  if (group <= 16) SMQ_ATTN(64, false, 16);
-  if (group <= 32) SMQ_ATTN(64, false, 32);
-  if (group <= 64) SMQ_ATTN(64, false, 64);
-  SMQ_ATTN(64, false, 128);
+  SMQ_ATTN_GROUPS(64, false);
+#undef SMQ_ATTN_GROUPS
 #undef SMQ_ATTN
 }
 
 }  // namespace
 
 cudaError_t prepare_attention(int head_dim, bool e4m3, int group) {
-  return with_kernel(head_dim, e4m3, group, [](auto kernel, size_t smem) {
+  return with_kernel(head_dim, e4m3, group, [](auto kernel, auto shape) {
     // the register split waits for ever on a launch with fewer registers than it hands out
     cudaFuncAttributes a;
     const cudaError_t rc = cudaFuncGetAttributes(&a, kernel);
     if (rc != cudaSuccess) return rc;
-    if (a.numRegs != 128) return cudaErrorInvalidKernelImage;
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (a.numRegs != decltype(shape)::kRegs) return cudaErrorInvalidKernelImage;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, decltype(shape)::kSmem);
   });
 }
 
 cudaError_t launch_attention(const AttnParams& p, bool e4m3, int grid, cudaStream_t stream) {
-  cudaError_t rc = with_kernel(p.head_dim, e4m3, p.group, [&](auto kernel, size_t smem) {
-    return launch(kernel, dim3(grid), kThreads, smem, stream, p);
+  cudaError_t rc = with_kernel(p.head_dim, e4m3, p.group, [&](auto kernel, auto shape) {
+    return launch(kernel, dim3(grid), decltype(shape)::kThreads, decltype(shape)::kSmem, stream, p);
   });
   if (rc != cudaSuccess) return rc;
   // no row is shared where the tile list is cut between items only

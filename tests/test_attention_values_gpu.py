@@ -1,0 +1,76 @@
+"""Attention over the whole range of what a cache and its queries may hold: value vectors of zeros and of very different
+sizes beside each other, single tokens that hold most of the weight, small elements beside large ones, infinities. All
+rows attend over one long sequence, so that every CTA sees most of it in one run of tiles."""
+
+import numpy as np
+import pytest
+import torch
+
+import sparse_attention_top_expand_gb300 as smq
+
+import attention_bounds as ab
+import attention_ref as ref
+from test_attention_gpu import Rows
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+ROWS = 160  # at least one row a CTA
+
+
+def _sink(rng, dtype, n, weight, amplitude, sink_value, heads=16, at=0):
+    """A sequence of n tokens with values of about `amplitude`, whose token `at` draws about `weight` of the softmax and
+    has values of size `sink_value`."""
+    cache = ref.Cache(rng, 1, 128, 64, dtype, [n])
+    k = rng.standard_normal((n, 1, 128)).astype(np.float32)
+    k[:, 0, 0] = 0
+    k[at] = 0
+    k[at, 0, 0] = (np.log(n) + 1.1 + np.log(weight / (1 - weight))) * np.sqrt(128) / 8
+    v = (rng.standard_normal((n, 1, 128)) * amplitude).astype(np.float32)
+    v[at] = rng.standard_normal((1, 128)) * sink_value
+    ab.put(cache, 0, np.arange(n), 0, k)
+    ab.put(cache, 0, np.arange(n), 1, v)
+    rows = Rows(rng, cache, heads, [0] * ROWS)
+    q = rows.q.clone()
+    q[:, :, 0] = 8
+    _queries(rows, q)
+    return rows
+
+
+def _queries(rows, q):
+    rows.q = q
+    rows.q_dev = q.to(DEV)
+
+
+def _check(rows, positions, which=(0, 77, ROWS - 1), absolute=0.0):
+    k, v = rows.cache.tokens(0, positions)
+    for r in which:
+        ab.check(rows.dev["out"][r], rows.dev["lse"][r], rows.q[r].to(torch.float64).numpy(), k, v, rows.scale,
+                 f"row {r}", absolute)
+
+
+@pytest.mark.parametrize("n,weight,amplitude,sink_value", [
+    (2048, 0.3, 1.0, 0.0), (2048, 0.5, 1.0, 0.0), (2048, 0.9, 1.0, 0.0), (32768, 0.3, 1.0, 0.0),  # a token of zeros
+    (2048, 0.5, 1e-3, 0.0), (2048, 0.5, 1e-9, 0.0), (2048, 0.01, 1e-6, 0.0),
+    (2048, 0.5, 1.0, 1.0), (131072, 0.5, 1.0, 1.0), (131072, 0.9, 1.0, 1.0),                      # before a long tail
+    (2048, 0.5, 1.0, 1e-6), (2048, 1e-5, 1e-4, 1.0), (2048, 0.9, 1e20, 1e25),
+])
+@pytest.mark.parametrize("dtype", ["e4m3", "bf16"])
+def test_one_token_that_holds_much_of_the_weight(dtype, n, weight, amplitude, sink_value):
+    rng = np.random.Generator(np.random.PCG64(n + int(weight * 100)))
+    rows = _sink(rng, dtype, n, weight, amplitude, sink_value, heads=16 if n < 10000 else 3)
+    assert rows.call(row_ke=torch.full((ROWS,), n, dtype=torch.int32, device=DEV)) == 0
+    _check(rows, np.arange(n), (0, ROWS - 1) if n < 10000 else (77,))
+
+
+@pytest.mark.parametrize("sink_value", [0.0, 1.0])
+@pytest.mark.parametrize("dtype", ["e4m3", "bf16"])
+def test_a_selected_token_that_holds_much_of_the_weight(dtype, sink_value):
+    rng = np.random.Generator(np.random.PCG64(12))
+    rows = _sink(rng, dtype, 5000, 0.5, 0.01, sink_value, at=4321)
+    ids = np.stack([np.r_[rng.permutation(4000)[:2000], -1, 4321] for _ in range(ROWS)]).astype(np.int32)
+    for i in ids:
+        rng.shuffle(i)
+    assert rows.call(token_ids=torch.from_numpy(ids).to(DEV)) == 0
+    for r in (0, 77, ROWS - 1):
+        _check(rows, ids[r][ids[r] >= 0], [r])
