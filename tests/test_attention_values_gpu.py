@@ -74,3 +74,19 @@ def test_a_selected_token_that_holds_much_of_the_weight(dtype, sink_value):
     assert rows.call(token_ids=torch.from_numpy(ids).to(DEV)) == 0
     for r in (0, 77, ROWS - 1):
         _check(rows, ids[r][ids[r] >= 0], [r])
+
+
+@pytest.mark.parametrize("n", [1, 700])
+def test_a_value_vector_below_the_reciprocal_range(n):
+    """A value scale whose reciprocal is past fp32. The absolute term: a weight times such a scale is below the normal
+    range (2^-126), times a code of at most 448."""
+    rng = np.random.Generator(np.random.PCG64(n))
+    cache = ref.Cache(rng, 1, 128, 64, "e4m3", [n])
+    ab.put(cache, 0, [n // 2], 1, (rng.standard_normal((1, 1, 128)) * 1e-37).astype(np.float32))
+    assert 0 < float(cache.scales[cache.table[0][n // 2 // 64], 1, 0, n // 2 % 64]) < 2.0 ** -129
+    for strength in (0.0, 100.0):  # as heavy as any, and of no weight at all
+        ab.put(cache, 0, [n // 2], 0, np.full((1, 1, 128), -strength, np.float32))
+        rows = Rows(rng, cache, 16, [0] * ROWS)
+        _queries(rows, rows.q.abs())
+        assert rows.call(row_ke=torch.full((ROWS,), n, dtype=torch.int32, device=DEV)) == 0
+        _check(rows, np.arange(n), absolute=2.0 ** -117)
