@@ -90,3 +90,41 @@ def test_a_value_vector_below_the_reciprocal_range(n):
         _queries(rows, rows.q.abs())
         assert rows.call(row_ke=torch.full((ROWS,), n, dtype=torch.int32, device=DEV)) == 0
         _check(rows, np.arange(n), absolute=2.0 ** -117)
+
+
+@pytest.mark.parametrize("dtype", ["e4m3", "bf16"])
+def test_small_query_elements_beside_a_large_one(dtype):
+    """The scores come from elements far below the head's largest, which meets keys of zero."""
+    rng = np.random.Generator(np.random.PCG64(41))
+    n = 1000
+    cache = ref.Cache(rng, 1, 128, 64, dtype, [n])
+    k = rng.standard_normal((n, 1, 128)).astype(np.float32)
+    k[:, :, 9] = 0
+    ab.put(cache, 0, np.arange(n), 0, k)
+    rows = Rows(rng, cache, 16, [0] * ROWS)
+    q = rows.q.clone()
+    q[:, :, 9] = 2.0 ** torch.linspace(0, 40, 16)
+    _queries(rows, q)
+    assert rows.call(row_ke=torch.full((ROWS,), n, dtype=torch.int32, device=DEV)) == 0
+    _check(rows, np.arange(n))
+
+
+@pytest.mark.parametrize("dtype", ["e4m3", "bf16"])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_queries_that_are_not_finite(dtype, bad):
+    """An infinite element makes scores of both infinities, and the head's result is NaN; other heads keep theirs."""
+    rng = np.random.Generator(np.random.PCG64(42))
+    n = 300
+    cache = ref.Cache(rng, 1, 64, 16, dtype, [n])
+    rows = Rows(rng, cache, 20, [0] * ROWS)
+    clean = rows.q.clone()
+    q = clean.clone()
+    q[:, 3, 7] = bad
+    rows.q_dev = q.to(DEV)
+    assert rows.call(row_ke=torch.full((ROWS,), n, dtype=torch.int32, device=DEV)) == 0
+    out = rows.dev["out"]
+    assert bool(torch.isnan(out[:, 3]).all())
+    keep = [h for h in range(20) if h != 3]
+    k, v = cache.tokens(0, np.arange(n))
+    for r in (0, ROWS - 1):
+        ab.check(out[r, keep], rows.dev["lse"][r, keep], clean[r, keep].to(torch.float64).numpy(), k, v, rows.scale)
