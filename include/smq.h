@@ -430,7 +430,10 @@ SMQ_API int sparse_mqa_quantize_q(const smq_plan *plan, const uint16_t *q, const
  * bfloat16 queries and the cache's elements as they are; sums, maxima and
  * scores are fp32; a weight (times its token's value scale) enters the sum of
  * the values with 16 bits, whatever the other tokens' scales are. Keys and
- * values of tokens outside T are never used, whatever they hold.
+ * values of tokens outside T are never used, whatever they hold. An infinite
+ * value makes its element of out infinite, or NaN where its token's weight is
+ * too small for fp32; a score of +infinity or NaN makes out[h] and lse[h] NaN.
+ * Finite values stay below 2^100, so that unnormalised sums are finite.
  *
  * The cache: keys and values are two arrays of pages [KVH][page_size][D],
  * page p at base + p * page_stride elements, so that both may be views of one

@@ -299,6 +299,10 @@ __device__ __forceinline__ void split_bf16x2(float x0, float x1, uint32_t& hi, u
   lo = bf16x2(r0, r1);
 }
 
+// O from its two parts. Where hi's is infinite, as an infinite value makes it, lo's may be NaN (a lo of zero times
+// infinity) and has nothing to add.
+__device__ __forceinline__ float join_parts(float hi, float lo) { return fabsf(hi) == INFINITY ? hi : hi + lo; }
+
 // Four E4M3 codes as two pairs of bf16. Through fp16 and fp32, all of it exact: a value has 4 bits, NaN stays NaN.
 __device__ __forceinline__ void widen4(uint32_t codes, uint32_t& lo, uint32_t& hi) {
   asm("{\n .reg .b16 a, b, c, d;\n .reg .b32 f, g, x, y;\n"
@@ -973,7 +977,7 @@ __global__ void __launch_bounds__(Shape<D, kE4m3, N>::kThreads, 1) attention_ker
           float* const dst = p.part_o + (w.slot * p.group + c0 + c) * D + t;
 #pragma unroll
           for (int i = 0; i < kStep; ++i)
-            if (c0 + c + i < p.group) dst[i * D] = o[i] + o2[i];
+            if (c0 + c + i < p.group) dst[i * D] = join_parts(o[i], o2[i]);
         } else {
           // lanes 2 i and 2 i + 1 exchange, so that each writes two elements of every other head
           uint16_t* const dst = p.out +
@@ -981,8 +985,8 @@ __global__ void __launch_bounds__(Shape<D, kE4m3, N>::kThreads, 1) attention_ker
                                 (t & ~1);
 #pragma unroll
           for (int i = 0; i < kStep; i += 2) {
-            const float x = (o[i] + o2[i]) * inv_s[c0 + c + i];
-            const float y = (o[i + 1] + o2[i + 1]) * inv_s[c0 + c + i + 1];
+            const float x = join_parts(o[i], o2[i]) * inv_s[c0 + c + i];
+            const float y = join_parts(o[i + 1], o2[i + 1]) * inv_s[c0 + c + i + 1];
             const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? x : y, 1);
             if (c0 + c + i + (lane & 1) < p.group)
               *reinterpret_cast<uint32_t*>(dst + i * D) = lane & 1 ? bf16x2(got, y) : bf16x2(x, got);

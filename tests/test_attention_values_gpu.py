@@ -128,3 +128,27 @@ def test_queries_that_are_not_finite(dtype, bad):
     k, v = cache.tokens(0, np.arange(n))
     for r in (0, ROWS - 1):
         ab.check(out[r, keep], rows.dev["lse"][r, keep], clean[r, keep].to(torch.float64).numpy(), k, v, rows.scale)
+
+
+@pytest.mark.parametrize("n", [1, 300])
+def test_values_that_are_infinite(n):
+    """An infinite value of a token with any weight makes its element of the result infinite, and no other."""
+    rng = np.random.Generator(np.random.PCG64(43 + n))
+    cache = ref.Cache(rng, 1, 128, 64, "bf16", [n])
+    at = n // 2
+    v = rng.standard_normal((1, 1, 128)).astype(np.float32)
+    v[0, 0, [5, 64]] = np.inf
+    v[0, 0, 77] = -np.inf
+    ab.put(cache, 0, [at], 1, v)
+    ab.put(cache, 0, [at], 0, np.zeros((1, 1, 128), np.float32))
+    rows = Rows(rng, cache, 24, [0] * ROWS)
+    assert rows.call(row_ke=torch.full((ROWS,), n, dtype=torch.int32, device=DEV)) == 0
+    out = rows.dev["out"].float().cpu().numpy()
+    assert np.array_equal(np.isposinf(out), np.broadcast_to(np.isin(np.arange(128), [5, 64]), out.shape))
+    assert np.array_equal(np.isneginf(out), np.broadcast_to(np.arange(128) == 77, out.shape))
+    finite = [i for i in range(128) if i not in (5, 64, 77)]
+    k, v = cache.tokens(0, np.arange(n))
+    want, mean, lse, size = ab.attend(rows.q[0].to(torch.float64).numpy(), k, np.where(np.isinf(v), 0, v), rows.scale)
+    off, lse_off = ab.bound(want, mean, size, 128, n)
+    assert (np.abs(out[0] - want) <= off)[:, finite].all()
+    assert (np.abs(rows.dev["lse"][0].cpu().numpy() - lse) <= lse_off + 2.0 ** -22 * np.abs(lse)).all()
