@@ -426,7 +426,8 @@ SMQ_API int sparse_mqa_quantize_q(const smq_plan *plan, const uint16_t *q, const
  * head h / (H / KVH). For a row with queries q[h] and a set of tokens T,
  *     s[h][t] = softmax_scale * q[h] . k[t]
  *     out[h]  = sum_t exp(s[h][t] - lse[h]) v[t],  lse[h] = log sum_t exp(s[h][t]).
- * A row without tokens gets out = 0 and lse = -infinity. Products are of the
+ * A row without tokens, or a head without a score above -infinity, gets
+ * out = 0 and lse = -infinity. Products are of the
  * bfloat16 queries and the cache's elements as they are; sums, maxima and
  * scores are fp32; a weight (times its token's value scale) enters the sum of
  * the values with 16 bits, whatever the other tokens' scales are. Keys and

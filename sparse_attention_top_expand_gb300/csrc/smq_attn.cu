@@ -1015,7 +1015,8 @@ __global__ void __launch_bounds__(Shape<D, kE4m3, N>::kThreads, 1) attention_ker
       }
 #pragma unroll
       for (int c = 0; c < C; ++c) l[c] = 0.f;
-      bool fresh = true;  // no token so far
+      bool fresh = true;  // some head has had no score above minus infinity so far
+      bool mine = wt < C && c0 + wt < p.group;  // the head that this thread keeps the maximum of is one of them
       for (int j = 0; j < sg.ntiles; ++j, ++it) {
         const int a = it % S::kRing;
         if (__builtin_expect(!s_ready, 0)) wait(kSFull + (it & 1), (it >> 1) & 1);
@@ -1075,12 +1076,13 @@ __global__ void __launch_bounds__(Shape<D, kE4m3, N>::kThreads, 1) attention_ker
           }
           if (wt < C) {
             const float top = fmaxf(fmaxf(red[wt], red[C + wt]), fmaxf(red[2 * C + wt], red[3 * C + wt]));
-            const float up = top == -INFINITY ? 0.f : first ? top : fmaxf(top, 0.f);
+            const float up = top == -INFINITY ? 0.f : mine ? top : fmaxf(top, 0.f);
             nm_s[c0 + wt] -= up;
             up_s[c0 + wt] = up;
-            alpha_s[c0 + wt] = first ? 0.f : ex2(-up);
+            alpha_s[c0 + wt] = mine ? 1.f : ex2(-up);  // nothing to rescale at a head's first scores
+            mine = mine && top == -INFINITY;
           }
-          bar_sync(bar_id, 128);
+          fresh = bar_or(bar_id, 128, mine);
 #pragma unroll
           for (int c = 0; c < C; c += 4) {
             const float4 a4 = *reinterpret_cast<const float4*>(alpha_s + c0 + c);
@@ -1088,7 +1090,6 @@ __global__ void __launch_bounds__(Shape<D, kE4m3, N>::kThreads, 1) attention_ker
             l[c] *= a4.x, l[c + 1] *= a4.y, l[c + 2] *= a4.z, l[c + 3] *= a4.w;
             s[c] -= u4.x, s[c + 1] -= u4.y, s[c + 2] -= u4.z, s[c + 3] -= u4.w;
           }
-          if (first) fresh = false;
         }
         // this thread's row of P: C heads of token t, in two parts
         uint32_t hi[kWords], lo[kWords];
@@ -1142,7 +1143,7 @@ __global__ void __launch_bounds__(Shape<D, kE4m3, N>::kThreads, 1) attention_ker
       if (wt < C) {
         const int h = c0 + wt;
         const float sum = red[wt] + red[C + wt] + red[2 * C + wt] + red[3 * C + wt];
-        const float m = fresh ? kUnset : -nm_s[h];
+        const float m = mine ? kUnset : -nm_s[h];
         nm_s[h] = 0.f;
         inv_s[h] = sum == 0.f ? 0.f : __fdividef(1.f, sum);
         if (h < p.group) {

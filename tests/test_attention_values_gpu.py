@@ -152,3 +152,46 @@ def test_values_that_are_infinite(n):
     off, lse_off = ab.bound(want, mean, size, 128, n)
     assert (np.abs(out[0] - want) <= off)[:, finite].all()
     assert (np.abs(rows.dev["lse"][0].cpu().numpy() - lse) <= lse_off + 2.0 ** -22 * np.abs(lse)).all()
+
+
+@pytest.mark.parametrize("first", [1, 128, 300])
+@pytest.mark.parametrize("heads", [3, 40])
+def test_scores_of_minus_infinity_before_others(first, heads):
+    """Tokens whose score is minus infinity for half of the heads have no weight there, also where a row begins with
+    whole tiles of them and what follows has scores far below zero."""
+    rng = np.random.Generator(np.random.PCG64(44))
+    n = 600
+    cache = ref.Cache(rng, 1, 128, 64, "bf16", [n])
+    k = rng.standard_normal((n, 1, 128)).astype(np.float32)
+    k[:, 0, 0] = 0
+    k[:first, 0, 0] = -np.inf
+    k[first:, 0, 1] = -300 * np.sqrt(128)
+    ab.put(cache, 0, np.arange(n), 0, k)
+    rows = Rows(rng, cache, heads, [0] * ROWS)
+    q = rows.q.clone()
+    q[:, :, 1] = 1
+    q[:, ::2, 0] = 1           # these heads: minus infinity first
+    q[:, 1::2, 0] = -1         # these: plus infinity, so NaN
+    _queries(rows, q)
+    assert rows.call(row_ke=torch.full((ROWS,), n, dtype=torch.int32, device=DEV)) == 0
+    out, lse = rows.dev["out"], rows.dev["lse"]
+    assert bool(torch.isnan(out[:, 1::2]).all())
+    keep = list(range(0, heads, 2))
+    kk, vv = cache.tokens(0, np.arange(first, n))
+    for r in (0, 77, ROWS - 1):
+        ab.check(out[r, keep], lse[r, keep], q[r, keep].to(torch.float64).numpy(), kk, vv, rows.scale)
+
+
+def test_scores_of_minus_infinity_alone():
+    """A head without a score above minus infinity has the result of a row without tokens."""
+    rng = np.random.Generator(np.random.PCG64(45))
+    cache = ref.Cache(rng, 1, 64, 64, "bf16", [400])
+    k = rng.standard_normal((400, 1, 64)).astype(np.float32)
+    k[:, 0, 0] = -np.inf
+    ab.put(cache, 0, np.arange(400), 0, k)
+    rows = Rows(rng, cache, 4, [0] * ROWS)
+    q = rows.q.clone()
+    q[:, :, 0] = 2
+    _queries(rows, q)
+    assert rows.call(row_ke=torch.full((ROWS,), 400, dtype=torch.int32, device=DEV)) == 0
+    assert bool((rows.dev["out"] == 0).all()) and bool(torch.isneginf(rows.dev["lse"]).all())
