@@ -23,6 +23,7 @@ import sparse_attention_top_expand_gb300 as smq
 
 HEADS, KV_HEADS, DIM, PAGE = 64, 1, 128, 64        # attention
 INDEX_HEADS, BLOCK, BLOCKS, TOPK = 64, 128, 32, 2048  # indexer
+CHUNK = 4096  # tokens of a prefill call
 
 
 class Step:
@@ -32,7 +33,7 @@ class Step:
         dev = torch.device("cuda", torch.cuda.current_device())
         g = torch.Generator(device=dev).manual_seed(seed)
         rows = len(lens)
-        self.attn = smq.AttentionPlan(HEADS, KV_HEADS, DIM, PAGE, max_rows=max(rows, 8192), cache_dtype=cache_dtype)
+        self.attn = smq.AttentionPlan(HEADS, KV_HEADS, DIM, PAGE, max_rows=max(rows, CHUNK), cache_dtype=cache_dtype)
         self.index = smq.Plan(INDEX_HEADS, PAGE, BLOCK, BLOCKS, TOPK, max_rows=rows)
         width = -(-longest // PAGE)
         pages = rows * width
@@ -67,8 +68,8 @@ class Step:
     def _prefill(self):
         """Fill the contexts with random keys and values, through the same calls."""
         for r, n in enumerate(self.lens.tolist()):
-            for start in range(0, n, 4096):
-                at = torch.arange(start, min(n, start + 4096), device=self.device)
+            for start in range(0, n, CHUNK):
+                at = torch.arange(start, min(n, start + CHUNK), device=self.device)
                 slots = self.slots(torch.full_like(at, r), at)
                 k, v = self.randn(len(at), KV_HEADS, DIM), self.randn(len(at), KV_HEADS, DIM)
                 smq.sparse_mqa_append_kv(self.attn, None, k, v, at, self.cos_sin, slots, workspace=self.ws_attn, **self.sides())
