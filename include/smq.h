@@ -491,7 +491,7 @@ typedef struct smq_append_args {
   const uint16_t *q;          /* device bf16, row t at q + t * q_stride: [H][D], 16-byte aligned; or NULL */
   const uint16_t *k;          /* device bf16, row t at k + t * k_stride: [KVH][D], 16-byte aligned */
   const uint16_t *v;          /* device bf16, row t at v + t * v_stride: [KVH][D], 16-byte aligned */
-  int64_t q_stride;           /* elements, multiples of 8 */
+  int64_t q_stride;           /* elements, multiples of 8, at least a row's */
   int64_t k_stride;
   int64_t v_stride;
   const int64_t *positions;   /* device [rows]; one outside the table raises SMQ_ERR_BOUNDS and skips
@@ -519,8 +519,8 @@ typedef struct smq_append_args {
 SMQ_API int sparse_mqa_append_kv(const smq_attn_plan *plan, const smq_append_args *args, void *stream);
 
 /* Attention rows. sparse_mqa_attention_decode takes T = the positions
- * [row_ks, row_ke) of the row's sequence (row_ks NULL: zero; a window of a
- * sliding layer otherwise). sparse_mqa_attention_selected takes T = the
+ * [row_ks, row_ke) of the row's sequence (row_ks NULL or negative: zero; a
+ * window of a sliding layer otherwise). sparse_mqa_attention_selected takes T = the
  * non-negative entries of token_ids[row][0 .. num_ids), positions in the row's
  * sequence such as topk_out of the indexer calls; -1 entries may stand
  * anywhere and an id listed twice counts twice. A position's page is
@@ -531,7 +531,7 @@ typedef struct smq_attention_args {
   uint32_t struct_size;
   int32_t rows;               /* R >= 0 */
   const uint16_t *q;          /* device bf16, row r at q + r * q_stride: [H][D], 16-byte aligned */
-  int64_t q_stride;           /* elements, a multiple of 8 */
+  int64_t q_stride;           /* elements, a multiple of 8, >= H * D */
   const void *k_cache;        /* device pages, 16-byte aligned */
   const void *v_cache;
   const float *k_scales;      /* device scales of an E4M3 cache, else NULL */

@@ -182,7 +182,8 @@ cudaError_t launch_append(const AppendParams& p, int head_dim, bool e4m3, int nu
   // A warp keeps the token's table row over its passes; with too few tokens to
   // fill the SMs the passes are spread over more warps instead, up to 16 warps
   // an SM (48 measured 31.6 against 32.3 us on the bf16 chunk, but 13.0 against
-  // 10.9 on the 8-bit one).
+  // 10.9 on the 8-bit one, whose 72 registers let an SM hold 28 warps: it then
+  // ran in two waves).
   int64_t parts = (static_cast<int64_t>(num_sms) * 16 + p.rows - 1) / p.rows;
   parts = parts < 1 ? 1 : parts > passes ? passes : parts;
   const int64_t warps = static_cast<int64_t>(p.rows) * parts;

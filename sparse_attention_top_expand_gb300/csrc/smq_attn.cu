@@ -27,7 +27,7 @@
 // Two E4M3 numbers for each lost what was below 2^-18 of the largest weight
 // times scale: a token of zero values, whose scale is 1, beside values of 1
 // then took 10 to 60 % of the result. It measured 97 against 127 us on 64 rows
-// of 4096 to 32768 tokens, and 60 against 69 us on 256 rows of 2048 selected.)
+// of 4096 to 32768 tokens, and 60 against 70 us on 256 rows of 2048 selected.)
 //
 // Split. The tiles of all items form one list, cut into equal ranges, one per
 // CTA and SM, whatever the rows' lengths are. A range that starts or ends
@@ -48,15 +48,17 @@
 //
 // Bounds (a plain copy reaches 6790 GB/s):
 //  - contexts of 4096 to 32768, 64 rows, 8 heads on each of 8 kv heads, bf16:
-//    700 to 708 us for 4.83 GB, 6.8 to 6.9 TB/s: DRAM.
-//  - 4096 rows of 2048 selected tokens, 64 heads on one kv head, bf16: 587 us.
+//    703 to 709 us for 4.83 GB, 6.8 to 6.9 TB/s: DRAM.
+//  - 4096 rows of 2048 selected tokens, 64 heads on one kv head, bf16: 588 us.
 //    Each tile's 64 KB come from L2 in 256-byte rows: 7.3 TB/s, where a kernel
-//    that only copies such rows into shared memory reaches 7.2 to 7.6.
+//    that only copies such rows into shared memory, by four warps, reaches 7.4.
 //  - 64 rows of such contexts, E4M3, 64 heads on one kv head: 127 us for 314 MB,
-//    2.5 TB/s; with 64 heads on 8 kv heads 653 us for 2.5 GB. A tile costs some
-//    7300 warp instructions at half of the issue slots and 128 KB of
-//    shared-memory traffic for the widening alone; without any loading or
-//    widening the rest of the first would still take 116 us, of the second 500.
+//    2.5 TB/s; with 64 heads on 8 kv heads 676 us for 2.5 GB. A tile costs some
+//    7500 warp instructions at half of the issue slots, and the widening alone
+//    128 KB of shared-memory traffic; without any loading or widening the rest of
+//    the first still took 116 us, of the second 500.
+//  - 128 heads on one kv head, the same contexts: 158 us over a bf16 cache, 168
+//    over an E4M3 one: the softmax, 64 heads a thread.
 //  - small calls: start-up (launch, three dependent loads to the first key, a
 //    tile's chain of copy, two products and softmax) and the join, 6 to 25 us.
 #include "smq_attn.cuh"
