@@ -195,3 +195,45 @@ def test_scores_of_minus_infinity_alone():
     _queries(rows, q)
     assert rows.call(row_ke=torch.full((ROWS,), 400, dtype=torch.int32, device=DEV)) == 0
     assert bool((rows.dev["out"] == 0).all()) and bool(torch.isneginf(rows.dev["lse"]).all())
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_every_code_of_an_8_bit_cache(dim):
+    """Rows of one token, whose result is its values and whose lse is its score: all 256 codes as values, and as keys
+    under queries of one element each. NaN codes stay NaN and touch nothing else."""
+    rng = np.random.Generator(np.random.PCG64(46))
+    seqs = 256 // dim
+    cache = ref.Cache(rng, 1, dim, 16, "e4m3", [1] * seqs)
+    codes = np.arange(256, dtype=np.uint8).reshape(seqs, 1, 1, dim)
+    for s in range(seqs):
+        for side in (0, 1):
+            ab.put(cache, s, [0], side, codes[s], np.full((1, 1), 0.375, np.float32))
+    rows = Rows(rng, cache, dim, list(range(seqs)), scale=0.5)
+    values = ref.e4m3_values(codes.reshape(seqs, dim)) * 0.375
+    # values: zero queries, so that every key's finite codes give a score of zero; NaN keys make every head NaN
+    _queries(rows, torch.zeros(seqs, dim, dim, dtype=torch.bfloat16))
+    assert rows.call(row_ke=torch.ones(seqs, dtype=torch.int32, device=DEV)) == 0
+    finite = [s for s in range(seqs) if np.isfinite(values[s]).all()]
+    for s in finite:
+        want = torch.from_numpy(values[s]).to(torch.bfloat16).expand(dim, dim)
+        assert torch.equal(rows.dev["out"][s].cpu(), want)
+        assert bool((rows.dev["lse"][s] == 0).all())
+    for s in set(range(seqs)) - set(finite):
+        assert bool(torch.isnan(rows.dev["out"][s]).all())
+    # the same with keys of zero: a NaN value is NaN in its element only
+    for s in range(seqs):
+        ab.put(cache, s, [0], 0, np.zeros((1, 1, dim), np.uint8), np.ones((1, 1), np.float32))
+    rows.dev.update(cache.to(DEV))
+    assert rows.call(row_ke=torch.ones(seqs, dtype=torch.int32, device=DEV)) == 0
+    for s in range(seqs):
+        want = torch.from_numpy(values[s]).to(torch.bfloat16).expand(dim, dim)
+        got = rows.dev["out"][s].cpu()
+        assert torch.equal(torch.isnan(got), torch.isnan(want)) and torch.equal(got.nan_to_num(), want.nan_to_num())
+    # keys: head h asks for element h alone
+    for s in range(seqs):
+        ab.put(cache, s, [0], 0, np.where(np.isnan(values[s]), 0, codes[s]).astype(np.uint8), np.full((1, 1), 0.375, np.float32))
+    rows.dev.update(cache.to(DEV))
+    _queries(rows, torch.eye(dim, dtype=torch.bfloat16).expand(seqs, dim, dim).contiguous())
+    assert rows.call(row_ke=torch.ones(seqs, dtype=torch.int32, device=DEV)) == 0
+    want = np.where(np.isnan(values), 0, values) * 0.5
+    assert (np.abs(rows.dev["lse"].cpu().numpy() - want) <= 2.0 ** -21 * np.abs(want)).all()
