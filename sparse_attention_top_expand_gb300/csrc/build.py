@@ -18,7 +18,7 @@ LIB = os.path.join(PKG, "libsmq.so")
 TRACE_LIB = os.path.join(PKG, "libsmq_trace.so")  # -DSMQ_TRACE: phase timestamps (include/smq_trace.h)
 SOURCES = ["smq_api.cu", "smq_kernels.cu", "smq_producers.cu", "smq_prefill.cu", "smq_attn_api.cu", "smq_append.cu",
            "smq_attn.cu"]
-HEADERS = ["smq_kernels.cuh", "smq_ptx.cuh", "smq_attn.cuh"]
+HEADERS = ["smq_kernels.cuh", "smq_ptx.cuh", "smq_attn.cuh", "smq_attn_ptx.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",
