@@ -31,7 +31,8 @@
  *    was enqueued.
  *  - Errors the GPU detects are OR-ed into a status word at the start of
  *    the workspace: an out-of-range page, block-table row or block id
- *    (SMQ_ERR_BOUNDS), or a pipeline wait that gave up (SMQ_ERR_TIMEOUT).
+ *    (SMQ_ERR_BOUNDS), a pipeline wait that gave up (SMQ_ERR_TIMEOUT), or too
+ *    few free pages (SMQ_ERR_NO_PAGES).
  *    The outputs of a call that raised one are unspecified.
  *    smq_get_status reads the word and clears it.
  *  - The arguments are checked once, at plan creation ("engine start").
@@ -84,7 +85,8 @@ typedef enum smq_status {
   SMQ_ERR_WORKSPACE_TOO_SMALL = 3, /* workspace_bytes < smq_workspace_size() */
   SMQ_ERR_CUDA = 4,                /* a CUDA runtime or driver call failed */
   SMQ_ERR_BOUNDS = 8,              /* device: page / row / block id out of range */
-  SMQ_ERR_TIMEOUT = 16             /* device: a pipeline wait gave up */
+  SMQ_ERR_TIMEOUT = 16,            /* device: a pipeline wait gave up */
+  SMQ_ERR_NO_PAGES = 32            /* device: a page was wanted and none was free */
 } smq_status;
 
 typedef struct smq_plan smq_plan;
@@ -167,7 +169,8 @@ SMQ_API int smq_workspace_init(const smq_plan *plan, void *workspace, size_t wor
                                void *stream);
 
 /* Synchronise `stream`, read the workspace status word into *code (a
- * bitwise OR of SMQ_ERR_BOUNDS / SMQ_ERR_TIMEOUT, or 0), then clear it. */
+ * bitwise OR of SMQ_ERR_BOUNDS / SMQ_ERR_TIMEOUT / SMQ_ERR_NO_PAGES, or 0),
+ * then clear it. */
 SMQ_API int smq_get_status(const void *workspace, void *stream, int32_t *code);
 
 SMQ_API const char *smq_error_string(int code);
@@ -556,6 +559,206 @@ typedef struct smq_attention_args {
 
 SMQ_API int sparse_mqa_attention_decode(const smq_attn_plan *plan, const smq_attention_args *args, void *stream);
 SMQ_API int sparse_mqa_attention_selected(const smq_attn_plan *plan, const smq_attention_args *args, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention of whole sequences' query rows over the same cache: several rows
+ * of a sequence share its keys and values.
+ *   sparse_mqa_attention_window  causal, with a sliding window and a few first
+ *                                tokens that stay visible (sinks): prefill
+ *                                chunks and decode steps of a sliding layer
+ *   sparse_mqa_attention_tree    a tree of drafted tokens: each row sees the
+ *                                context and its own ancestors
+ * Formulas, heads, cache and the treatment of infinities and NaN are those of
+ * sparse_mqa_attention_decode above; only the sets T differ. A weight enters
+ * the sum of the values with the 8 bits of a bfloat16. Keys and values of
+ * tokens that a row does not see are never used for it, whatever they hold,
+ * also where another row of the same sequence sees them.
+ *
+ * Sequence b has the query rows cu_rows[b] .. cu_rows[b + 1] - 1, in order, and
+ * seq_len[b] tokens in the cache, the tokens of those rows included: row i of n
+ * is the token at position seq_len[b] - n + i. Its pages are those of table row
+ * seq_indices[b] (b where NULL).
+ *   window: T = { t <= position : t < sinks or t > position - window }.
+ *   tree:   T = { t < seq_len - n } and { seq_len - n + j : bit j of the row's
+ *           mask }: bit j % 32 of word j / 32. A row sees its own token only if
+ *           its own bit says so; bits past n are not read.
+ * Tokens before position 0 do not exist; a row at a negative position of a
+ * window sees nothing. Rows at or past cu_rows[num_seqs] belong to no sequence
+ * and their out and lse are left as they were, as are those of a sequence that
+ * is refused: a sequence whose rows decrease, pass `rows` or are more than
+ * max_seq_rows raises SMQ_ERR_BOUNDS. A position past the block table, or a
+ * page or table row out of range (such as -1 for a page that was given back),
+ * where a row would see it, raises SMQ_ERR_BOUNDS and is left out.
+ * --------------------------------------------------------------------------- */
+typedef struct smq_seq_attention_args {
+  uint32_t struct_size;
+  int32_t rows;               /* rows of q, out and lse, 0 .. the plan's max_rows */
+  const uint16_t *q;          /* device bf16, row r at q + r * q_stride: [H][D], 16-byte aligned */
+  int64_t q_stride;           /* elements, a multiple of 8, >= H * D */
+  const void *k_cache;        /* device pages, 16-byte aligned */
+  const void *v_cache;
+  const float *k_scales;      /* device scales of an E4M3 cache, else NULL */
+  const float *v_scales;
+  int64_t num_pages;
+  int64_t page_stride;        /* elements, >= KVH * page_size * D, a multiple of 16 */
+  int64_t scale_page_stride;  /* floats, >= KVH * page_size (E4M3) */
+  const int32_t *block_table; /* device [bt_rows][bt_stride] page ids */
+  int32_t bt_rows;
+  int32_t bt_stride;
+  int32_t num_seqs;           /* sequences, 0 .. the plan's max_rows */
+  int32_t max_seq_rows;       /* no sequence has more rows: 1 .. the plan's max_rows */
+  const int32_t *seq_indices; /* device [num_seqs] sequence -> block-table row, or NULL = identity */
+  const int32_t *cu_rows;     /* device [num_seqs + 1] */
+  const int32_t *seq_len;     /* device [num_seqs] */
+  int32_t window;             /* window call: tokens that a row sees, its own included, >= 1; tree: 0 */
+  int32_t sinks;              /* window call: first tokens that stay visible, >= 0; tree: 0 */
+  const int32_t *tree_mask;   /* tree call: device [rows][mask_words]; window: NULL */
+  int32_t mask_words;         /* tree call: 1 .. 32, max_seq_rows <= 32 * mask_words; window: 0 */
+  uint16_t *out;              /* device [rows][H][D] bf16, 16-byte aligned */
+  float *lse;                 /* device [rows][H] natural log-sum-exp, or NULL */
+  void *workspace;            /* device, >= smq_seq_attention_workspace_size(plan), 16-byte aligned */
+  size_t workspace_bytes;
+} smq_seq_attention_args;
+
+/* Device workspace bytes of the two calls: the status word and partial results.
+ * It does not depend on rows or lengths. smq_attn_workspace_init zeroes its
+ * status word. Calls that overlap on the GPU need workspaces of their own. */
+SMQ_API int smq_seq_attention_workspace_size(const smq_attn_plan *plan, size_t *bytes);
+
+SMQ_API int sparse_mqa_attention_window(const smq_attn_plan *plan, const smq_seq_attention_args *args, void *stream);
+SMQ_API int sparse_mqa_attention_tree(const smq_attn_plan *plan, const smq_seq_attention_args *args, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * The pages of the paged caches: who holds them, and what moves between them.
+ *   sparse_mqa_pages_resize   take and give back pages, so that rows of the
+ *                             block table cover the tokens they are to hold
+ *   sparse_mqa_pages_fork     rows that share another row's pages
+ *   sparse_mqa_cache_compact  move the kept tokens of rows together
+ *
+ * The state is the caller's, on the device: a block table [table_rows]
+ * [table_columns] of page ids, -1 where a row has no page, and a count of
+ * holders for each page, page_refs [num_pages]. A page is free where its count
+ * is zero; a new state is a table of -1 and counts of 0. Column c of a row
+ * holds the row's positions [c * page_size, (c + 1) * page_size). The attention
+ * calls, the indexer's calls and the append read the same table.
+ *
+ * Results do not depend on timing: new pages are the lowest-numbered ones whose
+ * count was zero before the call, given out in the order in which rows are
+ * listed, then columns. A page that a call gives back is free for later calls,
+ * not for the same one. Where too few pages are free, SMQ_ERR_NO_PAGES is
+ * raised and the entries past the last page stay -1.
+ *
+ * Rows are listed: distinct rows of the table. One out of range, or listed
+ * again, raises SMQ_ERR_BOUNDS and is skipped. Any negative entry is no page. An
+ * entry past the pool, and a count that would pass below zero, raise
+ * SMQ_ERR_BOUNDS and change no count.
+ * --------------------------------------------------------------------------- */
+typedef struct smq_page_plan smq_page_plan;
+
+typedef struct smq_page_plan_desc {
+  uint32_t struct_size;
+  int32_t page_size;      /* tokens per page, 1 .. 65536 */
+  int64_t num_pages;      /* pages of the pool, 1 .. 2^31 - 1 */
+  int32_t table_rows;     /* rows of the block table, 1 .. 8192 */
+  int32_t table_columns;  /* columns of the block table, 1 .. 1048576 */
+  int32_t device;         /* CUDA device ordinal the plan runs on */
+} smq_page_plan_desc;
+
+SMQ_API int smq_page_plan_create(const smq_page_plan_desc *desc, smq_page_plan **plan);
+SMQ_API int smq_page_plan_destroy(smq_page_plan *plan);
+
+/* Device workspace bytes of every call with this plan. smq_page_workspace_init
+ * zeroes the status word, smq_get_status reads it. Calls that overlap on the
+ * GPU need workspaces of their own (and may not share a state). */
+SMQ_API int smq_page_workspace_size(const smq_page_plan *plan, size_t *bytes);
+SMQ_API int smq_page_workspace_init(const smq_page_plan *plan, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Row rows[i] (i where NULL) is to cover the positions [begin, end): begin =
+ * row_begin[i] (0 where NULL), end = row_end[i], both as many as the table's
+ * row holds at most (more raises SMQ_ERR_BOUNDS), negative as 0. The first
+ * keep_first positions stay too, as far as they are below end: the sinks of a
+ * sliding layer. Wanted columns without a page take one; the others give
+ * theirs back and become -1. row_end = 0 frees a row. */
+typedef struct smq_pages_resize_args {
+  uint32_t struct_size;
+  int32_t num_rows;           /* 0 .. table_rows */
+  int32_t *block_table;       /* device [table_rows][table_columns], in and out */
+  int32_t *page_refs;         /* device [num_pages], in and out */
+  const int32_t *rows;        /* device [num_rows], or NULL */
+  const int32_t *row_begin;   /* device [num_rows], or NULL */
+  const int32_t *row_end;     /* device [num_rows] */
+  int32_t keep_first;         /* >= 0 */
+  void *workspace;            /* device, 16-byte aligned */
+  size_t workspace_bytes;
+} smq_pages_resize_args;
+
+SMQ_API int sparse_mqa_pages_resize(const smq_page_plan *plan, const smq_pages_resize_args *args, void *stream);
+
+/* One thing that a page holds: page p at base + p * page_stride bytes, as
+ * `vectors` runs (kv heads) of page_size tokens of token_bytes bytes. Keys,
+ * values and scales of an attention cache are planes with KVH vectors; the
+ * indexer's MXFP4 pages are two planes of one vector each: values of 64 bytes a
+ * token at offset 0 and scales of 4 bytes a token at offset 64 * page_size. */
+typedef struct smq_page_plane {
+  void *base;             /* device, 4-byte aligned */
+  int64_t page_stride;    /* bytes, a multiple of 4, >= vectors * page_size * token_bytes */
+  int32_t vectors;        /* >= 1 */
+  int32_t token_bytes;    /* a multiple of 4 */
+} smq_page_plane;
+
+enum { SMQ_MAX_PLANES = 8 };
+
+/* Fork i makes row dst_rows[i] one that shares the first row_len[i] tokens of
+ * row src_rows[i], as the rows were before the call: it holds the source's
+ * whole pages too, and a new page with a copy of the tokens of the page that
+ * row_len[i] ends inside, in every plane. Its other entries become -1, and what
+ * it held before is given back. Columns without a page at the source (given
+ * back by a window) have none in the fork. Destinations are the listed rows;
+ * sources may repeat, and may be destinations themselves, so beams can change
+ * places. A row forked onto itself stays as it is. A row_len past the table's
+ * row raises SMQ_ERR_BOUNDS and is cut there; a negative one is 0. */
+typedef struct smq_pages_fork_args {
+  uint32_t struct_size;
+  int32_t num_rows;           /* 0 .. table_rows */
+  int32_t *block_table;       /* device [table_rows][table_columns], in and out */
+  int32_t *page_refs;         /* device [num_pages], in and out */
+  const int32_t *src_rows;    /* device [num_rows] */
+  const int32_t *dst_rows;    /* device [num_rows] */
+  const int32_t *row_len;     /* device [num_rows] tokens */
+  const smq_page_plane *planes; /* host [num_planes], read during the call */
+  int32_t num_planes;         /* 0 .. SMQ_MAX_PLANES */
+  void *workspace;            /* device, 16-byte aligned */
+  size_t workspace_bytes;
+} smq_pages_fork_args;
+
+SMQ_API int sparse_mqa_pages_fork(const smq_page_plan *plan, const smq_pages_fork_args *args, void *stream);
+
+/* In row rows[i] (i where NULL), token keep_ids[i][j] moves to position
+ * row_start[i] + j, in every plane: the accepted path of a tree, the tokens
+ * that an eviction keeps. keep_ids[i] ascends strictly, has its first entry at
+ * or past row_start[i] >= 0, and ends at its first negative entry. Tokens that
+ * move may come from places that others move to. The table does not change;
+ * sparse_mqa_pages_resize gives back what is behind. A row is moved whole or
+ * not at all: a list that does not ascend, a position past the table, a page out
+ * of range or a destination page with more than one holder raises SMQ_ERR_BOUNDS,
+ * and the row stays as it is. A page that two listed rows hold is only read. */
+typedef struct smq_cache_compact_args {
+  uint32_t struct_size;
+  int32_t num_rows;           /* 0 .. table_rows */
+  const int32_t *block_table; /* device [table_rows][table_columns] */
+  const int32_t *page_refs;   /* device [num_pages] */
+  const int32_t *rows;        /* device [num_rows], or NULL */
+  const int32_t *row_start;   /* device [num_rows] */
+  const int32_t *keep_ids;    /* device [num_rows][keep_ld] */
+  int32_t num_keep;           /* 1 .. 1048576 */
+  int32_t keep_ld;            /* >= num_keep */
+  const smq_page_plane *planes; /* host [num_planes], read during the call */
+  int32_t num_planes;         /* 1 .. SMQ_MAX_PLANES */
+  void *workspace;            /* device, 16-byte aligned */
+  size_t workspace_bytes;
+} smq_cache_compact_args;
+
+SMQ_API int sparse_mqa_cache_compact(const smq_page_plan *plan, const smq_cache_compact_args *args, void *stream);
 
 #ifdef __cplusplus
 }

@@ -27,6 +27,8 @@ SMQ_ERR_WORKSPACE_TOO_SMALL = 3
 SMQ_ERR_CUDA = 4
 SMQ_ERR_BOUNDS = 8
 SMQ_ERR_TIMEOUT = 16
+SMQ_ERR_NO_PAGES = 32
+SMQ_MAX_PLANES = 8
 SMQ_NOALLOC_SCRATCH_BYTES = 8 << 20  # logits scratch of sparse_mqa_logits_topk_decode_noalloc
 
 _c_i32 = ctypes.c_int32
@@ -96,6 +98,43 @@ class SMQAttentionArgs(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t)]
 
 
+class SMQSeqAttentionArgs(ctypes.Structure):
+    _fields_ = [("struct_size", _c_u32), ("rows", _c_i32), ("q", _vp), ("q_stride", _c_i64), ("k_cache", _vp),
+                ("v_cache", _vp), ("k_scales", _vp), ("v_scales", _vp), ("num_pages", _c_i64), ("page_stride", _c_i64),
+                ("scale_page_stride", _c_i64), ("block_table", _vp), ("bt_rows", _c_i32), ("bt_stride", _c_i32),
+                ("num_seqs", _c_i32), ("max_seq_rows", _c_i32), ("seq_indices", _vp), ("cu_rows", _vp), ("seq_len", _vp),
+                ("window", _c_i32), ("sinks", _c_i32), ("tree_mask", _vp), ("mask_words", _c_i32), ("out", _vp),
+                ("lse", _vp), ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class SMQPagePlanDesc(ctypes.Structure):
+    _fields_ = [("struct_size", _c_u32), ("page_size", _c_i32), ("num_pages", _c_i64), ("table_rows", _c_i32),
+                ("table_columns", _c_i32), ("device", _c_i32)]
+
+
+class SMQPagePlane(ctypes.Structure):
+    _fields_ = [("base", _vp), ("page_stride", _c_i64), ("vectors", _c_i32), ("token_bytes", _c_i32)]
+
+
+class SMQPagesResizeArgs(ctypes.Structure):
+    _fields_ = [("struct_size", _c_u32), ("num_rows", _c_i32), ("block_table", _vp), ("page_refs", _vp), ("rows", _vp),
+                ("row_begin", _vp), ("row_end", _vp), ("keep_first", _c_i32), ("workspace", _vp),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
+class SMQPagesForkArgs(ctypes.Structure):
+    _fields_ = [("struct_size", _c_u32), ("num_rows", _c_i32), ("block_table", _vp), ("page_refs", _vp), ("src_rows", _vp),
+                ("dst_rows", _vp), ("row_len", _vp), ("planes", ctypes.POINTER(SMQPagePlane)), ("num_planes", _c_i32),
+                ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class SMQCacheCompactArgs(ctypes.Structure):
+    _fields_ = [("struct_size", _c_u32), ("num_rows", _c_i32), ("block_table", _vp), ("page_refs", _vp), ("rows", _vp),
+                ("row_start", _vp), ("keep_ids", _vp), ("num_keep", _c_i32), ("keep_ld", _c_i32),
+                ("planes", ctypes.POINTER(SMQPagePlane)), ("num_planes", _c_i32), ("workspace", _vp),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
 EXPORTED = [
     "smq_plan_create", "smq_plan_destroy", "smq_plan_get_info", "smq_workspace_size", "smq_workspace_init",
     "smq_prefill_workspace_size",
@@ -106,6 +145,9 @@ EXPORTED = [
     "smq_attn_plan_create", "smq_attn_plan_destroy", "smq_attn_plan_set_wait_limit", "smq_attn_plan_inject_stall",
     "smq_attn_workspace_size", "smq_attn_workspace_init", "sparse_mqa_append_kv", "sparse_mqa_attention_decode",
     "sparse_mqa_attention_selected",
+    "smq_seq_attention_workspace_size", "sparse_mqa_attention_window", "sparse_mqa_attention_tree",
+    "smq_page_plan_create", "smq_page_plan_destroy", "smq_page_workspace_size", "smq_page_workspace_init",
+    "sparse_mqa_pages_resize", "sparse_mqa_pages_fork", "sparse_mqa_cache_compact",
 ]
 
 _lib = None
@@ -150,6 +192,16 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.sparse_mqa_append_kv.argtypes = [_vp, P(SMQAppendArgs), _vp]
     lib.sparse_mqa_attention_decode.argtypes = [_vp, P(SMQAttentionArgs), _vp]
     lib.sparse_mqa_attention_selected.argtypes = [_vp, P(SMQAttentionArgs), _vp]
+    lib.smq_seq_attention_workspace_size.argtypes = [_vp, P(ctypes.c_size_t)]
+    lib.sparse_mqa_attention_window.argtypes = [_vp, P(SMQSeqAttentionArgs), _vp]
+    lib.sparse_mqa_attention_tree.argtypes = [_vp, P(SMQSeqAttentionArgs), _vp]
+    lib.smq_page_plan_create.argtypes = [P(SMQPagePlanDesc), P(_vp)]
+    lib.smq_page_plan_destroy.argtypes = [_vp]
+    lib.smq_page_workspace_size.argtypes = [_vp, P(ctypes.c_size_t)]
+    lib.smq_page_workspace_init.argtypes = [_vp, _vp, ctypes.c_size_t, _vp]
+    lib.sparse_mqa_pages_resize.argtypes = [_vp, P(SMQPagesResizeArgs), _vp]
+    lib.sparse_mqa_pages_fork.argtypes = [_vp, P(SMQPagesForkArgs), _vp]
+    lib.sparse_mqa_cache_compact.argtypes = [_vp, P(SMQCacheCompactArgs), _vp]
     for name in EXPORTED:
         if name != "smq_error_string":
             getattr(lib, name).restype = ctypes.c_int
@@ -535,6 +587,18 @@ class AttentionPlan:
         smq_attn_workspace_init(self, ws, stream)
         return ws
 
+    def sequence_workspace_size(self) -> int:
+        n = ctypes.c_size_t()
+        _check(load_library().smq_seq_attention_workspace_size(self.handle, ctypes.byref(n)),
+               "smq_seq_attention_workspace_size")
+        return n.value
+
+    def sequence_workspace(self, stream=None) -> torch.Tensor:
+        """The same for sparse_mqa_attention_window and sparse_mqa_attention_tree."""
+        ws = torch.empty(self.sequence_workspace_size(), dtype=torch.uint8, device=self.device)
+        smq_attn_workspace_init(self, ws, stream)
+        return ws
+
     def close(self) -> None:
         if getattr(self, "handle", None):
             load_library().smq_attn_plan_destroy(self.handle)
@@ -723,3 +787,306 @@ class AttentionCall:
         rc = self._fn(self.plan.handle, self._ref, _stream(stream))
         if rc != 0:
             _check(rc, self._name)
+
+
+# ---------------------------------------------------------------------------
+# Attention of whole sequences' query rows: a sliding window, a drafted tree.
+
+
+def _seq_attention_args(plan: AttentionPlan, q, k_cache, v_cache, block_table, cu_rows, seq_len, max_seq_rows, out, workspace,
+                        window, sinks, tree_mask, seq_indices, lse, k_scales, v_scales):
+    dev = plan.device
+    a = SMQSeqAttentionArgs()
+    a.struct_size = ctypes.sizeof(SMQSeqAttentionArgs)
+    a.rows = rows = int(q.shape[0])
+    a.q, a.q_stride = _inner_ptr(q, (torch.bfloat16,), "q", dev, (plan.num_heads, plan.head_dim))
+    _set_cache(a, plan, k_cache, v_cache, k_scales, v_scales)
+    a.block_table = _ptr(block_table, _I32, "block_table", dev)
+    a.bt_rows = int(block_table.shape[0])
+    a.bt_stride = int(block_table.shape[1])
+    a.num_seqs = seqs = int(seq_len.shape[0])
+    a.max_seq_rows = int(max_seq_rows)
+    a.seq_indices = _ptr(seq_indices, _I32, "seq_indices", dev)
+    a.cu_rows = _ptr(cu_rows, _I32, "cu_rows", dev)
+    a.seq_len = _ptr(seq_len, _I32, "seq_len", dev)
+    _shaped(seq_len, "seq_len", (seqs,))
+    _shaped(cu_rows, "cu_rows", (seqs + 1,))
+    _shaped(seq_indices, "seq_indices", (seqs,))
+    if seq_indices is None and a.bt_rows < seqs:
+        raise ValueError("block_table needs a row for each sequence, or seq_indices")
+    if tree_mask is None:
+        a.window, a.sinks = int(window), int(sinks)
+    else:
+        a.tree_mask = _ptr(tree_mask, _I32, "tree_mask", dev)
+        _shaped(tree_mask, "tree_mask", (rows, tree_mask.shape[-1]))
+        a.mask_words = int(tree_mask.shape[-1])
+    a.out = _ptr(out, (torch.bfloat16,), "out", dev)
+    _shaped(out, "out", q.shape)
+    a.lse = _ptr(lse, _F32, "lse", dev)
+    _shaped(lse, "lse", (rows, plan.num_heads))
+    a.workspace = _ptr(workspace, _U8, "workspace", dev)
+    a.workspace_bytes = workspace.numel()
+    return a
+
+
+def sparse_mqa_attention_window(plan: AttentionPlan, q, k_cache, v_cache, block_table, cu_rows, seq_len, max_seq_rows: int, out,
+                                workspace, window: int, sinks: int = 0, seq_indices=None, lse=None, k_scales=None,
+                                v_scales=None, stream=None) -> None:
+    """Causal attention of the query rows q [R, H, D] (bf16) of sequences: sequence b has rows cu_rows[b] to
+    cu_rows[b + 1] (int32 [S + 1]), the last of its seq_len[b] (int32 [S]) cached tokens. A row sees the `window` tokens up to
+    its own, and the first `sinks` of the sequence. No sequence has more than max_seq_rows rows."""
+    a = _seq_attention_args(plan, q, k_cache, v_cache, block_table, cu_rows, seq_len, max_seq_rows, out, workspace, window, sinks,
+                            None, seq_indices, lse, k_scales, v_scales)
+    _check(load_library().sparse_mqa_attention_window(plan.handle, ctypes.byref(a), _stream(stream)),
+           "sparse_mqa_attention_window")
+
+
+def sparse_mqa_attention_tree(plan: AttentionPlan, q, k_cache, v_cache, block_table, cu_rows, seq_len, max_seq_rows: int, out,
+                              workspace, tree_mask, seq_indices=None, lse=None, k_scales=None, v_scales=None,
+                              stream=None) -> None:
+    """Attention of drafted tokens: as sparse_mqa_attention_window, but a row of a sequence of n rows sees the
+    seq_len[b] - n tokens before them, and of the n those whose bits are set in its tree_mask [R, words] (int32)."""
+    if tree_mask is None:
+        raise ValueError("tree_mask is needed")
+    a = _seq_attention_args(plan, q, k_cache, v_cache, block_table, cu_rows, seq_len, max_seq_rows, out, workspace, 0, 0,
+                            tree_mask, seq_indices, lse, k_scales, v_scales)
+    _check(load_library().sparse_mqa_attention_tree(plan.handle, ctypes.byref(a), _stream(stream)),
+           "sparse_mqa_attention_tree")
+
+
+class SequenceAttentionCall:
+    """sparse_mqa_attention_window (with window) or sparse_mqa_attention_tree (with tree_mask) with its arguments
+    marshalled once, as DecodeCall does for the indexer."""
+
+    def __init__(self, plan: AttentionPlan, q, k_cache, v_cache, block_table, cu_rows, seq_len, max_seq_rows: int, out,
+                 workspace, window: Optional[int] = None, sinks: int = 0, tree_mask=None, seq_indices=None, lse=None,
+                 k_scales=None, v_scales=None):
+        if (window is None) == (tree_mask is None) or (tree_mask is not None and sinks != 0):
+            raise ValueError("give window (and sinks) or tree_mask")
+        self.plan = plan
+        self.args = _seq_attention_args(plan, q, k_cache, v_cache, block_table, cu_rows, seq_len, max_seq_rows, out, workspace,
+                                        window, sinks, tree_mask, seq_indices, lse, k_scales, v_scales)
+        self._keep = (q, k_cache, v_cache, block_table, cu_rows, seq_len, out, workspace, tree_mask, seq_indices, lse, k_scales,
+                      v_scales)
+        self._name = "sparse_mqa_attention_window" if tree_mask is None else "sparse_mqa_attention_tree"
+        self._fn = getattr(load_library(), self._name)
+        self._ref = ctypes.byref(self.args)
+
+    def __call__(self, stream=None) -> None:
+        rc = self._fn(self.plan.handle, self._ref, _stream(stream))
+        if rc != 0:
+            _check(rc, self._name)
+
+
+# ---------------------------------------------------------------------------
+# Pages of the caches: counts of holders, the block table, and what moves.
+
+
+class PagePlan:
+    """The geometry of a pool of pages and of a block table (smq_page_plan_create); close() or GC frees it.
+
+    The state is two int32 tensors of the caller: page_refs [num_pages], zero where a page is free, and block_table
+    [table_rows, table_columns], -1 where a row has no page. state() makes an empty one."""
+
+    def __init__(self, page_size: int, num_pages: int, table_rows: int, table_columns: int, device: Optional[int] = None):
+        lib = load_library()
+        if device is None:
+            device = torch.cuda.current_device()
+        self.device_index = int(device)
+        self.device = torch.device("cuda", self.device_index)
+        d = SMQPagePlanDesc(ctypes.sizeof(SMQPagePlanDesc), page_size, num_pages, table_rows, table_columns, self.device_index)
+        h = _vp()
+        _check(lib.smq_page_plan_create(ctypes.byref(d), ctypes.byref(h)), "smq_page_plan_create")
+        self.handle = h
+        self.page_size = page_size
+        self.num_pages = num_pages
+        self.table_rows = table_rows
+        self.table_columns = table_columns
+
+    def state(self):
+        """An empty state: (page_refs, block_table), every page free."""
+        return (torch.zeros(self.num_pages, dtype=torch.int32, device=self.device),
+                torch.full((self.table_rows, self.table_columns), -1, dtype=torch.int32, device=self.device))
+
+    def workspace_size(self) -> int:
+        n = ctypes.c_size_t()
+        _check(load_library().smq_page_workspace_size(self.handle, ctypes.byref(n)), "smq_page_workspace_size")
+        return n.value
+
+    def workspace(self, stream=None) -> torch.Tensor:
+        """Allocate (here, by torch) and initialise a workspace for this plan's calls."""
+        ws = torch.empty(self.workspace_size(), dtype=torch.uint8, device=self.device)
+        smq_page_workspace_init(self, ws, stream)
+        return ws
+
+    def close(self) -> None:
+        if getattr(self, "handle", None):
+            load_library().smq_page_plan_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def smq_page_workspace_init(plan: PagePlan, workspace: torch.Tensor, stream=None) -> None:
+    _check(load_library().smq_page_workspace_init(plan.handle, _ptr(workspace, _U8, "workspace", plan.device),
+                                                  workspace.numel(), _stream(stream)), "smq_page_workspace_init")
+
+
+def indexer_planes(plan: Plan, k_cache: torch.Tensor):
+    """The indexer's MXFP4 cache [pages, page_bytes] (uint8) as two planes of its pages: values and scales."""
+    if k_cache.dtype != torch.uint8 or k_cache.dim() != 2 or k_cache.shape[1] != plan.page_bytes or k_cache.stride(1) != 1:
+        raise ValueError(f"k_cache must be uint8 [pages, {plan.page_bytes}], contiguous within a page")
+    size = plan.page_size
+    per = plan.head_dim // 2
+    return [k_cache[:, :size * per].unflatten(1, (1, size, per)), k_cache[:, size * per:].unflatten(1, (1, size, -1))]
+
+
+def _planes(plan: PagePlan, planes):
+    """Tensors [pages, vectors, page_size, ...], contiguous within a page, as the library's planes."""
+    if len(planes) > SMQ_MAX_PLANES:
+        raise ValueError(f"{len(planes)} planes, at most {SMQ_MAX_PLANES}")
+    got = (SMQPagePlane * max(1, len(planes)))()
+    for i, t in enumerate(planes):
+        name = f"planes[{i}]"
+        if t.dim() < 3 or t.shape[0] != plan.num_pages or t.shape[2] != plan.page_size:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{plan.num_pages}, vectors, {plan.page_size}, ...]")
+        ptr, stride = _inner_ptr(t, (t.dtype,), name, plan.device, t.shape[1:])
+        size = t.element_size()
+        token = size
+        for n in t.shape[3:]:
+            token *= int(n)
+        if token % 4 or (stride * size) % 4 or ptr % 4:
+            raise ValueError(f"{name}: tokens and pages must be whole 4-byte words, 4-byte aligned")
+        got[i] = SMQPagePlane(ptr, stride * size, int(t.shape[1]), token)
+    return got
+
+
+def _state(a, plan: PagePlan, page_refs, block_table, workspace) -> None:
+    dev = plan.device
+    a.block_table = _ptr(block_table, _I32, "block_table", dev)
+    a.page_refs = _ptr(page_refs, _I32, "page_refs", dev)
+    _shaped(block_table, "block_table", (plan.table_rows, plan.table_columns))
+    _shaped(page_refs, "page_refs", (plan.num_pages,))
+    a.workspace = _ptr(workspace, _U8, "workspace", dev)
+    a.workspace_bytes = workspace.numel()
+
+
+def _listed_rows(plan: PagePlan, rows, count):
+    _shaped(rows, "rows", (count,))
+    if rows is None and count > plan.table_rows:
+        raise ValueError(f"{count} rows, but the table has {plan.table_rows}")
+    return _ptr(rows, _I32, "rows", plan.device)
+
+
+def _resize_args(plan: PagePlan, page_refs, block_table, row_end, workspace, row_begin, keep_first, rows):
+    a = SMQPagesResizeArgs()
+    a.struct_size = ctypes.sizeof(SMQPagesResizeArgs)
+    a.num_rows = int(row_end.shape[0])
+    _state(a, plan, page_refs, block_table, workspace)
+    a.rows = _listed_rows(plan, rows, a.num_rows)
+    a.row_end = _ptr(row_end, _I32, "row_end", plan.device)
+    a.row_begin = _ptr(row_begin, _I32, "row_begin", plan.device)
+    _shaped(row_end, "row_end", (a.num_rows,))
+    _shaped(row_begin, "row_begin", (a.num_rows,))
+    a.keep_first = int(keep_first)
+    return a
+
+
+def sparse_mqa_pages_resize(plan: PagePlan, page_refs, block_table, row_end, workspace, row_begin=None, keep_first: int = 0,
+                            rows=None, stream=None) -> None:
+    """Give row rows[i] (row i where None) of block_table the pages for positions row_begin[i] (0 where None) to row_end[i]
+    (int32), and for its first keep_first positions; pages of other positions are given back."""
+    a = _resize_args(plan, page_refs, block_table, row_end, workspace, row_begin, keep_first, rows)
+    _check(load_library().sparse_mqa_pages_resize(plan.handle, ctypes.byref(a), _stream(stream)), "sparse_mqa_pages_resize")
+
+
+def _fork_args(plan: PagePlan, page_refs, block_table, src_rows, dst_rows, row_len, planes, workspace):
+    a = SMQPagesForkArgs()
+    a.struct_size = ctypes.sizeof(SMQPagesForkArgs)
+    a.num_rows = int(dst_rows.shape[0])
+    _state(a, plan, page_refs, block_table, workspace)
+    for name, t in (("src_rows", src_rows), ("dst_rows", dst_rows), ("row_len", row_len)):
+        _shaped(t, name, (a.num_rows,))
+        setattr(a, name, _ptr(t, _I32, name, plan.device))
+    a.planes = _planes(plan, planes)
+    a.num_planes = len(planes)
+    return a
+
+
+def sparse_mqa_pages_fork(plan: PagePlan, page_refs, block_table, src_rows, dst_rows, row_len, planes, workspace,
+                          stream=None) -> None:
+    """Make row dst_rows[i] of block_table share the first row_len[i] tokens of row src_rows[i] (int32 each): whole pages are
+    shared, the page that row_len[i] ends inside is copied, in every one of planes, tensors [num_pages, vectors, page_size,
+    ...] such as a cache's keys, values and scales."""
+    a = _fork_args(plan, page_refs, block_table, src_rows, dst_rows, row_len, planes, workspace)
+    _check(load_library().sparse_mqa_pages_fork(plan.handle, ctypes.byref(a), _stream(stream)), "sparse_mqa_pages_fork")
+
+
+def _compact_args(plan: PagePlan, page_refs, block_table, row_start, keep_ids, planes, workspace, rows):
+    a = SMQCacheCompactArgs()
+    a.struct_size = ctypes.sizeof(SMQCacheCompactArgs)
+    a.num_rows = int(row_start.shape[0])
+    _state(a, plan, page_refs, block_table, workspace)
+    a.rows = _listed_rows(plan, rows, a.num_rows)
+    a.row_start = _ptr(row_start, _I32, "row_start", plan.device)
+    a.keep_ids = _ptr(keep_ids, _I32, "keep_ids", plan.device)
+    _shaped(row_start, "row_start", (a.num_rows,))
+    _shaped(keep_ids, "keep_ids", (a.num_rows, keep_ids.shape[-1]))
+    a.num_keep = a.keep_ld = int(keep_ids.shape[-1])
+    a.planes = _planes(plan, planes)
+    a.num_planes = len(planes)
+    return a
+
+
+def sparse_mqa_cache_compact(plan: PagePlan, page_refs, block_table, row_start, keep_ids, planes, workspace, rows=None,
+                             stream=None) -> None:
+    """Move token keep_ids[i][j] (int32 [rows, K], ascending, ended by -1) of row rows[i] (row i where None) to position
+    row_start[i] + j, in every one of planes (as sparse_mqa_pages_fork)."""
+    a = _compact_args(plan, page_refs, block_table, row_start, keep_ids, planes, workspace, rows)
+    _check(load_library().sparse_mqa_cache_compact(plan.handle, ctypes.byref(a), _stream(stream)), "sparse_mqa_cache_compact")
+
+
+class _PagesCall:
+    """A page call with its arguments marshalled once, as DecodeCall does for the indexer."""
+
+    def __init__(self, plan: PagePlan, name: str, args, keep):
+        self.plan, self.args, self._name, self._keep = plan, args, name, keep
+        self._fn = getattr(load_library(), name)
+        self._ref = ctypes.byref(args)
+
+    def __call__(self, stream=None) -> None:
+        rc = self._fn(self.plan.handle, self._ref, _stream(stream))
+        if rc != 0:
+            _check(rc, self._name)
+
+
+class ResizeCall(_PagesCall):
+    """sparse_mqa_pages_resize with its arguments marshalled once."""
+
+    def __init__(self, plan: PagePlan, page_refs, block_table, row_end, workspace, row_begin=None, keep_first: int = 0,
+                 rows=None):
+        super().__init__(plan, "sparse_mqa_pages_resize",
+                         _resize_args(plan, page_refs, block_table, row_end, workspace, row_begin, keep_first, rows),
+                         (page_refs, block_table, row_end, workspace, row_begin, rows))
+
+
+class ForkCall(_PagesCall):
+    """sparse_mqa_pages_fork with its arguments marshalled once."""
+
+    def __init__(self, plan: PagePlan, page_refs, block_table, src_rows, dst_rows, row_len, planes, workspace):
+        super().__init__(plan, "sparse_mqa_pages_fork",
+                         _fork_args(plan, page_refs, block_table, src_rows, dst_rows, row_len, planes, workspace),
+                         (page_refs, block_table, src_rows, dst_rows, row_len, planes, workspace))
+
+
+class CompactCall(_PagesCall):
+    """sparse_mqa_cache_compact with its arguments marshalled once."""
+
+    def __init__(self, plan: PagePlan, page_refs, block_table, row_start, keep_ids, planes, workspace, rows=None):
+        super().__init__(plan, "sparse_mqa_cache_compact",
+                         _compact_args(plan, page_refs, block_table, row_start, keep_ids, planes, workspace, rows),
+                         (page_refs, block_table, row_start, keep_ids, planes, workspace, rows))

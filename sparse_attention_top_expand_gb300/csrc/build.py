@@ -17,8 +17,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsmq.so")
 TRACE_LIB = os.path.join(PKG, "libsmq_trace.so")  # -DSMQ_TRACE: phase timestamps (include/smq_trace.h)
 SOURCES = ["smq_api.cu", "smq_kernels.cu", "smq_producers.cu", "smq_prefill.cu", "smq_attn_api.cu", "smq_append.cu",
-           "smq_attn.cu"]
-HEADERS = ["smq_kernels.cuh", "smq_ptx.cuh", "smq_attn.cuh", "smq_attn_ptx.cuh"]
+           "smq_attn.cu", "smq_seq_attn.cu", "smq_pages_api.cu", "smq_pages.cu"]
+HEADERS = ["smq_kernels.cuh", "smq_ptx.cuh", "smq_attn.cuh", "smq_attn_ptx.cuh", "smq_pages.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",

@@ -333,6 +333,8 @@ SMQ_API const char* smq_error_string(int code) {
     case SMQ_ERR_BOUNDS: return "device: index out of range";
     case SMQ_ERR_TIMEOUT: return "device: pipeline wait timed out";
     case SMQ_ERR_BOUNDS | SMQ_ERR_TIMEOUT: return "device: index out of range and pipeline wait timed out";
+    case SMQ_ERR_NO_PAGES: return "device: too few free pages";
+    case SMQ_ERR_BOUNDS | SMQ_ERR_NO_PAGES: return "device: index out of range and too few free pages";
     default: return "unknown status";
   }
 }

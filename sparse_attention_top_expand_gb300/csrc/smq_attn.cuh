@@ -80,8 +80,45 @@ struct AttnParams {
   int32_t stall_tile;
 };
 
+// Attention of sequences' query rows (smq_seq_attn.cu): a sliding window with
+// sinks, or a tree of drafted tokens.
+struct SeqAttnParams {
+  int32_t rows;
+  int32_t kv_heads;
+  int32_t group;       // query heads per kv head
+  int32_t head_dim;
+  int32_t page_size;
+  int32_t page_shift;  // log2 of page_size, or -1
+  float scale_log2;    // softmax_scale * log2(e)
+  const uint16_t* q;
+  int64_t q_stride;
+  const void* k_cache;
+  const void* v_cache;
+  const float* k_scales;
+  const float* v_scales;
+  int64_t num_pages;
+  int64_t page_stride;        // elements
+  int64_t scale_page_stride;  // floats
+  const int32_t* block_table;
+  int32_t bt_rows;
+  int32_t bt_stride;
+  int32_t num_seqs;
+  int32_t max_seq_rows;
+  const int32_t* seq_indices;  // may be null
+  const int32_t* cu_rows;
+  const int32_t* seq_len;
+  int32_t window;              // 0: tree
+  int32_t sinks;
+  const int32_t* tree_mask;    // null: window
+  int32_t mask_words;
+  uint16_t* out;
+  float* lse;  // may be null
+  int32_t* status;
+};
+
 cudaError_t launch_append(const AppendParams& p, int head_dim, bool e4m3, int num_sms, cudaStream_t stream);
 cudaError_t prepare_attention(int head_dim, bool e4m3, int group);  // raise the dynamic-smem limit, once per plan
 cudaError_t launch_attention(const AttnParams& p, bool e4m3, int grid, cudaStream_t stream);
+cudaError_t launch_seq_attention(const SeqAttnParams& p, bool e4m3, int grid, cudaStream_t stream);
 
 }  // namespace smq

@@ -44,6 +44,17 @@ Scratch scratch_of(const smq_attn_plan* p) {
   return s;
 }
 
+// Workspace of the sequences' attention.
+struct SeqScratch {
+  size_t end;
+};
+
+SeqScratch seq_scratch_of(const smq_attn_plan*) {
+  SeqScratch s;
+  s.end = kStatusBytes;
+  return s;
+}
+
 int check_device(smq_attn_plan* p) {
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return SMQ_ERR_CUDA;
@@ -145,6 +156,72 @@ int run_attention(const smq_attn_plan* plan, const smq_attention_args* args, boo
   p.wait_ns = plan->wait_ns;
   p.stall_tile = plan->stall_tile;
   return smq::launch_attention(p, d.cache_type == SMQ_CACHE_E4M3, plan->num_sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? SMQ_OK
+             : SMQ_ERR_CUDA;
+}
+
+int run_seq_attention(const smq_attn_plan* plan, const smq_seq_attention_args* args, bool tree, void* stream) {
+  if (!plan || !args || args->struct_size < sizeof(smq_seq_attention_args)) return SMQ_ERR_INVALID_ARG;
+  const smq_seq_attention_args& a = *args;
+  const smq_attn_plan_desc& d = plan->desc;
+  if (a.rows < 0 || a.rows > d.max_rows || a.num_seqs < 0 || a.num_seqs > d.max_rows) return SMQ_ERR_INVALID_ARG;
+  if (a.max_seq_rows <= 0 || a.max_seq_rows > d.max_rows) return SMQ_ERR_INVALID_ARG;
+  if (tree) {
+    if (a.window != 0 || a.sinks != 0 || a.mask_words <= 0 || a.mask_words > 32 || a.max_seq_rows > 32 * a.mask_words)
+      return SMQ_ERR_INVALID_ARG;
+  } else if (a.window <= 0 || a.sinks < 0 || a.tree_mask || a.mask_words != 0) {
+    return SMQ_ERR_INVALID_ARG;
+  }
+  if (a.rows == 0 || a.num_seqs == 0) return SMQ_OK;
+  if (tree && (!a.tree_mask || !aligned(a.tree_mask, 4))) return SMQ_ERR_INVALID_ARG;
+  if (!strided_ok(a.q, a.q_stride, static_cast<int64_t>(d.num_heads) * d.head_dim)) return SMQ_ERR_INVALID_ARG;
+  int rc = check_cache(plan, {a.k_cache, a.v_cache, a.k_scales, a.v_scales, a.num_pages, a.page_stride, a.scale_page_stride});
+  if (rc != SMQ_OK) return rc;
+  if (!a.block_table || !aligned(a.block_table, 4) || a.bt_rows <= 0 || a.bt_stride <= 0 || !aligned(a.seq_indices, 4) ||
+      !a.cu_rows || !aligned(a.cu_rows, 4) || !a.seq_len || !aligned(a.seq_len, 4))
+    return SMQ_ERR_INVALID_ARG;
+  if (!a.out || !aligned(a.out, 16) || !aligned(a.lse, 4) || !a.workspace || !aligned(a.workspace, 16))
+    return SMQ_ERR_INVALID_ARG;
+  if (a.workspace_bytes < seq_scratch_of(plan).end) return SMQ_ERR_WORKSPACE_TOO_SMALL;
+  rc = check_device(const_cast<smq_attn_plan*>(plan));
+  if (rc != SMQ_OK) return rc;
+  smq::SeqAttnParams p;
+  std::memset(&p, 0, sizeof p);
+  p.rows = a.rows;
+  p.kv_heads = d.num_kv_heads;
+  p.group = d.num_heads / d.num_kv_heads;
+  p.head_dim = d.head_dim;
+  p.page_size = d.page_size;
+  p.page_shift = -1;
+  for (int i = 0; i <= 16; ++i)
+    if (d.page_size == 1 << i) p.page_shift = i;
+  p.scale_log2 = plan->scale * 1.4426950408889634f;
+  p.q = a.q;
+  p.q_stride = a.q_stride;
+  p.k_cache = a.k_cache;
+  p.v_cache = a.v_cache;
+  p.k_scales = a.k_scales;
+  p.v_scales = a.v_scales;
+  p.num_pages = a.num_pages;
+  p.page_stride = a.page_stride;
+  p.scale_page_stride = a.scale_page_stride;
+  p.block_table = a.block_table;
+  p.bt_rows = a.bt_rows;
+  p.bt_stride = a.bt_stride;
+  p.num_seqs = a.num_seqs;
+  p.max_seq_rows = a.max_seq_rows;
+  p.seq_indices = a.seq_indices;
+  p.cu_rows = a.cu_rows;
+  p.seq_len = a.seq_len;
+  p.window = a.window;
+  p.sinks = a.sinks;
+  p.tree_mask = a.tree_mask;
+  p.mask_words = a.mask_words;
+  p.out = a.out;
+  p.lse = a.lse;
+  p.status = static_cast<int32_t*>(a.workspace);
+  return smq::launch_seq_attention(p, d.cache_type == SMQ_CACHE_E4M3, plan->num_sms, static_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
              ? SMQ_OK
              : SMQ_ERR_CUDA;
 }
@@ -274,6 +351,20 @@ SMQ_API int sparse_mqa_attention_decode(const smq_attn_plan* plan, const smq_att
 
 SMQ_API int sparse_mqa_attention_selected(const smq_attn_plan* plan, const smq_attention_args* args, void* stream) {
   return run_attention(plan, args, true, stream);
+}
+
+SMQ_API int smq_seq_attention_workspace_size(const smq_attn_plan* plan, size_t* bytes) {
+  if (!plan || !bytes) return SMQ_ERR_INVALID_ARG;
+  *bytes = seq_scratch_of(plan).end;
+  return SMQ_OK;
+}
+
+SMQ_API int sparse_mqa_attention_window(const smq_attn_plan* plan, const smq_seq_attention_args* args, void* stream) {
+  return run_seq_attention(plan, args, false, stream);
+}
+
+SMQ_API int sparse_mqa_attention_tree(const smq_attn_plan* plan, const smq_seq_attention_args* args, void* stream) {
+  return run_seq_attention(plan, args, true, stream);
 }
 
 }  // extern "C"
