@@ -10,7 +10,8 @@
 
 namespace smq {
 
-constexpr int kAttnTile = 128;  // tokens per tile
+constexpr int kAttnTile = 128;    // tokens per tile
+constexpr int kSeqQueries = 256;  // most queries of an item of the sequences' attention
 
 struct AppendParams {
   int32_t rows;
@@ -113,12 +114,19 @@ struct SeqAttnParams {
   int32_t mask_words;
   uint16_t* out;
   float* lse;  // may be null
+  // partial results, as in AttnParams: seg_info[c] = (first row, rows, kv head, CTAs that continue it)
+  int4* seg_info;   // [grid]
+  float2* part_ml;  // [2 grid][kSeqQueries] running maximum (log2) and sum
+  float* part_o;    // [2 grid][head_dim][kSeqQueries]
   int32_t* status;
+  int64_t wait_ns;
+  int32_t stall_tile;
 };
 
 cudaError_t launch_append(const AppendParams& p, int head_dim, bool e4m3, int num_sms, cudaStream_t stream);
 cudaError_t prepare_attention(int head_dim, bool e4m3, int group);  // raise the dynamic-smem limit, once per plan
 cudaError_t launch_attention(const AttnParams& p, bool e4m3, int grid, cudaStream_t stream);
+cudaError_t prepare_seq_attention(int head_dim, bool e4m3);
 cudaError_t launch_seq_attention(const SeqAttnParams& p, bool e4m3, int grid, cudaStream_t stream);
 
 }  // namespace smq

@@ -18,7 +18,7 @@ struct smq_attn_plan {
   int32_t stall_tile;  // failure-path tests: a withheld hand-off, -1: none
   int32_t num_sms;
   float scale;
-  bool prepared;
+  bool prepared, seq_prepared;  // the kernels' shared-memory limits are set
 };
 
 namespace {
@@ -44,22 +44,28 @@ Scratch scratch_of(const smq_attn_plan* p) {
   return s;
 }
 
-// Workspace of the sequences' attention.
-struct SeqScratch {
-  size_t end;
-};
-
-SeqScratch seq_scratch_of(const smq_attn_plan*) {
-  SeqScratch s;
-  s.end = kStatusBytes;
+// The same for the sequences' attention, whose items have up to kSeqQueries queries.
+Scratch seq_scratch_of(const smq_attn_plan* p) {
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const size_t slots = 2 * static_cast<size_t>(p->num_sms);
+  Scratch s;
+  s.info = kStatusBytes;
+  s.ml = s.info + up(p->num_sms * sizeof(int4));
+  s.o = s.ml + up(slots * smq::kSeqQueries * sizeof(float2));
+  s.end = s.o + slots * smq::kSeqQueries * p->desc.head_dim * sizeof(float);
   return s;
 }
 
-int check_device(smq_attn_plan* p) {
+int check_device(smq_attn_plan* p, bool sequences = false) {
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return SMQ_ERR_CUDA;
   if (dev != p->desc.device) return SMQ_ERR_INVALID_ARG;
-  if (!p->prepared) {
+  if (sequences) {
+    if (!p->seq_prepared) {
+      if (smq::prepare_seq_attention(p->desc.head_dim, p->desc.cache_type == SMQ_CACHE_E4M3) != cudaSuccess) return SMQ_ERR_CUDA;
+      p->seq_prepared = true;
+    }
+  } else if (!p->prepared) {
     if (smq::prepare_attention(p->desc.head_dim, p->desc.cache_type == SMQ_CACHE_E4M3,
                                p->desc.num_heads / p->desc.num_kv_heads) != cudaSuccess)
       return SMQ_ERR_CUDA;
@@ -183,7 +189,7 @@ int run_seq_attention(const smq_attn_plan* plan, const smq_seq_attention_args* a
   if (!a.out || !aligned(a.out, 16) || !aligned(a.lse, 4) || !a.workspace || !aligned(a.workspace, 16))
     return SMQ_ERR_INVALID_ARG;
   if (a.workspace_bytes < seq_scratch_of(plan).end) return SMQ_ERR_WORKSPACE_TOO_SMALL;
-  rc = check_device(const_cast<smq_attn_plan*>(plan));
+  rc = check_device(const_cast<smq_attn_plan*>(plan), true);
   if (rc != SMQ_OK) return rc;
   smq::SeqAttnParams p;
   std::memset(&p, 0, sizeof p);
@@ -219,7 +225,14 @@ int run_seq_attention(const smq_attn_plan* plan, const smq_seq_attention_args* a
   p.mask_words = a.mask_words;
   p.out = a.out;
   p.lse = a.lse;
+  const Scratch w = seq_scratch_of(plan);
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  p.seg_info = reinterpret_cast<int4*>(ws + w.info);
+  p.part_ml = reinterpret_cast<float2*>(ws + w.ml);
+  p.part_o = reinterpret_cast<float*>(ws + w.o);
   p.status = static_cast<int32_t*>(a.workspace);
+  p.wait_ns = plan->wait_ns;
+  p.stall_tile = plan->stall_tile;
   return smq::launch_seq_attention(p, d.cache_type == SMQ_CACHE_E4M3, plan->num_sms, static_cast<cudaStream_t>(stream)) ==
                  cudaSuccess
              ? SMQ_OK
@@ -255,7 +268,7 @@ SMQ_API int smq_attn_plan_create(const smq_attn_plan_desc* desc, smq_attn_plan**
   p->wait_ns = 2000000000ll;  // 2 s: far beyond any legitimate wait
   p->stall_tile = -1;
   p->num_sms = sms;
-  p->prepared = false;
+  p->prepared = p->seq_prepared = false;
   p->scale = d.softmax_scale != 0.f ? d.softmax_scale : 1.f / std::sqrt(static_cast<float>(d.head_dim));
   *plan = p;
   return SMQ_OK;

@@ -1,112 +1,1241 @@
 // Attention of sequences' query rows over a paged key-value cache (sm_103a): a
 // sliding window with sinks, or a tree of drafted tokens.
 //
-// The simplest form: a block per (sequence, row, kv head), a warp per query
-// head, one token after another with a running maximum and sum. Each lane holds
-// D / 32 elements of the query, the token's key and value, and the result.
+// An item is a block of a sequence's rows on one kv head. Its rows and their
+// query heads are the M side of the products: a tile of 128 holds 128 / G rows
+// with G heads each. Over tiles of 128 tokens,
+//   S = Q K^T       tcgen05.mma, M = 128 queries, N = 128 tokens, to TMEM
+//   P = 2^(c S - m) a thread owns one query: no value crosses threads
+//   O += P V        tcgen05.mma with P read from TMEM, where it replaces S
+// with a running maximum m and sum l per thread, in one pass over the tokens.
+// m is raised only when a score exceeds it by kTau (in log2), so the rescale of
+// O stays out of the common path.
+//
+// Two streams, each with its own S, P and O in TMEM and its own softmax group,
+// keep the tensor core busy: one stream's products run behind the other's
+// softmax. Where sequences have more queries than a tile (kPair) the streams are
+// two tiles of queries, and each key and value is read once for both. Otherwise
+// they are one tile of queries over every other tile of tokens, joined in TMEM.
 #include "smq_attn.cuh"
 #include "smq_attn_ptx.cuh"
 #include "smq_kernels.cuh"
 #include "smq_ptx.cuh"
 
+#include <type_traits>
+
 namespace smq {
 
 namespace {
 
-constexpr int kSimpleThreads = 128;
+constexpr int kLoaders = 128;  // threads; over an E4M3 cache as many again, a group for keys and one for values
+constexpr int kSegRing = 8;    // segments published ahead
+constexpr int kRing = 4;       // tiles whose addresses, masks and scales may be ahead of the softmax
+constexpr float kUnset = -3.0e38f;         // the running maximum of a partial without tokens
+constexpr int kSmemLimit = 232448 - 1024;  // less the static part
+constexpr float kTau = 8.f;                // log2 of the largest P
 
-template <bool kE4m3>
-__device__ __forceinline__ float element(const void* base, int64_t at) {
-  if (kE4m3) {
-    uint32_t lo, hi;
-    widen4(static_cast<const uint8_t*>(base)[at], lo, hi);
-    return __uint_as_float(lo << 16);
+// A run of token tiles of one item. The item's tokens are numbered e = 0 .. count - 1: position e below s0, e + gap from
+// there on.
+struct SeqSeg {
+  int32_t row0, nrows;    // rows of q and out
+  int32_t kvh;
+  int32_t tile0, ntiles;  // ntiles = 0: the end of this CTA's work
+  int32_t slot;           // partial slot, -1: the whole item, write the result
+  int32_t table_row;      // of the block table, -1: out of range
+  int32_t s0, gap, count;
+  int32_t end0;           // window: position of the first row, plus one; tree: tokens before the drafted ones
+  int32_t pad[5];
+};
+static_assert(sizeof(SeqSeg) == 64, "");
+
+// A kernel's shapes. Shared memory holds the queries, kSlots tiles of K or V as the tensor core reads them, over an E4M3
+// cache kRaws tiles of codes of each side, and the rings.
+template <int D, bool kE4m3, bool kPair>
+struct SeqShape {
+  static constexpr int kBlocks = D / 64;                 // 128-byte columns of a token
+  static constexpr int kUnit = kBlocks * 128 * 128;      // bytes of a K, V or Q tile
+  static constexpr int kRaw = kE4m3 ? 128 * D : 0;       // bytes of a tile's codes
+  static constexpr int kQBytes = (kPair ? 2 : 1) * kUnit;
+  static constexpr int kQueries = kPair ? kSeqQueries : 128;
+  static constexpr int kThreads = kE4m3 ? 640 : 512;
+  // registers of a thread: at launch all of an SM's, then most for the 256 softmax threads
+  static constexpr int kRegs = kE4m3 ? 96 : 128;
+  static constexpr int kSoftmaxRegs = kE4m3 ? 152 : 184;
+  static constexpr int kOtherRegs = kE4m3 ? 56 : 72;
+  static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= kThreads * kRegs, "");
+  static constexpr bool kHold = !kE4m3;                  // a thread holds a tile's scores in registers
+  static constexpr int kAddrReaders = (kE4m3 ? 8 : 4) + (kPair ? 8 : 4);  // loader and softmax warps of a tile
+  static constexpr int kSegReaders = (kE4m3 ? 8 : 4) + 8 + 2;             // and MMA and address warps
+  static constexpr int kRingBytes = kRing * 128 * (8 + (kE4m3 ? 8 : 0)) + kRing * 16;
+  static constexpr int kMisc = kRingBytes + kSegRing * 64 + 512 /*barriers*/ + 2 * 128 * 8 /*m and l*/ + 64 /*flags*/;
+  static constexpr int kFree = kSmemLimit - kQBytes - kMisc;
+  // over an E4M3 cache one or two units of each side (each side's loaders keep to slots of their own, so that a wait's
+  // parity names one phase), so that what is left over goes to the copies ahead
+  static constexpr int kFit = kE4m3 ? (kFree >= 4 * kUnit + 4 * kRaw ? 4 : 2) : kFree / kUnit;
+  static constexpr int kSlots = kFit > 8 ? 8 : kFit;
+  static constexpr int kRawFit = kE4m3 ? (kFree - kSlots * kUnit) / (kE4m3 ? 2 * kRaw : 1) : 0;
+  static constexpr int kRaws = kRawFit > 4 ? 4 : kRawFit;  // of each side
+  static constexpr int kSmem = kSlots * kUnit + 2 * kRaws * kRaw + kQBytes + kMisc;
+  static constexpr int kTmem = 512;                        // two S (P takes its place), two O
+  static_assert((kE4m3 ? kSlots % 2 == 0 && kRaws >= 1 : kSlots >= 3) && kSmem <= kSmemLimit, "");
+};
+
+// Instruction descriptor of O += P V: fp32 accumulation, bf16 operands, N-major B, M = 128.
+__host__ __device__ constexpr uint32_t pv_idesc(int n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | (static_cast<uint32_t>(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// D[tmem] (+)= A[tmem] x B; b is a descriptor's two words.
+__device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint32_t b, uint32_t b_hi, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 y;\n mov.b64 y, {%2, %3};\n setp.ne.b32 p, %5, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n}" ::"r"(d),
+      "r"(a), "r"(b), "r"(b_hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+      "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+// Sequence b: its first row, rows and length; no rows where it is refused.
+struct Sequence {
+  int32_t first, rows, len;
+};
+__device__ __forceinline__ Sequence sequence_of(const SeqAttnParams& p, int b, bool report) {
+  Sequence s;
+  const int32_t last = p.cu_rows[b + 1];
+  s.first = p.cu_rows[b];
+  s.rows = 0;
+  s.len = max(p.seq_len[b], 0);
+  if (s.first < 0 || last < s.first || last > p.rows || last - s.first > p.max_seq_rows) {
+    if (report) atomicOr(p.status, kStatusBounds);
+  } else {
+    s.rows = last - s.first;
   }
-  return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(base)[at]) << 16);
+  return s;
+}
+
+// The tokens of rows i0 .. i0 + rows - 1 of a sequence: positions [0, s0) and [lo, hi).
+struct Tokens {
+  int32_t s0, lo, hi;
+  bool past;  // the rows' last token is past the block table
+  __device__ int32_t count() const { return s0 + hi - lo; }
+  __device__ int32_t tiles() const { return max(1, (count() + kAttnTile - 1) / kAttnTile); }  // without tokens there still is a result
+};
+__device__ __forceinline__ Tokens tokens_of(const SeqAttnParams& p, int32_t n, int32_t len, int32_t i0, int32_t rows) {
+  const int64_t room = static_cast<int64_t>(p.bt_stride) * p.page_size;
+  const int32_t cap = room > INT32_MAX ? INT32_MAX : static_cast<int32_t>(room);
+  Tokens t;
+  const int32_t last = p.tree_mask ? len : len - n + i0 + rows;
+  t.hi = min(max(last, 0), cap);
+  t.past = last > cap;
+  t.lo = 0;
+  if (!p.tree_mask) {
+    const int32_t first = len - n + i0 + 1;
+    t.lo = min(first > p.window ? first - p.window : 0, t.hi);
+  }
+  t.s0 = min(p.sinks, t.lo);
+  return t;
+}
+
+// Bits of the tokens below x among the 32 from e on.
+__device__ __forceinline__ uint32_t bits_below(int32_t x, int32_t e) {
+  return x <= e ? 0u : x - e >= 32 ? 0xffffffffu : (1u << (x - e)) - 1u;
 }
 
 }  // namespace
 
-template <int D, bool kE4m3>
-__global__ void __launch_bounds__(kSimpleThreads) seq_attention_kernel(const __grid_constant__ SeqAttnParams p) {
-  constexpr int kPer = D / 32;
+template <int D, bool kE4m3, bool kPair>
+__global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
+    seq_attention_kernel(const __grid_constant__ SeqAttnParams p) {
+  using S = SeqShape<D, kE4m3, kPair>;
+  constexpr int kThreads = S::kThreads;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  // operands first (1024-byte aligned), then rings, state and barriers
+  uint8_t* const units = smem;
+  uint8_t* const q_s = units + S::kSlots * S::kUnit;
+  uint8_t* const raws = q_s + S::kQBytes;                                              // E4M3
+  int64_t* const ring_off = reinterpret_cast<int64_t*>(raws + 2 * S::kRaws * S::kRaw);  // [ring][128]
+  float* const ring_ks = reinterpret_cast<float*>(ring_off + kRing * 128);             // [ring][128], E4M3
+  float* const ring_vs = ring_ks + (kE4m3 ? kRing * 128 : 0);
+  uint32_t* const ring_mask = reinterpret_cast<uint32_t*>(ring_vs + (kE4m3 ? kRing * 128 : 0));  // [ring][4]
+  SeqSeg* const segs = reinterpret_cast<SeqSeg*>(ring_mask + kRing * 4);
+  float2* const ml_s = reinterpret_cast<float2*>(segs + kSegRing);  // [2][128] maxima and sums to be joined
+  int* const flags = reinterpret_cast<int*>(ml_s + 256);            // [2][2][4] infinite values, [2] products left out
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(flags + 20);
+  constexpr int kFull = 0, kEmpty = kFull + S::kSlots, kSFull = kEmpty + S::kSlots, kPFull = kSFull + 2, kPvDone = kPFull + 2,
+                kScan = kPvDone + 2, kJoin = kScan + 2, kQEmpty = kJoin + 1, kQFull = kQEmpty + 1, kSegFull = kQFull + 1,
+                kSegEmpty = kSegFull + kSegRing, kAFull = kSegEmpty + kSegRing, kAEmpty = kAFull + kRing,
+                kDrain = kAEmpty + kRing, kScFull = kDrain + 1, kBars = kScFull + (kE4m3 ? kRing : 0);
+  static_assert(kBars * 8 <= 512 && kBars <= kThreads, "");
+  auto bar = [&](int i) { return smem_addr(bars + i); };
+
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  __shared__ long long warp_sum[kThreads / 32];
+  __shared__ int start_seq;
+  __shared__ long long start_idx;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint64_t limit = static_cast<uint64_t>(p.wait_ns);
+  griddep_launch_dependents();
+
+  if (tid < kBars) {  // a barrier a thread
+    const int i = tid;
+    const int count = i < kEmpty ? (kE4m3 ? kLoaders / 32 : kLoaders)   // K and V units: loader warps, or each thread's copies
+                      : i < kPFull ? 1                                  // freed by the MMAs; S
+                      : i < kPvDone ? 4                                 // P written: each softmax warp
+                      : i < kScan ? 1                                   // O
+                      : i < kJoin ? 4 : i < kQEmpty ? 8                 // values scanned; both streams' results
+                      : i < kQFull ? 1 : i < kSegFull ? kLoaders        // queries (E4M3: each thread's copies)
+                      : i < kSegEmpty ? 1 : i < kAFull ? S::kSegReaders // segments
+                      : i < kAEmpty ? 1 : i < kDrain ? S::kAddrReaders  // addresses
+                      : i < kScFull ? 1 : 64;                           // drain; scales: each lane's copies, and its stores
+    mbar_init(bar(i), count);
+    mbar_init_fence();
+  }
+  if (tid == 0) {
+    abort_flag = 0;
+    start_seq = -1;
+  }
+  if (tid < 2) flags[16 + tid] = 0;
+  if (warp == 5) tmem_alloc(smem_addr(&tmem_slot), S::kTmem);
+  griddep_wait();
+
+  // ---- this CTA's range of the tile list: sequences, kv heads, blocks of rows, tiles
+  tc_fence_before();
+  const int per_tile = 128 / p.group, per_item = (kPair ? 2 : 1) * per_tile;  // rows of a tile of queries, and of an item
+  // tiles of sequence base + lane on one kv head, for the sequences below end
+  auto head_tiles = [&](int base, int end, bool report) {
+    const int b = base + lane;
+    Sequence s = {0, 0, 0};
+    if (b < end) s = sequence_of(p, b, report);
+    long long mine = 0;
+    if (s.rows > 0 && s.rows <= per_item) mine = tokens_of(p, s.rows, s.len, 0, s.rows).tiles();
+    for (uint32_t many = __ballot_sync(0xffffffffu, s.rows > per_item); many; many &= many - 1) {
+      const int src = __ffs(many) - 1;
+      const int n = __shfl_sync(0xffffffffu, s.rows, src), len = __shfl_sync(0xffffffffu, s.len, src);
+      long long wide = 0;
+      for (int i = lane * per_item; i < n; i += 32 * per_item) wide += tokens_of(p, n, len, i, min(per_item, n - i)).tiles();
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) wide += __shfl_xor_sync(0xffffffffu, wide, o);
+      if (lane == src) mine = wide;
+    }
+    return mine;
+  };
+  auto scan_lanes = [&](long long v) {  // inclusive prefix sums
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += x;
+    }
+    return v;
+  };
+  constexpr int kWarps = kThreads / 32;
+  const int groups = (p.num_seqs + 31) / 32, per_warp = (groups + kWarps - 1) / kWarps;
+  const int seq0 = warp * per_warp * 32, seq1 = min(p.num_seqs, (warp + 1) * per_warp * 32);
+  long long mine = 0;
+  for (int base = seq0; base < seq1; base += 32) mine += head_tiles(base, seq1, blockIdx.x == 0);
+  mine = scan_lanes(mine * p.kv_heads);
+  if (lane == 31) warp_sum[warp] = mine;
+  __syncthreads();
+  long long before = 0, total = 0;
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += warp_sum[w];
+    total += warp_sum[w];
+  }
+  const long long chunk = div_of(total + gridDim.x - 1, gridDim.x), begin = chunk * blockIdx.x;
+  const long long work = begin < total ? min(chunk, total - begin) : 0;
+  if (work > 0 && begin >= before && begin < before + warp_sum[warp]) {
+    long long at = before;
+    for (int base = seq0; base < seq1; base += 32) {
+      const long long t = head_tiles(base, seq1, false) * p.kv_heads, incl = scan_lanes(t);
+      if (begin >= at + incl - t && begin < at + incl) {
+        start_seq = base + lane;
+        start_idx = begin - (at + incl - t);
+      }
+      at += __shfl_sync(0xffffffffu, incl, 31);
+    }
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  const volatile int* const abort = &abort_flag;
+  auto fail = [&] { *reinterpret_cast<volatile int*>(&abort_flag) = 1; };  // reported at the end
+
+  // the softmax threads take registers that the others do not need
+  if (warp < 8 || warp >= 16) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kOtherRegs));
+    bool ok = true;
+    auto wait = [&](int b, uint32_t parity) {
+      ok = wait_phase(bar(b), parity, abort, limit);
+      return ok;
+    };
+    if (warp < 4 || warp >= 16) {
+      // ------------------------------------------------------------ loaders
+      const int stall_tile = blockIdx.x == 0 ? p.stall_tile : -1;  // tests: its keys are not handed over
+      const uint32_t units_a = smem_addr(units);
+      auto fetch_queries = [&](const SeqSeg& sg) {
+        constexpr int kChunks = D / 8, kQTok = 32 / kChunks;  // 16-byte pieces of a query, queries per warp instruction
+        const int c = lane % kChunks;
+        const uint16_t* const base = p.q + static_cast<int64_t>(sg.kvh) * p.group * D + c * 8;
+#pragma unroll 4
+        for (int i = warp * kQTok + lane / kChunks; i < S::kQueries; i += 4 * kQTok) {
+          const int t = kPair ? i >> 7 : 0, m = i & 127, r = m / p.group, row = t * per_tile + r;
+          const bool there = r < per_tile && row < sg.nrows;
+          cp16(smem_addr(q_s) + t * S::kUnit + (c >> 3) * 16384 + m * 128 + (((c & 7) ^ (m & 7)) << 4),
+               base + (there ? (static_cast<int64_t>(sg.row0) + row) * p.q_stride + (m - r * p.group) * D : 0), there ? 16 : 0);
+        }
+      };
+      if constexpr (kE4m3) {
+        // Warps 0-3 bring keys, warps 16-19 values. Each lane copies pieces of 16 codes into a place of its own and widens
+        // them later into the unit that the tensor core reads, so the copies need no barrier. Two cursors go over the
+        // tiles: one copies, up to kRaws tiles ahead of the one that widens.
+        constexpr int kPieces = D / 16;                       // of a token
+        constexpr int kTok = 32 / kPieces, kPer = 32 / kTok;  // tokens per warp instruction, pieces per lane and unit
+        // Eight lanes have two neighbouring tokens' pieces of one 128-byte column, so that their stores, two 16-byte
+        // chunks apart within a token and swizzled by the token, meet every bank once.
+        const int piece = (lane & 3) | (kPieces == 8 ? (lane >> 1) & 4 : 0);
+        const int sub = kPieces == 8 ? ((lane >> 2) & 1) | ((lane >> 3) & 2) : lane >> 2;
+        const bool values = warp >= 16;
+        const int w0 = (warp & 3) * 32;                       // the warp's first token
+        uint8_t* const mine_raw = raws + (values ? S::kRaws * S::kRaw : 0) + w0 * D + lane * 16;
+        const uint8_t* const base = static_cast<const uint8_t*>(values ? p.v_cache : p.k_cache) + piece * 16;
+        int ahead = 0;                                        // tiles copied and not yet widened
+        int cseg = 0, cleft = 0, ctile = 0, craw = 0;         // copying
+        int seg = 0, left = 0, tile = 0, raw = 0;             // widening
+        int slot = values ? 1 : 0;                            // keys in the even units, values in the odd ones
+        uint32_t turn = 1;
+        bool more = true;
+        auto ready = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test_wait(bar(b), parity)); };
+        while (true) {
+          if (more && ahead < S::kRaws) {
+            // copy the next tile; as long as there is something to widen, only if its segment and addresses are there
+            bool there = true;
+            if (cleft == 0) {
+              const int at = kSegFull + cseg % kSegRing, parity = (cseg / kSegRing) & 1;
+              there = ahead > 0 ? ready(at, parity) : wait(at, parity);
+              if (there) {
+                cleft = segs[cseg % kSegRing].ntiles;
+                more = there = cleft > 0;
+                ++cseg;
+              }
+            }
+            if (there) {
+              const int at = kAFull + ctile % kRing, parity = (ctile / kRing) & 1;
+              there = ahead > 0 ? ready(at, parity) : wait(at, parity);
+            }
+            if (!ok) break;
+            if (there) {
+              const int64_t* const offs = ring_off + ctile % kRing * 128 + w0 + sub;
+              const uint32_t dst = smem_addr(mine_raw) + craw * S::kRaw;
+              const bool whole = ring_mask[ctile % kRing * 4 + (warp & 3)] == 0xffffffffu;  // every token is there
+              if (__builtin_expect(whole, 1)) {
+#pragma unroll
+                for (int i0 = 0; i0 < kPer; i0 += 4) {
+                  const uint8_t* src[4];
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) src[i] = base + offs[(i0 + i) * kTok];
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) cp16(dst + (i0 + i) * 512, src[i]);
+                }
+              } else {
+#pragma unroll 1
+                for (int i = 0; i < kPer; ++i) {
+                  const int64_t o = offs[i * kTok];
+                  cp16(dst + i * 512, base + (o < 0 ? 0 : o), o < 0 ? 0 : 16);
+                }
+              }
+              cp_commit();
+              __syncwarp();
+              arrive_one(bar(kAEmpty + ctile % kRing), lane);
+              ++ctile;
+              --cleft;
+              if (++craw == S::kRaws) craw = 0;
+              ++ahead;
+              continue;
+            }
+          }
+          if (ahead == 0) break;
+          if (left == 0) {
+            left = segs[seg % kSegRing].ntiles;
+            if (!values) {
+              if (!wait(kQEmpty, (seg + 1) & 1)) break;
+              fetch_queries(segs[seg % kSegRing]);
+              cp_arrive(bar(kQFull));
+            }
+            __syncwarp();
+            arrive_one(bar(kSegEmpty + seg % kSegRing), lane);
+            ++seg;
+          }
+          if (!wait(kEmpty + slot, turn)) break;
+          if (ahead == S::kRaws)
+            cp_wait<S::kRaws - 1>();  // the oldest tile has landed
+          else
+            cp_wait_all();
+          const uint8_t* const src = mine_raw + raw * S::kRaw;
+          const uint32_t dst = units_a + slot * S::kUnit + (piece >> 2) * 16384 + (w0 + sub) * 128;
+#pragma unroll 1
+          for (int i0 = 0; i0 < kPer; i0 += 2) {
+            uint4 w[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) w[i] = *reinterpret_cast<const uint4*>(src + (i0 + i) * 512);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t row = dst + (i0 + i) * (kTok * 128), t = (i * kTok + sub) & 7;  // i0 * kTok is a multiple of 8
+              uint32_t x[4];
+              widen4(w[i].x, x[0], x[1]);
+              widen4(w[i].y, x[2], x[3]);
+              sts16(row + (((piece & 3) * 2 ^ t) << 4), x[0], x[1], x[2], x[3]);
+              widen4(w[i].z, x[0], x[1]);
+              widen4(w[i].w, x[2], x[3]);
+              sts16(row + (((piece & 3) * 2 + 1 ^ t) << 4), x[0], x[1], x[2], x[3]);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (values || stall_tile != tile) arrive_one(bar(kFull + slot), lane);
+          slot += 2;
+          if (slot >= S::kSlots) {
+            slot -= S::kSlots;
+            turn ^= 1;
+          }
+          if (++raw == S::kRaws) raw = 0;
+          --ahead;
+          ++tile;
+          --left;
+        }
+      } else {
+        constexpr int kChunks = D / 8;      // 16-byte pieces of a token
+        constexpr int kTok = 32 / kChunks;  // tokens per warp instruction
+        const int piece = lane % kChunks, sub = lane / kChunks;
+        // Units: K 0, V 0, K 1, V 1, ... The unit's barrier counts each thread's copies when they land; the MMA warp's
+        // proxy fence, after its wait, orders them before the tensor core's reads.
+        int slot = 0, seg = 0, left = 0, tile = 0;  // left: tiles of this segment
+        uint32_t turn = 1;                          // parity that says that the slot is free
+        for (bool values = false; ok; values = !values) {
+          if (!values) {
+            if (left == 0) {
+              if (!wait(kSegFull + seg % kSegRing, (seg / kSegRing) & 1)) break;
+              const SeqSeg& sg = segs[seg % kSegRing];
+              left = sg.ntiles;
+              if (left == 0) break;
+              // the segment's queries: its first K tile's barrier covers them
+              if (!wait(kQEmpty, (seg + 1) & 1)) break;
+              fetch_queries(sg);
+              __syncwarp();
+              arrive_one(bar(kSegEmpty + seg % kSegRing), lane);
+              ++seg;
+            }
+            if (!wait(kAFull + tile % kRing, (tile / kRing) & 1)) break;
+          }
+          if (!wait(kEmpty + slot, turn)) break;
+          const uint8_t* const base = static_cast<const uint8_t*>(values ? p.v_cache : p.k_cache) + piece * 16;
+          const int64_t* const offs = ring_off + tile % kRing * 128 + warp * 32 + sub;
+          constexpr int kBatch = 32 / kTok < 8 ? 32 / kTok : 8;  // addresses first, so that the copies issue back to back
+          const uint32_t dst = units_a + slot * S::kUnit + (piece >> 3) * 16384 + (warp * 32 + sub) * 128;
+          const bool whole = ring_mask[tile % kRing * 4 + warp] == 0xffffffffu;  // every token of the warp is there
+          if (__builtin_expect(whole, 1)) {
+#pragma unroll
+            for (int i0 = 0; i0 < 32 / kTok; i0 += kBatch) {
+              const uint8_t* src[kBatch];
+#pragma unroll
+              for (int i = 0; i < kBatch; ++i) src[i] = base + offs[(i0 + i) * kTok];
+#pragma unroll
+              for (int i = 0; i < kBatch; ++i)
+                cp16(dst + (i0 + i) * kTok * 128 + (((piece & 7) ^ (((i0 + i) * kTok + sub) & 7)) << 4), src[i]);
+            }
+          } else {
+#pragma unroll 1
+            for (int i0 = 0; i0 < 32 / kTok; i0 += 4) {
+              int64_t o[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[i] = offs[(i0 + i) * kTok];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                cp16(dst + (i0 + i) * kTok * 128 + (((piece & 7) ^ (((i0 + i) * kTok + sub) & 7)) << 4),
+                     base + (o[i] < 0 ? 0 : o[i]), o[i] < 0 ? 0 : 16);
+            }
+          }
+          if (values || stall_tile != tile) cp_arrive(bar(kFull + slot));
+          if (++slot == S::kSlots) {
+            slot = 0;
+            turn ^= 1;
+          }
+          if (values) {
+            __syncwarp();
+            arrive_one(bar(kAEmpty + tile % kRing), lane);
+            ++tile;
+            --left;
+          }
+        }
+      }
+      if (!ok && lane == 0) fail();
+      cp_wait_all();
+    } else if (warp == 4) {
+      // ---------------------------------------------------------- scheduler
+      long long left = work;
+      int b = 0, g = 0, k = 0, tile0 = 0;  // sequence, kv head, block, and tile of the block
+      int base = -64;                      // sequences base .. base + 31 are held, one a lane
+      Sequence mine_s = {0, 0, 0}, s = {0, 0, 0};
+      int32_t mine_t = 0, table_row = 0;
+      auto load = [&](int at) {  // sequence `at`
+        if (at >= base + 32 || at < base) {
+          base = at;
+          mine_s = {0, 0, 0};
+          if (at + lane < p.num_seqs) {
+            mine_s = sequence_of(p, at + lane, false);
+            mine_t = p.seq_indices ? p.seq_indices[at + lane] : at + lane;
+            if (mine_t < 0 || mine_t >= p.bt_rows) mine_t = -1;
+          }
+        }
+        s.first = __shfl_sync(0xffffffffu, mine_s.first, at - base);
+        s.rows = __shfl_sync(0xffffffffu, mine_s.rows, at - base);
+        s.len = __shfl_sync(0xffffffffu, mine_s.len, at - base);
+        table_row = __shfl_sync(0xffffffffu, mine_t, at - base);
+      };
+      if (work > 0) {
+        // the first segment's place within its sequence
+        b = start_seq;
+        load(b);
+        const long long per_head = __shfl_sync(0xffffffffu, head_tiles(b, b + 1, false), 0);
+        long long idx = start_idx;
+        g = static_cast<int>(div_of(idx, per_head));
+        idx -= g * per_head;
+        for (bool found = false; !found && k * per_item < s.rows; k += found ? 0 : 32) {
+          const int i = (k + lane) * per_item;
+          const long long t = i < s.rows ? tokens_of(p, s.rows, s.len, i, min(per_item, s.rows - i)).tiles() : 0;
+          const long long incl = scan_lanes(t);
+          const uint32_t here = __ballot_sync(0xffffffffu, idx >= incl - t && idx < incl);
+          const int src = here ? __ffs(here) - 1 : 31;
+          const long long skip = __shfl_sync(0xffffffffu, here ? incl - t : incl, src);
+          idx -= skip;
+          if (here) {
+            k += src;
+            found = true;
+          }
+        }
+        tile0 = static_cast<int>(idx);
+      }
+      int4 info = make_int4(0, 0, 0, 0);
+      int seg = 0;
+      while (ok) {
+        SeqSeg sg;
+        sg.ntiles = 0;
+        if (left > 0) {
+          const int i0 = k * per_item, rows = min(per_item, s.rows - i0);
+          const Tokens tk = tokens_of(p, s.rows, s.len, i0, rows);
+          const int t = tk.tiles();
+          if (tk.past && lane == 0) atomicOr(p.status, kStatusBounds);
+          sg.row0 = s.first + i0;
+          sg.nrows = rows;
+          sg.kvh = g;
+          sg.tile0 = tile0;
+          sg.ntiles = static_cast<int>(min(static_cast<long long>(t - tile0), left));
+          sg.table_row = table_row;
+          sg.s0 = tk.s0;
+          sg.gap = tk.lo - tk.s0;
+          sg.count = tk.count();
+          sg.end0 = p.tree_mask ? s.len - s.rows : s.len - s.rows + i0 + 1;
+          const bool starts = tile0 == 0, ends = tile0 + sg.ntiles == t;
+          sg.slot = starts && ends ? -1 : 2 * static_cast<int>(blockIdx.x) + (starts ? 1 : 0);
+          if (starts && !ends) info = make_int4(sg.row0, rows, g, static_cast<int>(div_of(t - sg.ntiles + chunk - 1, chunk)));
+          left -= sg.ntiles;
+          tile0 += sg.ntiles;
+          if (ends) {
+            tile0 = 0;
+            if (++k * per_item >= s.rows) {
+              k = 0;
+              if (++g == p.kv_heads) {
+                g = 0;
+                while (left > 0) {  // (there is another sequence as long as there is work)
+                  if (++b >= p.num_seqs) left = 0;
+                  load(b);
+                  if (s.rows > 0) break;
+                }
+              }
+            }
+          }
+        }
+        if (seg >= kSegRing) wait(kSegEmpty + seg % kSegRing, (seg / kSegRing - 1) & 1);
+        if (!ok) break;
+        if (lane == 0) {
+          segs[seg % kSegRing] = sg;
+          mbar_arrive(bar(kSegFull + seg % kSegRing));
+        }
+        __syncwarp();
+        ++seg;
+        if (sg.ntiles == 0) break;
+      }
+      if (lane == 0) {
+        if (!ok) fail();
+        p.seg_info[blockIdx.x] = info;
+      }
+    } else if (warp == 5) {
+      // ---------------------------------------------------------------- MMA
+      // The whole warp runs the loop, so that descriptors stay in uniform registers, and one elected thread issues. The
+      // products of one thread with one kind and M run in the order in which they are issued: S of a tile may follow the
+      // product that reads P from its place.
+      constexpr uint32_t kRowHi = desc_hi(128);
+      const uint32_t units_a = smem_addr(units), q_a = smem_addr(q_s);
+      uint32_t done[2] = {0, 0};  // tiles of each stream
+      uint32_t unit = 0;          // K of the next tile
+      bool issued = false;
+      auto slot_of = [&](uint32_t u) { return static_cast<int>(u % S::kSlots); };
+      auto full = [&](uint32_t u) { return wait(kFull + slot_of(u), (u / S::kSlots) & 1); };
+      auto scores = [&](int s, uint32_t u, bool free_unit, bool free_q) {  // S[s] = Q K^T
+        fence_proxy_async_smem();
+        tc_fence_after();
+        const uint32_t a = desc_lo(q_a + (kPair ? s * S::kUnit : 0), 16), k = desc_lo(units_a + slot_of(u) * S::kUnit, 16);
+        if (elect_one()) {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const uint32_t at = ((i >> 2) * 16384 + (i & 3) * 32) >> 4;
+            mma(tmem + s * 128, a + at, kRowHi, k + at, kRowHi, mma_idesc(false, 128), i > 0);
+          }
+          mma_commit(bar(kSFull + s));
+          if (free_unit) mma_commit(bar(kEmpty + slot_of(u)));
+          if (free_q) mma_commit(bar(kQEmpty));
+        }
+        __syncwarp();
+        issued = true;
+      };
+      auto values = [&](int s, uint32_t u, bool first, bool free_unit) {  // O[s] += P[s] V
+        if (!wait(kPFull + s, done[s] & 1) || !full(u)) return false;
+        ++done[s];
+        fence_proxy_async_smem();
+        tc_fence_after();
+        const bool left_out = flags[16 + s];  // the softmax has added this tile itself
+        const uint32_t v = desc_lo(units_a + slot_of(u) * S::kUnit, 16384);
+        if (elect_one()) {
+          if (!left_out) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)  // 16 tokens
+              mma_tmem_a(tmem + 256 + s * D, tmem + s * 128 + i * 8, v + ((i * 16 * 128) >> 4), kRowHi, pv_idesc(D),
+                         first && i == 0 ? 0 : 1);
+          }
+          mma_commit(bar(kPvDone + s));
+          if (free_unit) mma_commit(bar(kEmpty + slot_of(u)));
+        }
+        __syncwarp();
+        issued = true;
+        return true;
+      };
+      for (int seg = 0; ok; ++seg) {
+        if (!wait(kSegFull + seg % kSegRing, (seg / kSegRing) & 1)) break;
+        const int n = segs[seg % kSegRing].ntiles;
+        const bool two = kPair && segs[seg % kSegRing].nrows > per_tile;
+        __syncwarp();
+        arrive_one(bar(kSegEmpty + seg % kSegRing), lane);
+        if (n == 0) break;
+        if (kE4m3 && !wait(kQFull, seg & 1)) break;
+        if (kPair) {
+          for (int j = 0; j <= n && ok; ++j) {
+            const uint32_t u = unit + 2 * j;
+            for (int s = 0; s < (two ? 2 : 1) && ok; ++s) {
+              const bool last = s == (two ? 1 : 0);
+              if (j > 0 && !values(s, u - 1, j == 1, last)) break;
+              if (j == n) continue;
+              // the softmax reads the tile's mask and scales behind S: they are there before S is issued
+              if (s == 0 && (!wait((kE4m3 ? kScFull : kAFull) + (u / 2) % kRing, (u / 2 / kRing) & 1) || !full(u))) break;
+              scores(s, u, last, last && j == n - 1);
+            }
+          }
+        } else {
+          for (int j = 0; j < n + 2 && ok; ++j) {
+            if (j >= 2 && !values(j & 1, unit + 2 * (j - 2) + 1, j < 4, true)) break;
+            if (j >= n) continue;
+            const uint32_t u = unit + 2 * j;
+            if (!wait((kE4m3 ? kScFull : kAFull) + (u / 2) % kRing, (u / 2 / kRing) & 1) || !full(u)) break;
+            scores(j & 1, u, true, j == n - 1);
+          }
+        }
+        unit += 2 * n;
+      }
+      if (!ok && lane == 0) fail();
+      // The MMAs issued so far read shared memory and write TMEM, which a softmax whose waits ran out would free under
+      // them: they end by themselves, so this wait has a limit of its own and not the plan's.
+      if (issued) {
+        if (elect_one()) mma_commit(bar(kDrain));
+        __syncwarp();
+        const int never = 0;
+        wait_phase(bar(kDrain), 0, &never, 2000000000ull);
+      }
+    } else if (warp == 6) {
+      // ---------------------------------------------------------- addresses
+      // One warp, four tokens a lane; the next tile's pages are looked up while this tile's addresses are written.
+      const int shift = p.page_shift;
+      SeqSeg sg;
+      sg.ntiles = 0;
+      int seg = -1, j = 0;
+      for (int it = 0;; ++it) {
+        if (++j >= sg.ntiles) {
+          ++seg;
+          j = 0;
+          if (!wait(kSegFull + seg % kSegRing, (seg / kSegRing) & 1)) break;
+          sg = segs[seg % kSegRing];
+          __syncwarp();
+          arrive_one(bar(kSegEmpty + seg % kSegRing), lane);
+          if (sg.ntiles == 0) break;
+        }
+        const int32_t* const table = sg.table_row >= 0 ? p.block_table + static_cast<int64_t>(sg.table_row) * p.bt_stride : nullptr;
+        const int64_t head = static_cast<int64_t>(sg.kvh) * p.page_size;
+        int32_t in_page[4], page[4];
+        bool asked[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int32_t e = (sg.tile0 + j) * kAttnTile + i * 32 + lane;
+          asked[i] = e < sg.count;
+          page[i] = -1;
+          in_page[i] = 0;
+          if (asked[i]) {
+            const int32_t pos = e < sg.s0 ? e : e + sg.gap;
+            const int32_t col = shift >= 0 ? pos >> shift : pos / p.page_size;
+            in_page[i] = pos - col * p.page_size;
+            if (table) page[i] = table[col];
+          }
+        }
+        const int a = it % kRing;
+        if (!wait(kAEmpty + a, (it / kRing + 1) & 1)) break;
+        bool bad = false;
+        int64_t off[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          off[i] = -1;
+          const int at = a * 128 + i * 32 + lane;
+          if (page[i] >= 0 && page[i] < p.num_pages) {
+            const int64_t vec = head + in_page[i];
+            off[i] = (page[i] * p.page_stride + vec * D) * (kE4m3 ? 1 : 2);
+            if (kE4m3) {
+              const int64_t from = page[i] * p.scale_page_stride + vec;
+              cp4(smem_addr(ring_ks + at), p.k_scales + from);
+              cp4(smem_addr(ring_vs + at), p.v_scales + from);
+            }
+          } else {
+            if (kE4m3) ring_ks[at] = ring_vs[at] = 1.f;
+            bool seen = asked[i];
+            const int32_t node = (sg.tile0 + j) * kAttnTile + i * 32 + lane - sg.end0;
+            if (seen && p.tree_mask && node >= 0) {  // a drafted token: does a row of the item see it?
+              seen = false;
+              for (int r = 0; r < sg.nrows && (node >> 5) < p.mask_words; ++r)
+                seen |= p.tree_mask[(static_cast<int64_t>(sg.row0) + r) * p.mask_words + (node >> 5)] >> (node & 31) & 1;
+            }
+            bad |= seen;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          ring_off[a * 128 + i * 32 + lane] = off[i];
+          const uint32_t mask = __ballot_sync(0xffffffffu, off[i] >= 0);
+          if (lane == 0) ring_mask[a * 4 + i] = mask;
+        }
+        if (kE4m3) {
+          cp_arrive(bar(kScFull + a));
+          mbar_arrive(bar(kScFull + a));
+        }
+        if (bad) atomicOr(p.status, kStatusBounds);
+        __syncwarp();
+        arrive_one(bar(kAFull + a), lane);
+      }
+      if (!ok && lane == 0) fail();
+      cp_wait_all();
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kSoftmaxRegs));
+    const int st = (warp - 8) >> 2, quarter = warp & 3;  // stream; this warp's lanes of TMEM
+    const int m_row = quarter * 32 + lane;               // this thread's query within its tile
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t s_col = tmem + lanes + st * 128, o_col = tmem + lanes + 256 + st * D;
+    const int my_r = m_row / p.group, my_h = m_row - my_r * p.group;
+    bool ok = true;
+    auto wait = [&](int b, uint32_t parity) {
+      ok = wait_phase(bar(b), parity, abort, limit);
+      return ok;
+    };
+    uint32_t done = 0, other = 0, tile = 0, scans = 0, joins = 0;  // tiles of this stream and of the other; of all; ...
+    for (int seg = 0;; ++seg) {
+      if (!wait(kSegFull + seg % kSegRing, (seg / kSegRing) & 1)) break;
+      const SeqSeg sg = segs[seg % kSegRing];
+      __syncwarp();
+      arrive_one(bar(kSegEmpty + seg % kSegRing), lane);
+      if (sg.ntiles == 0) break;
+      const int first_row = kPair ? st * per_tile : 0;  // of this tile of queries, within the item
+      const int rows = min(per_tile, sg.nrows - first_row);
+      const bool mine_q = my_r < rows;                  // this thread has a query
+      const int my_row = sg.row0 + first_row + my_r;
+      // what this thread's row sees, in the item's numbering: [0, see_a) and [see_b, see_c) for a window; what all rows of
+      // the tile of queries see: [0, all_a) and [all_b, all_c)
+      int32_t see_a = 0, see_b = 0, see_c = 0, all_a = 0, all_b = 0, all_c = 0;
+      if (p.tree_mask) {
+        all_c = sg.end0;
+      } else {
+        auto range = [&](int r, int32_t& x, int32_t& y, int32_t& z) {
+          const int32_t end = sg.end0 + first_row + r;
+          z = end - sg.gap;
+          y = (end > p.window ? end - p.window : 0) - sg.gap;
+          x = sg.gap > 0 ? sg.s0 : min(p.sinks, z);
+        };
+        int32_t skip;
+        range(my_r, see_a, see_b, see_c);
+        range(0, all_a, skip, all_c);
+        range(rows - 1, skip, all_b, skip);
+        if (all_b <= all_a) all_b = 0;
+      }
+      const int step = kPair ? 1 : 2;
+      float nm = 0.f, l0 = 0.f, l1 = 0.f;  // running maximum, negated; sum
+      bool fresh = true;                   // no score above minus infinity so far
+      if (rows > 0) {
+        for (int j = kPair ? 0 : st; j < sg.ntiles; j += step) {
+          const int a = (tile + j) % kRing;
+          if (!wait(kSFull + st, done & 1)) break;
+          tc_fence_after();
+          const int32_t e0 = (sg.tile0 + j) * kAttnTile;
+          const uint4 there = *reinterpret_cast<const uint4*>(ring_mask + a * 4);
+          const bool whole = (there.x & there.y & there.z & there.w) == 0xffffffffu &&
+                             ((e0 >= all_b && e0 + kAttnTile <= all_c) || e0 + kAttnTile <= all_a);
+          uint32_t see[4] = {there.x, there.y, there.z, there.w};
+          bool special = false;  // an infinite value that some row does not see: zero weights do not keep it out
+          if (__builtin_expect(!whole, 0)) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const int32_t e = e0 + 32 * w;
+              uint32_t v;
+              if (p.tree_mask) {
+                v = bits_below(sg.end0, e);
+                const int32_t node = e - sg.end0;  // of the word's first token
+                if (node > -32 && mine_q) {
+                  const int32_t* const words = p.tree_mask + static_cast<int64_t>(my_row) * p.mask_words;
+                  const int i = node >> 5, sh = node & 31;  // (rounds down)
+                  const uint32_t lo = i >= 0 && i < p.mask_words ? words[i] : 0;
+                  const uint32_t hi = i + 1 < p.mask_words ? words[i + 1] : 0;
+                  v |= __funnelshift_r(lo, hi, sh);
+                }
+              } else {
+                v = bits_below(see_a, e) | (bits_below(see_c, e) & ~bits_below(see_b, e));
+              }
+              see[w] = mine_q ? see[w] & v : 0u;
+            }
+            // The values of a tile in which a row does not see a token that is there: are they all finite? Each warp looks
+            // at a quarter, whatever its own rows see.
+            const uint32_t vu = 2 * (tile + j) + 1;
+            // With one unit of values, those of the tile before have to be done with: a parity does not tell them apart.
+            if (S::kSlots == 2 && !kPair && j > 0 && !wait(kPvDone + (st ^ 1), (other + (j + st) / 2 - 1) & 1)) break;
+            if (!wait(kFull + static_cast<int>(vu % S::kSlots), (vu / S::kSlots) & 1)) break;
+            const uint4* const v = reinterpret_cast<const uint4*>(units + (vu % S::kSlots) * S::kUnit + quarter * (S::kUnit / 4));
+            uint32_t inf = 0;
+#pragma unroll 4
+            for (int i = lane; i < S::kUnit / 64; i += 32) {
+              const uint4 x = v[i];
+              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                inf |= ((w[k] & 0x7f80u) == 0x7f80u) | ((w[k] & 0x7f800000u) == 0x7f800000u);
+            }
+            inf = __any_sync(0xffffffffu, inf);
+            int* const found = flags + (st * 2 + (scans & 1)) * 4;
+            if (lane == 0) {
+              found[quarter] = inf;
+              mbar_arrive(bar(kScan + st));
+            }
+            if (!wait(kScan + st, scans & 1)) break;
+            ++scans;
+            special = found[0] | found[1] | found[2] | found[3];
+          }
+          // scores of 32 tokens, less the running maximum
+          auto scores = [&](int c, float* y) {
+            tmem_ld<32>(s_col + 32 * c, y);
+            tmem_wait_ld();
+            pin<32>(y);
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              if (kE4m3) {
+                const float4 k = *reinterpret_cast<const float4*>(ring_ks + a * 128 + 32 * c + i);
+                mul2(y[i], y[i + 1], k.x, k.y);
+                mul2(y[i + 2], y[i + 3], k.z, k.w);
+              }
+              fma2(y[i], y[i + 1], p.scale_log2, p.scale_log2, nm, nm);
+              fma2(y[i + 2], y[i + 3], p.scale_log2, p.scale_log2, nm, nm);
+            }
+            if (__builtin_expect(!whole, 0)) {
+              const uint32_t w = c == 0 ? see[0] : c == 1 ? see[1] : c == 2 ? see[2] : see[3];
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!((w >> i) & 1)) y[i] = -INFINITY;
+            }
+          };
+          float y[S::kHold ? 128 : 32];
+          float most = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float* const yc = y + (S::kHold ? 32 * c : 0);
+            scores(c, yc);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) most = fmaxf(most, fmaxf(yc[i], yc[i + 1]));
+          }
+          const bool raise = fresh ? most > -INFINITY : most > kTau;
+          const bool first = j < step;
+          if (__builtin_expect(__any_sync(0xffffffffu, raise), 0)) {
+            const float up = raise ? most : 0.f, alpha = raise && !fresh ? ex2(-up) : 1.f;
+            nm -= up;
+            if (S::kHold) {
+#pragma unroll
+              for (int i = 0; i < (S::kHold ? 128 : 32); ++i) y[i] -= up;
+            }
+            if (!first && __any_sync(0xffffffffu, raise && !fresh)) {
+              l0 *= alpha;
+              l1 *= alpha;
+              if (!wait(kPvDone + st, (done - 1) & 1)) break;
+              tc_fence_after();
+#pragma unroll 2
+              for (int c = 0; c < D; c += 8) {
+                float o[8];
+                tmem_ld<8>(o_col + c, o);
+                tmem_wait_ld();
+                pin<8>(o);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] *= alpha;
+                tmem_st8(o_col + c, o);
+              }
+            }
+            fresh = fresh && !raise;
+          }
+          if (__builtin_expect(special, 0)) {
+            // Weights times values here, of what the row sees only, in fp32. Rare and slow.
+            if (!first && !wait(kPvDone + st, (done - 1) & 1)) break;
+            tc_fence_after();
+            const uint32_t vu = 2 * (tile + j) + 1;
+            const uint8_t* const v = units + (vu % S::kSlots) * S::kUnit;
+#pragma unroll 1
+            for (int d0 = 0; d0 < D; d0 += 8) {
+              float o[8];
+              if (!first) {
+                tmem_ld<8>(o_col + d0, o);
+                tmem_wait_ld();
+                pin<8>(o);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] = 0.f;
+              }
+#pragma unroll 1
+              for (int t = 0; t < 128; t += 8) {
+                float x[8];
+                __syncwarp();
+                tmem_ld<8>(s_col + t, x);
+                tmem_wait_ld();
+                pin<8>(x);
+                const uint32_t w = (t < 32 ? see[0] : t < 64 ? see[1] : t < 96 ? see[2] : see[3]) >> (t & 31);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  if (!((w >> i) & 1)) continue;
+                  float z = x[i];
+                  if (kE4m3) z *= ring_ks[a * 128 + t + i];
+                  float pt = ex2(fmaf(z, p.scale_log2, nm));
+                  if (d0 == 0) l0 += pt;
+                  if (kE4m3) pt *= ring_vs[a * 128 + t + i];
+                  const uint4 e = *reinterpret_cast<const uint4*>(v + (d0 >> 6) * 16384 + (t + i) * 128 +
+                                                                  ((((d0 >> 3) & 7) ^ ((t + i) & 7)) << 4));
+                  const uint32_t ew[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    o[2 * k] = fmaf(pt, __uint_as_float(ew[k] << 16), o[2 * k]);
+                    o[2 * k + 1] = fmaf(pt, __uint_as_float(ew[k] & 0xffff0000u), o[2 * k + 1]);
+                  }
+                }
+              }
+              __syncwarp();
+              tmem_st8(o_col + d0, o);
+            }
+          } else {
+            // P in bf16, in the place of S: 16 columns of pairs for 32 tokens, behind the reads of those
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              float* const yc = y + (S::kHold ? 32 * c : 0);
+              if (!S::kHold) scores(c, yc);
+              uint32_t w[16];
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                yc[i] = ex2(yc[i]);
+                yc[i + 1] = ex2(yc[i + 1]);
+                add2(l0, l1, yc[i], yc[i + 1]);
+              }
+              if (kE4m3) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                  const float4 k = *reinterpret_cast<const float4*>(ring_vs + a * 128 + 32 * c + i);
+                  mul2(yc[i], yc[i + 1], k.x, k.y);
+                  mul2(yc[i + 2], yc[i + 3], k.z, k.w);
+                }
+                if (__builtin_expect(!whole, 0)) {  // a weight of zero stays zero, whatever its scale
+                  const uint32_t vis = c == 0 ? see[0] : c == 1 ? see[1] : c == 2 ? see[2] : see[3];
+#pragma unroll
+                  for (int i = 0; i < 32; ++i)
+                    if (!((vis >> i) & 1)) yc[i] = 0.f;
+                }
+              }
+#pragma unroll
+              for (int i = 0; i < 16; ++i) w[i] = bf16x2(yc[2 * i], yc[2 * i + 1]);
+              tmem_st16(s_col + 16 * c, w);
+            }
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          if (quarter == 0) flags[16 + st] = special;
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar(kPFull + st));
+            mbar_arrive(bar(kAEmpty + a));
+          }
+          __syncwarp();
+          ++done;
+        }
+      } else if (kPair) {
+        // this stream has no queries in the item: its share of the tiles' addresses is free at once
+        for (int j = 0; j < sg.ntiles; ++j) {
+          if (!wait(kAFull + (tile + j) % kRing, ((tile + j) / kRing) & 1)) break;
+          arrive_one(bar(kAEmpty + (tile + j) % kRing), lane);
+        }
+      }
+      if (!ok) break;
+      tile += sg.ntiles;
+      // ---- the segment's result
+      float m = fresh ? kUnset : -nm, l = l0 + l1;
+      float w_own = 1.f, w_other = 0.f;
+      constexpr int kCols = kPair ? D : D / 2;  // this thread's columns of the result
+      const int col0 = kPair ? 0 : st * kCols;
+      const int mine_n = kPair ? sg.ntiles : (sg.ntiles + 1 - st) / 2, other_n = kPair ? 0 : sg.ntiles - mine_n;
+      if (rows > 0 && mine_n > 0 && !wait(kPvDone + st, (done - 1) & 1)) break;
+      if (!kPair) {
+        other += other_n;
+        ml_s[st * 128 + m_row] = make_float2(m, l);
+        __syncwarp();
+        arrive_one(bar(kJoin), lane);
+        if (!wait(kJoin, joins & 1)) break;
+        ++joins;
+        if (other_n > 0 && !wait(kPvDone + (st ^ 1), (other - 1) & 1)) break;
+        const float2 x = ml_s[(st ^ 1) * 128 + m_row];
+        const float top = fmaxf(m, x.x);
+        w_own = mine_n > 0 ? ex2(m - top) : 0.f;
+        w_other = other_n > 0 ? ex2(x.x - top) : 0.f;
+        l = (mine_n > 0 ? l * w_own : 0.f) + (other_n > 0 ? x.y * w_other : 0.f);
+        m = top;
+      }
+      if (rows > 0) {
+        tc_fence_after();
+        const int64_t head = (static_cast<int64_t>(my_row) * p.kv_heads + sg.kvh) * p.group + my_h;
+        const float inv = l == 0.f ? 0.f : __fdividef(1.f, l);
+        const int m_item = (kPair ? st * 128 : 0) + m_row;
+        float* const part = p.part_o + (static_cast<int64_t>(max(sg.slot, 0)) * D + col0) * S::kQueries + m_item;
+        uint16_t* const out = p.out + head * D + col0;
+#pragma unroll 2
+        for (int c = 0; c < kCols; c += 8) {
+          float o[8], x[8];
+          __syncwarp();
+          if (kPair || mine_n > 0) tmem_ld<8>(o_col + col0 + c, o);
+          if (!kPair && other_n > 0) tmem_ld<8>(tmem + lanes + 256 + (st ^ 1) * D + col0 + c, x);
+          tmem_wait_ld();
+          pin<8>(o);
+          pin<8>(x);
+          if (!kPair) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = (mine_n > 0 ? o[i] * w_own : 0.f) + (other_n > 0 ? x[i] * w_other : 0.f);
+          }
+          if (sg.slot >= 0) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) part[(c + i) * S::kQueries] = o[i];
+          } else if (mine_q) {
+            uint4 w;
+            w.x = bf16x2(o[0] * inv, o[1] * inv);
+            w.y = bf16x2(o[2] * inv, o[3] * inv);
+            w.z = bf16x2(o[4] * inv, o[5] * inv);
+            w.w = bf16x2(o[6] * inv, o[7] * inv);
+            *reinterpret_cast<uint4*>(out + c) = w;
+          }
+        }
+        if (kPair || st == 0) {
+          if (sg.slot >= 0)
+            p.part_ml[static_cast<int64_t>(sg.slot) * S::kQueries + m_item] = make_float2(m, l);
+          else if (p.lse && mine_q)
+            p.lse[head] = l == 0.f ? -INFINITY : (m + lg2(l)) * 0.69314718055994531f;
+        }
+        tc_fence_before();
+      }
+      if (!kPair) {  // both have read both results before either's next product
+        __syncwarp();
+        arrive_one(bar(kJoin), lane);
+        if (!wait(kJoin, joins & 1)) break;
+        ++joins;
+      }
+    }
+    if (!ok && lane == 0) fail();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (tid == 0 && abort_flag) atomicOr(p.status, kStatusTimeout);
+  if (warp == 5) tmem_dealloc(tmem, S::kTmem);
+}
+
+// Join the partials of an item that CTA `first` of the attention kernel began
+// and others continued: out = sum_i w_i O_i / sum_i w_i l_i with
+// w_i = 2^(m_i - max m), in the order of the list. A block per CTA and 32
+// queries, a lane each; a warp has every eighth column of the result, or with
+// kFew (few items, whose partials are many) every eighth partial of 16 columns.
+template <int D, int kQueries, bool kFew>
+__global__ void __launch_bounds__(256) seq_combine_kernel(const __grid_constant__ SeqAttnParams p) {
+  constexpr int kCols = kFew ? 16 : D, kPer = kFew ? 16 : D / 8, kWarpParts = kFew ? 8 : 1;
   griddep_launch_dependents();
   griddep_wait();
-  const int b = blockIdx.z, i = blockIdx.x, g = blockIdx.y;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int first = p.cu_rows[b], last = p.cu_rows[b + 1], n = last - first;
-  if (first < 0 || last < first || last > p.rows || n > p.max_seq_rows) {
-    if (threadIdx.x == 0) atomicOr(p.status, kStatusBounds);
-    return;
+  __shared__ float o_s[kFew ? 8 : 1][kCols][33];
+  __shared__ float2 ml_s[8][32];
+  const int first = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int4 info = p.seg_info[first];
+  if (info.w == 0) return;
+  const int parts = info.w + 1, per_tile = 128 / p.group;
+  const int m0 = blockIdx.y * 32, mi = m0 + lane, col0 = kFew ? blockIdx.z * kCols : 0;
+  auto row_of = [&](int i, int& h) {  // the item's row of query i, -1: none
+    const int t = i >> 7, r = (i & 127) / p.group, row = t * per_tile + r;
+    h = (i & 127) - r * p.group;
+    return r < per_tile && row < info.y ? row : -1;
+  };
+  int h;
+  const bool there = row_of(mi, h) >= 0;
+  if (!__syncthreads_or(there)) return;
+  auto slot = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * first + 1 : 2 * (first + i)); };
+  float m = kUnset, l = 0.f, acc[kPer];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
+#pragma unroll 2
+  for (int i = kFew ? warp : 0; i < parts; i += kWarpParts) {
+    const float2 ml = p.part_ml[slot(i) * kQueries + mi];
+    float x[kPer];
+    const float* const o = p.part_o + (slot(i) * D + col0 + (kFew ? 0 : warp)) * kQueries + mi;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) x[k] = o[k * (kFew ? 1 : 8) * kQueries];
+    const float now = fmaxf(m, ml.x), old = ex2(m - now), w = ex2(ml.x - now);
+    m = now;
+    l = l * old + ml.y * w;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) acc[k] = acc[k] * old + x[k] * w;
   }
-  if (i >= n) return;
-  const int64_t length = p.seq_len[b], base = length - n, row = first + i;
-  int table_row = p.seq_indices ? p.seq_indices[b] : b;
-  if (table_row < 0 || table_row >= p.bt_rows) table_row = -1;
-  // visible: [0, sinks) and [from, to), or the context and the mask's tokens
-  const int64_t to = p.tree_mask ? length : base + i + 1;
-  const int64_t from = p.tree_mask ? 0 : max(static_cast<int64_t>(0), to - p.window);
-  for (int h = warp; h < p.group; h += kSimpleThreads / 32) {
-    const int64_t head = static_cast<int64_t>(g) * p.group + h;
-    float q[kPer], acc[kPer], m = -INFINITY, l = 0.f;
-    for (int k = 0; k < kPer; ++k) {
-      q[k] = element<false>(p.q + row * p.q_stride + head * D, lane * kPer + k);
-      acc[k] = 0.f;
+  if (kFew) {
+    ml_s[warp][lane] = make_float2(m, l);
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) o_s[warp][k][lane] = acc[k];
+    __syncthreads();
+    m = kUnset;
+    l = 0.f;
+    for (int w = 0; w < 8; ++w) m = fmaxf(m, ml_s[w][lane].x);
+    float sum[kPer / 8] = {};
+    for (int w = 0; w < 8; ++w) {
+      const float2 ml = ml_s[w][lane];
+      const float f = ex2(ml.x - m);
+      l += ml.y * f;
+#pragma unroll
+      for (int k = 0; k < kPer / 8; ++k) sum[k] += o_s[w][warp + 8 * k][lane] * f;
     }
-    for (int64_t t = 0; t < to; ++t) {
-      if (t >= p.sinks && t < from) t = from;
-      if (p.tree_mask && t >= base) {
-        const int j = static_cast<int>(t - base);
-        if (!(p.tree_mask[row * p.mask_words + j / 32] >> (j % 32) & 1)) continue;
-      }
-      const int64_t col = t / p.page_size;
-      int64_t page = -1;
-      if (table_row >= 0 && col < p.bt_stride) page = p.block_table[static_cast<int64_t>(table_row) * p.bt_stride + col];
-      if (page < 0 || page >= p.num_pages) {
-        if (lane == 0) atomicOr(p.status, kStatusBounds);
-        if (table_row < 0 || col >= p.bt_stride) break;
-        continue;
-      }
-      const int64_t vec = static_cast<int64_t>(g) * p.page_size + t % p.page_size;
-      const int64_t at = page * p.page_stride + vec * D + lane * kPer;
-      float s = 0.f, v[kPer];
-      for (int k = 0; k < kPer; ++k) s = fmaf(q[k], element<kE4m3>(p.k_cache, at + k), s);
-      for (int k = 0; k < kPer; ++k) v[k] = element<kE4m3>(p.v_cache, at + k);
-      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (kE4m3) {
-        s *= p.k_scales[page * p.scale_page_stride + vec];
-        const float vs = p.v_scales[page * p.scale_page_stride + vec];
-        for (int k = 0; k < kPer; ++k) v[k] *= vs;
-      }
-      s *= p.scale_log2;
-      const float now = fmaxf(m, s), ref = now == -INFINITY ? 0.f : now;
-      const float old = ex2(m - ref), w = ex2(s - ref);
-      m = now;
-      l = l * old + w;
-      for (int k = 0; k < kPer; ++k) acc[k] = acc[k] * old + w * v[k];
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    for (int k = 0; k < kPer; k += 2)
-      *reinterpret_cast<uint32_t*>(p.out + (row * p.kv_heads * p.group + head) * D + lane * kPer + k) =
-          bf16x2(acc[k] * inv, acc[k + 1] * inv);
-    if (p.lse && lane == 0) p.lse[row * p.kv_heads * p.group + head] = l == 0.f ? -INFINITY : (m + lg2(l)) * 0.69314718055994531f;
+    __syncthreads();
+    const float inv = l == 0.f ? 0.f : __fdividef(1.f, l);
+#pragma unroll
+    for (int k = 0; k < kPer / 8; ++k) o_s[0][warp + 8 * k][lane] = sum[k] * inv;
+  } else {
+    const float inv = l == 0.f ? 0.f : __fdividef(1.f, l);
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) o_s[0][warp + 8 * k][lane] = acc[k] * inv;
+  }
+  if (p.lse && warp == 0 && there && col0 == 0) {
+    const int row = row_of(mi, h);
+    p.lse[(static_cast<int64_t>(info.x + row) * p.kv_heads + info.z) * p.group + h] =
+        l == 0.f ? -INFINITY : (m + lg2(l)) * 0.69314718055994531f;
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < 32 * (kCols / 2); e += 256) {
+    const int q = e / (kCols / 2), c = e % (kCols / 2) * 2;
+    const int row = row_of(m0 + q, h);
+    if (row >= 0)
+      *reinterpret_cast<uint32_t*>(p.out + ((static_cast<int64_t>(info.x + row) * p.kv_heads + info.z) * p.group + h) * D + col0 + c) =
+          bf16x2(o_s[0][c][q], o_s[0][c + 1][q]);
   }
 }
 
-cudaError_t launch_seq_attention(const SeqAttnParams& p, bool e4m3, int grid, cudaStream_t stream) {
-  (void)grid;
+namespace {
+
+template <typename K, typename... A>
+cudaError_t launch(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.max_seq_rows, p.kv_heads, p.num_seqs);
-  cfg.blockDim = dim3(kSimpleThreads);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  auto kernel = p.head_dim == 128 ? (e4m3 ? seq_attention_kernel<128, true> : seq_attention_kernel<128, false>)
-                                  : (e4m3 ? seq_attention_kernel<64, true> : seq_attention_kernel<64, false>);
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Calls f with the kernel of a geometry and its shape.
+template <typename F>
+cudaError_t with_kernel(int head_dim, bool e4m3, bool pair, F f) {
+#define SMQ_SEQ(D, E, P) return f(seq_attention_kernel<D, E, P>, SeqShape<D, E, P>())
+#define SMQ_SEQ_STREAMS(D, E) \
+  if (pair) SMQ_SEQ(D, E, true); \
+  SMQ_SEQ(D, E, false)
+  if (head_dim == 128) {
+    if (e4m3) {
+      SMQ_SEQ_STREAMS(128, true);
+    }
+    SMQ_SEQ_STREAMS(128, false);
+  }
+  if (e4m3) {
+    SMQ_SEQ_STREAMS(64, true);
+  }
+  SMQ_SEQ_STREAMS(64, false);
+#undef SMQ_SEQ_STREAMS
+#undef SMQ_SEQ
+}
+
+template <int D, int kQueries>
+cudaError_t launch_combine(const SeqAttnParams& p, int grid, cudaStream_t stream) {
+  const int64_t per = kQueries / 128 * (128 / p.group);
+  const int64_t items = (static_cast<int64_t>(p.rows) / per + p.num_seqs) * p.kv_heads;  // at most
+  if (items * 4 < grid)
+    return launch(seq_combine_kernel<D, kQueries, true>, dim3(grid, kQueries / 32, D / 16), 256, 0, stream, p);
+  return launch(seq_combine_kernel<D, kQueries, false>, dim3(grid, kQueries / 32), 256, 0, stream, p);
+}
+
+}  // namespace
+
+cudaError_t prepare_seq_attention(int head_dim, bool e4m3) {
+  for (int pair = 0; pair < 2; ++pair) {
+    const cudaError_t rc = with_kernel(head_dim, e4m3, pair != 0, [](auto kernel, auto shape) {
+      // the register split waits for ever on a launch with fewer registers than it hands out
+      cudaFuncAttributes a;
+      const cudaError_t err = cudaFuncGetAttributes(&a, kernel);
+      if (err != cudaSuccess) return err;
+      if (a.numRegs != decltype(shape)::kRegs) return cudaErrorInvalidKernelImage;
+      return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, decltype(shape)::kSmem);
+    });
+    if (rc != cudaSuccess) return rc;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_seq_attention(const SeqAttnParams& p, bool e4m3, int grid, cudaStream_t stream) {
+  const bool pair = p.max_seq_rows > 128 / p.group;
+  cudaError_t rc = with_kernel(p.head_dim, e4m3, pair, [&](auto kernel, auto shape) {
+    return launch(kernel, dim3(grid), decltype(shape)::kThreads, decltype(shape)::kSmem, stream, p);
+  });
+  if (rc != cudaSuccess) return rc;
+  if (p.head_dim == 128) return pair ? launch_combine<128, 256>(p, grid, stream) : launch_combine<128, 128>(p, grid, stream);
+  return pair ? launch_combine<64, 256>(p, grid, stream) : launch_combine<64, 128>(p, grid, stream);
 }
 
 }  // namespace smq
