@@ -90,7 +90,8 @@ struct SeqAttnParams {
   int32_t head_dim;
   int32_t page_size;
   int32_t page_shift;  // log2 of page_size, or -1
-  float scale_log2;    // softmax_scale * log2(e)
+  float scale_log2;    // |softmax_scale| * log2(e)
+  int32_t negate;      // of a negative softmax_scale
   const uint16_t* q;
   int64_t q_stride;
   const void* k_cache;

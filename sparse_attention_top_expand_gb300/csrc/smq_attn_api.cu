@@ -201,7 +201,8 @@ int run_seq_attention(const smq_attn_plan* plan, const smq_seq_attention_args* a
   p.page_shift = -1;
   for (int i = 0; i <= 16; ++i)
     if (d.page_size == 1 << i) p.page_shift = i;
-  p.scale_log2 = plan->scale * 1.4426950408889634f;
+  p.scale_log2 = std::fabs(plan->scale) * 1.4426950408889634f;
+  p.negate = plan->scale < 0.f;
   p.q = a.q;
   p.q_stride = a.q_stride;
   p.k_cache = a.k_cache;

@@ -587,6 +587,8 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
       uint32_t done[2] = {0, 0};  // tiles of each stream
       uint32_t unit = 0;          // K of the next tile
       bool issued = false;
+      // a negative softmax scale turns the queries round, so that the largest product is the largest score
+      const uint32_t idesc = mma_idesc(false, 128) | (p.negate ? 1u << 13 : 0u);
       auto slot_of = [&](uint32_t u) { return static_cast<int>(u % S::kSlots); };
       auto full = [&](uint32_t u) { return wait(kFull + slot_of(u), (u / S::kSlots) & 1); };
       auto scores = [&](int s, uint32_t u, bool free_unit, bool free_q) {  // S[s] = Q K^T
@@ -597,7 +599,7 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
             const uint32_t at = ((i >> 2) * 16384 + (i & 3) * 32) >> 4;
-            mma(tmem + s * 128, a + at, kRowHi, k + at, kRowHi, mma_idesc(false, 128), i > 0);
+            mma(tmem + s * 128, a + at, kRowHi, k + at, kRowHi, idesc, i > 0);
           }
           mma_commit(bar(kSFull + s));
           if (free_unit) mma_commit(bar(kEmpty + slot_of(u)));
@@ -848,20 +850,15 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
             ++scans;
             special = found[0] | found[1] | found[2] | found[3];
           }
-          // scores of 32 tokens, less the running maximum
-          auto scores = [&](int c, float* y) {
-            tmem_ld<32>(s_col + 32 * c, y);
-            tmem_wait_ld();
-            pin<32>(y);
+          // 32 tokens' products, times their key scales; minus infinity where the row does not see the token
+          auto products = [&](int c, float* y) {
+            if (kE4m3) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              if (kE4m3) {
+              for (int i = 0; i < 32; i += 4) {
                 const float4 k = *reinterpret_cast<const float4*>(ring_ks + a * 128 + 32 * c + i);
                 mul2(y[i], y[i + 1], k.x, k.y);
                 mul2(y[i + 2], y[i + 3], k.z, k.w);
               }
-              fma2(y[i], y[i + 1], p.scale_log2, p.scale_log2, nm, nm);
-              fma2(y[i + 2], y[i + 3], p.scale_log2, p.scale_log2, nm, nm);
             }
             if (__builtin_expect(!whole, 0)) {
               const uint32_t w = c == 0 ? see[0] : c == 1 ? see[1] : c == 2 ? see[2] : see[3];
@@ -871,29 +868,45 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
             }
           };
           float y[S::kHold ? 128 : 32];
-          float most = -INFINITY;
+          float most = -INFINITY, most2 = -INFINITY;
+          auto look = [&](const float* y) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float* const yc = y + (S::kHold ? 32 * c : 0);
-            scores(c, yc);
+            for (int i = 0; i < 32; i += 4) {
+              most = fmaxf(fmaxf(most, y[i]), y[i + 1]);
+              most2 = fmaxf(fmaxf(most2, y[i + 2]), y[i + 3]);
+            }
+          };
+          if constexpr (S::kHold) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) most = fmaxf(most, fmaxf(yc[i], yc[i + 1]));
+            for (int c = 0; c < 4; ++c) tmem_ld<32>(s_col + 32 * c, y + 32 * c);
+            tmem_wait_ld();
+            pin<128>(y);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) products(c, y + 32 * c);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) look(y + 32 * c);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              tmem_ld<32>(s_col + 32 * c, y);
+              tmem_wait_ld();
+              pin<32>(y);
+              products(c, y);
+              look(y);
+            }
           }
-          const bool raise = fresh ? most > -INFINITY : most > kTau;
+          most = fmaxf(most, most2) * p.scale_log2;
+          const bool raise = fresh ? most > -INFINITY : most + nm > kTau;
           const bool first = j < step;
           if (__builtin_expect(__any_sync(0xffffffffu, raise), 0)) {
-            const float up = raise ? most : 0.f, alpha = raise && !fresh ? ex2(-up) : 1.f;
-            nm -= up;
-            if (S::kHold) {
-#pragma unroll
-              for (int i = 0; i < (S::kHold ? 128 : 32); ++i) y[i] -= up;
-            }
+            const float now = raise ? -most : nm, alpha = raise && !fresh ? ex2(now - nm) : 1.f;
+            nm = now;
             if (!first && __any_sync(0xffffffffu, raise && !fresh)) {
               l0 *= alpha;
               l1 *= alpha;
               if (!wait(kPvDone + st, (done - 1) & 1)) break;
               tc_fence_after();
-#pragma unroll 2
+#pragma unroll 1
               for (int c = 0; c < D; c += 8) {
                 float o[8];
                 tmem_ld<8>(o_col + c, o);
@@ -957,10 +970,16 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               float* const yc = y + (S::kHold ? 32 * c : 0);
-              if (!S::kHold) scores(c, yc);
+              if constexpr (!S::kHold) {
+                tmem_ld<32>(s_col + 32 * c, yc);
+                tmem_wait_ld();
+                pin<32>(yc);
+                products(c, yc);
+              }
               uint32_t w[16];
 #pragma unroll
               for (int i = 0; i < 32; i += 2) {
+                fma2(yc[i], yc[i + 1], p.scale_log2, p.scale_log2, nm, nm);
                 yc[i] = ex2(yc[i]);
                 yc[i + 1] = ex2(yc[i + 1]);
                 add2(l0, l1, yc[i], yc[i + 1]);
