@@ -63,9 +63,10 @@ struct SeqShape {
   static constexpr int kSoftmaxRegs = kE4m3 ? 152 : 184;
   static constexpr int kOtherRegs = kE4m3 ? 56 : 72;
   static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= kThreads * kRegs, "");
-  static constexpr bool kHold = !kE4m3;                  // a thread holds a tile's scores in registers
+  // a thread holds a tile's scores in registers, or reads them twice in loops of 32
+  static constexpr bool kHold = !kE4m3;
   static constexpr int kAddrReaders = (kE4m3 ? 8 : 4) + (kPair ? 8 : 4);  // loader and softmax warps of a tile
-  static constexpr int kSegReaders = (kE4m3 ? 8 : 4) + 8 + 2;             // and MMA and address warps
+  static constexpr int kSegReaders = (kE4m3 ? 8 : 4) + 8 + 3;             // and MMA and address warps
   static constexpr int kRingBytes = kRing * 128 * (8 + (kE4m3 ? 8 : 0)) + kRing * 16;
   static constexpr int kMisc = kRingBytes + kSegRing * 64 + 512 /*barriers*/ + 2 * 128 * 8 /*m and l*/ + 64 /*flags*/;
   static constexpr int kFree = kSmemLimit - kQBytes - kMisc;
@@ -77,7 +78,7 @@ struct SeqShape {
   static constexpr int kRaws = kRawFit > 4 ? 4 : kRawFit;  // of each side
   static constexpr int kSmem = kSlots * kUnit + 2 * kRaws * kRaw + kQBytes + kMisc;
   static constexpr int kTmem = 512;                        // two S (P takes its place), two O
-  static_assert((kE4m3 ? kSlots % 2 == 0 && kRaws >= 1 : kSlots >= 3) && kSmem <= kSmemLimit, "");
+  static_assert((kE4m3 ? kSlots % 2 == 0 && kRaws >= 1 : kSlots >= 3) && kSlots <= 8 && kSmem <= kSmemLimit, "");
 };
 
 // Instruction descriptor of O += P V: fp32 accumulation, bf16 operands, N-major B, M = 128.
@@ -169,15 +170,21 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
   float2* const ml_s = reinterpret_cast<float2*>(segs + kSegRing);  // [2][128] maxima and sums to be joined
   int* const flags = reinterpret_cast<int*>(ml_s + 256);            // [2][2][4] infinite values, [2] products left out
   uint64_t* const bars = reinterpret_cast<uint64_t*>(flags + 20);
-  constexpr int kFull = 0, kEmpty = kFull + S::kSlots, kSFull = kEmpty + S::kSlots, kPFull = kSFull + 2, kPvDone = kPFull + 2,
+  // kFull: keys, then values, of a stream's tile n (with kPair of both streams'), as many barriers as tiles may be ahead, so
+  // that a wait's parity names one phase
+  constexpr int kFull = 0, kEmpty = kFull + 8, kSFull = kEmpty + S::kSlots, kPFull = kSFull + 2, kPvDone = kPFull + 2,
                 kScan = kPvDone + 2, kJoin = kScan + 2, kQEmpty = kJoin + 1, kQFull = kQEmpty + 1, kSegFull = kQFull + 1,
                 kSegEmpty = kSegFull + kSegRing, kAFull = kSegEmpty + kSegRing, kAEmpty = kAFull + kRing,
-                kDrain = kAEmpty + kRing, kScFull = kDrain + 1, kBars = kScFull + (kE4m3 ? kRing : 0);
+                kDrain = kAEmpty + kRing, kScFull = kDrain + 2, kBars = kScFull + (kE4m3 ? kRing : 0);
   static_assert(kBars * 8 <= 512 && kBars <= kThreads, "");
   auto bar = [&](int i) { return smem_addr(bars + i); };
+  auto full_bar = [](int stream, int side, uint32_t n) {
+    return kFull + (kPair ? side * 4 + static_cast<int>(n & 3) : (stream * 2 + side) * 2 + static_cast<int>(n & 1));
+  };
+  auto full_parity = [](uint32_t n) { return (n >> (kPair ? 2 : 1)) & 1; };
 
   __shared__ uint32_t tmem_slot;
-  __shared__ int abort_flag;
+  __shared__ int abort_flag, tensor_lock;
   __shared__ long long warp_sum[kThreads / 32];
   __shared__ int start_seq;
   __shared__ long long start_idx;
@@ -189,19 +196,20 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
   if (tid < kBars) {  // a barrier a thread
     const int i = tid;
     const int count = i < kEmpty ? (kE4m3 ? kLoaders / 32 : kLoaders)   // K and V units: loader warps, or each thread's copies
-                      : i < kPFull ? 1                                  // freed by the MMAs; S
+                      : i < kSFull ? (kPair ? 2 : 1)                    // freed by the MMAs of each stream that reads them
+                      : i < kPFull ? 1                                  // S
                       : i < kPvDone ? 4                                 // P written: each softmax warp
                       : i < kScan ? 1                                   // O
                       : i < kJoin ? 4 : i < kQEmpty ? 8                 // values scanned; both streams' results
-                      : i < kQFull ? 1 : i < kSegFull ? kLoaders        // queries (E4M3: each thread's copies)
+                      : i < kQFull ? 2 : i < kSegFull ? kLoaders        // queries: freed by both streams; E4M3: each thread's copies
                       : i < kSegEmpty ? 1 : i < kAFull ? S::kSegReaders // segments
                       : i < kAEmpty ? 1 : i < kDrain ? S::kAddrReaders  // addresses
-                      : i < kScFull ? 1 : 64;                           // drain; scales: each lane's copies, and its stores
+                      : i < kScFull ? 1 : 64;                           // drains; scales: each lane's copies, and its stores
     mbar_init(bar(i), count);
     mbar_init_fence();
   }
   if (tid == 0) {
-    abort_flag = 0;
+    abort_flag = tensor_lock = 0;
     start_seq = -1;
   }
   if (tid < 2) flags[16 + tid] = 0;
@@ -311,6 +319,14 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
         int cseg = 0, cleft = 0, ctile = 0, craw = 0;         // copying
         int seg = 0, left = 0, tile = 0, raw = 0;             // widening
         int slot = values ? 1 : 0;                            // keys in the even units, values in the odd ones
+        uint32_t mine_n = 0, other_n = 0;                     // tiles so far of the next tile's stream, and of the other
+        int stream = 0;
+        auto swap_streams = [&] {
+          stream ^= 1;
+          const uint32_t x = mine_n;
+          mine_n = other_n;
+          other_n = x;
+        };
         uint32_t turn = 1;
         bool more = true;
         auto ready = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test_wait(bar(b), parity)); };
@@ -365,6 +381,7 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
           if (ahead == 0) break;
           if (left == 0) {
             left = segs[seg % kSegRing].ntiles;
+            if (stream == 1) swap_streams();  // a segment begins with stream 0
             if (!values) {
               if (!wait(kQEmpty, (seg + 1) & 1)) break;
               fetch_queries(segs[seg % kSegRing]);
@@ -400,7 +417,9 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (values || stall_tile != tile) arrive_one(bar(kFull + slot), lane);
+          if (values || stall_tile != tile) arrive_one(bar(full_bar(stream, values, mine_n)), lane);
+          ++mine_n;
+          if (!kPair) swap_streams();
           slot += 2;
           if (slot >= S::kSlots) {
             slot -= S::kSlots;
@@ -419,9 +438,18 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
         // proxy fence, after its wait, orders them before the tensor core's reads.
         int slot = 0, seg = 0, left = 0, tile = 0;  // left: tiles of this segment
         uint32_t turn = 1;                          // parity that says that the slot is free
+        uint32_t mine_n = 0, other_n = 0;           // tiles so far of the next tile's stream, and of the other
+        int stream = 0;
+        auto swap_streams = [&] {
+          stream ^= 1;
+          const uint32_t x = mine_n;
+          mine_n = other_n;
+          other_n = x;
+        };
         for (bool values = false; ok; values = !values) {
           if (!values) {
             if (left == 0) {
+              if (stream == 1) swap_streams();  // a segment begins with stream 0
               if (!wait(kSegFull + seg % kSegRing, (seg / kSegRing) & 1)) break;
               const SeqSeg& sg = segs[seg % kSegRing];
               left = sg.ntiles;
@@ -463,7 +491,7 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
                      base + (o[i] < 0 ? 0 : o[i]), o[i] < 0 ? 0 : 16);
             }
           }
-          if (values || stall_tile != tile) cp_arrive(bar(kFull + slot));
+          if (values || stall_tile != tile) cp_arrive(bar(full_bar(stream, values, mine_n)));
           if (++slot == S::kSlots) {
             slot = 0;
             turn ^= 1;
@@ -473,6 +501,8 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
             arrive_one(bar(kAEmpty + tile % kRing), lane);
             ++tile;
             --left;
+            ++mine_n;
+            if (!kPair) swap_streams();
           }
         }
       }
@@ -577,85 +607,80 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
         if (!ok) fail();
         p.seg_info[blockIdx.x] = info;
       }
-    } else if (warp == 5) {
+    } else if (warp != 6) {
       // ---------------------------------------------------------------- MMA
-      // The whole warp runs the loop, so that descriptors stay in uniform registers, and one elected thread issues. The
-      // products of one thread with one kind and M run in the order in which they are issued: S of a tile may follow the
-      // product that reads P from its place.
+      // A warp for each stream, so that neither waits for the other's softmax. The whole warp runs the loop, so that
+      // descriptors stay in uniform registers, and one elected thread issues. The products of one thread with one kind and M
+      // run in the order in which they are issued: S of a tile may follow the product that reads P from its place.
       constexpr uint32_t kRowHi = desc_hi(128);
-      const uint32_t units_a = smem_addr(units), q_a = smem_addr(q_s);
-      uint32_t done[2] = {0, 0};  // tiles of each stream
-      uint32_t unit = 0;          // K of the next tile
-      bool issued = false;
+      const int st = warp == 5 ? 0 : 1;
+      const uint32_t units_a = smem_addr(units), q_lo = desc_lo(smem_addr(q_s) + (kPair ? st * S::kUnit : 0), 16);
+      const uint32_t s_at = tmem + st * 128, o_at = tmem + 256 + st * D;
       // a negative softmax scale turns the queries round, so that the largest product is the largest score
       const uint32_t idesc = mma_idesc(false, 128) | (p.negate ? 1u << 13 : 0u);
+      constexpr int step = kPair ? 1 : 2;
+      uint32_t done = 0;  // tiles of this stream
+      uint32_t unit = 0;  // K of the segment's first tile
+      bool issued = false;
       auto slot_of = [&](uint32_t u) { return static_cast<int>(u % S::kSlots); };
-      auto full = [&](uint32_t u) { return wait(kFull + slot_of(u), (u / S::kSlots) & 1); };
-      auto scores = [&](int s, uint32_t u, bool free_unit, bool free_q) {  // S[s] = Q K^T
-        fence_proxy_async_smem();
-        tc_fence_after();
-        const uint32_t a = desc_lo(q_a + (kPair ? s * S::kUnit : 0), 16), k = desc_lo(units_a + slot_of(u) * S::kUnit, 16);
-        if (elect_one()) {
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            const uint32_t at = ((i >> 2) * 16384 + (i & 3) * 32) >> 4;
-            mma(tmem + s * 128, a + at, kRowHi, k + at, kRowHi, idesc, i > 0);
-          }
-          mma_commit(bar(kSFull + s));
-          if (free_unit) mma_commit(bar(kEmpty + slot_of(u)));
-          if (free_q) mma_commit(bar(kQEmpty));
-        }
-        __syncwarp();
-        issued = true;
-      };
-      auto values = [&](int s, uint32_t u, bool first, bool free_unit) {  // O[s] += P[s] V
-        if (!wait(kPFull + s, done[s] & 1) || !full(u)) return false;
-        ++done[s];
-        fence_proxy_async_smem();
-        tc_fence_after();
-        const bool left_out = flags[16 + s];  // the softmax has added this tile itself
-        const uint32_t v = desc_lo(units_a + slot_of(u) * S::kUnit, 16384);
-        if (elect_one()) {
-          if (!left_out) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)  // 16 tokens
-              mma_tmem_a(tmem + 256 + s * D, tmem + s * 128 + i * 8, v + ((i * 16 * 128) >> 4), kRowHi, pv_idesc(D),
-                         first && i == 0 ? 0 : 1);
-          }
-          mma_commit(bar(kPvDone + s));
-          if (free_unit) mma_commit(bar(kEmpty + slot_of(u)));
-        }
-        __syncwarp();
-        issued = true;
-        return true;
-      };
+      auto full = [&](int side, uint32_t n) { return wait(full_bar(st, side, n), full_parity(n)); };
       for (int seg = 0; ok; ++seg) {
         if (!wait(kSegFull + seg % kSegRing, (seg / kSegRing) & 1)) break;
         const int n = segs[seg % kSegRing].ntiles;
-        const bool two = kPair && segs[seg % kSegRing].nrows > per_tile;
+        const bool idle = kPair && st == 1 && segs[seg % kSegRing].nrows <= per_tile;  // no queries for this stream
         __syncwarp();
         arrive_one(bar(kSegEmpty + seg % kSegRing), lane);
         if (n == 0) break;
-        if (kE4m3 && !wait(kQFull, seg & 1)) break;
-        if (kPair) {
-          for (int j = 0; j <= n && ok; ++j) {
-            const uint32_t u = unit + 2 * j;
-            for (int s = 0; s < (two ? 2 : 1) && ok; ++s) {
-              const bool last = s == (two ? 1 : 0);
-              if (j > 0 && !values(s, u - 1, j == 1, last)) break;
-              if (j == n) continue;
-              // the softmax reads the tile's mask and scales behind S: they are there before S is issued
-              if (s == 0 && (!wait((kE4m3 ? kScFull : kAFull) + (u / 2) % kRing, (u / 2 / kRing) & 1) || !full(u))) break;
-              scores(s, u, last, last && j == n - 1);
+        if (idle) {  // as if it had read them: each unit when it is there, so that its phases pass one by one
+          for (uint32_t u = unit; u < unit + 2 * n && full(u & 1, u >> 1); ++u) arrive_one(bar(kEmpty + slot_of(u)), lane);
+          arrive_one(bar(kQEmpty), lane);
+        } else if (kPair || st < n) {
+          // O += P V of tile j, and S = Q K^T of this stream's next tile behind it
+          for (int j = st * (kPair ? 0 : 1) - step; j < n; j += step) {
+            const uint32_t v = unit + 2 * j + 1, k = unit + 2 * (j + step);
+            const bool values = j >= 0, scores = j + step < n;
+            const uint32_t nv = kPair ? v >> 1 : done;  // the tile's number at its barriers, and the next one's
+            if ((values && !full(1, nv)) || (scores && !full(0, kPair ? k >> 1 : done + values))) break;
+            if (kE4m3 && !values && !wait(kQFull, seg & 1)) break;
+            fence_proxy_async_smem();
+            if (values && !wait(kPFull + st, done & 1)) break;
+            tc_fence_after();
+            const bool left_out = flags[16 + st];  // the softmax has added this tile itself
+            const uint32_t v_lo = desc_lo(units_a + slot_of(v) * S::kUnit, 16384), k_lo = desc_lo(units_a + slot_of(k) * S::kUnit, 16);
+            if (elect_one()) {
+              // Both products of a tile go to the tensor core together: mixed with the other stream's they would end with
+              // them, and the two softmaxes would run side by side instead of one behind the other's products. The holder
+              // waits for nothing, so the lock is free again soon; without it (the limit is never reached) only time is lost.
+              for (int tries = 0; tries < 100000 && atomicCAS(&tensor_lock, 0, 1) != 0; ++tries) {
+              }
+              if (values) {
+                if (!left_out) {
+#pragma unroll
+                  for (int i = 0; i < 8; ++i)  // 16 tokens
+                    mma_tmem_a(o_at, s_at + i * 8, v_lo + ((i * 16 * 128) >> 4), kRowHi, pv_idesc(D), j < step && i == 0 ? 0 : 1);
+                }
+                if (!scores) mma_commit(bar(kPvDone + st));
+              }
+              if (scores) {
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                  const uint32_t at = ((i >> 2) * 16384 + (i & 3) * 32) >> 4;
+                  mma(s_at, q_lo + at, kRowHi, k_lo + at, kRowHi, idesc, i > 0);
+                }
+                mma_commit(bar(kSFull + st));
+                mma_commit(bar(kEmpty + slot_of(k)));
+                if (j + 2 * step >= n) {
+                  mma_commit(bar(kQEmpty));
+                  if (!kPair && n == 1) mma_commit(bar(kQEmpty));  // for the stream that has no tile
+                }
+                if (values) mma_commit(bar(kPvDone + st));
+              }
+              if (values) mma_commit(bar(kEmpty + slot_of(v)));
+              atomicExch(&tensor_lock, 0);
             }
-          }
-        } else {
-          for (int j = 0; j < n + 2 && ok; ++j) {
-            if (j >= 2 && !values(j & 1, unit + 2 * (j - 2) + 1, j < 4, true)) break;
-            if (j >= n) continue;
-            const uint32_t u = unit + 2 * j;
-            if (!wait((kE4m3 ? kScFull : kAFull) + (u / 2) % kRing, (u / 2 / kRing) & 1) || !full(u)) break;
-            scores(j & 1, u, true, j == n - 1);
+            __syncwarp();
+            issued = true;
+            done += values;
           }
         }
         unit += 2 * n;
@@ -664,12 +689,12 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
       // The MMAs issued so far read shared memory and write TMEM, which a softmax whose waits ran out would free under
       // them: they end by themselves, so this wait has a limit of its own and not the plan's.
       if (issued) {
-        if (elect_one()) mma_commit(bar(kDrain));
+        if (elect_one()) mma_commit(bar(kDrain + st));
         __syncwarp();
         const int never = 0;
-        wait_phase(bar(kDrain), 0, &never, 2000000000ull);
+        wait_phase(bar(kDrain + st), 0, &never, 2000000000ull);
       }
-    } else if (warp == 6) {
+    } else {
       // ---------------------------------------------------------- addresses
       // One warp, four tokens a lane; the next tile's pages are looked up while this tile's addresses are written.
       const int shift = p.page_shift;
@@ -791,11 +816,12 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
         if (all_b <= all_a) all_b = 0;
       }
       const int step = kPair ? 1 : 2;
-      float nm = 0.f, l0 = 0.f, l1 = 0.f;  // running maximum, negated; sum
+      float nm = 0.f, l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;  // running maximum, negated; sum, in four parts
       bool fresh = true;                   // no score above minus infinity so far
       if (rows > 0) {
         for (int j = kPair ? 0 : st; j < sg.ntiles; j += step) {
           const int a = (tile + j) % kRing;
+          if (!wait((kE4m3 ? kScFull : kAFull) + a, ((tile + j) / kRing) & 1)) break;  // the tile's mask and scales
           if (!wait(kSFull + st, done & 1)) break;
           tc_fence_after();
           const int32_t e0 = (sg.tile0 + j) * kAttnTile;
@@ -826,10 +852,8 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
             }
             // The values of a tile in which a row does not see a token that is there: are they all finite? Each warp looks
             // at a quarter, whatever its own rows see.
-            const uint32_t vu = 2 * (tile + j) + 1;
-            // With one unit of values, those of the tile before have to be done with: a parity does not tell them apart.
-            if (S::kSlots == 2 && !kPair && j > 0 && !wait(kPvDone + (st ^ 1), (other + (j + st) / 2 - 1) & 1)) break;
-            if (!wait(kFull + static_cast<int>(vu % S::kSlots), (vu / S::kSlots) & 1)) break;
+            const uint32_t vu = 2 * (tile + j) + 1, nv = kPair ? tile + j : done;
+            if (!wait(full_bar(st, 1, nv), full_parity(nv))) break;
             const uint4* const v = reinterpret_cast<const uint4*>(units + (vu % S::kSlots) * S::kUnit + quarter * (S::kUnit / 4));
             uint32_t inf = 0;
 #pragma unroll 4
@@ -867,7 +891,7 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
                 if (!((w >> i) & 1)) y[i] = -INFINITY;
             }
           };
-          float y[S::kHold ? 128 : 32];
+          float y[S::kHold ? 128 : 1];
           float most = -INFINITY, most2 = -INFINITY;
           auto look = [&](const float* y) {
 #pragma unroll
@@ -886,13 +910,14 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
 #pragma unroll
             for (int c = 0; c < 4; ++c) look(y + 32 * c);
           } else {
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < 4; ++c) {
-              tmem_ld<32>(s_col + 32 * c, y);
+              float x[32];
+              tmem_ld<32>(s_col + 32 * c, x);
               tmem_wait_ld();
-              pin<32>(y);
-              products(c, y);
-              look(y);
+              pin<32>(x);
+              products(c, x);
+              look(x);
             }
           }
           most = fmaxf(most, most2) * p.scale_log2;
@@ -904,6 +929,8 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
             if (!first && __any_sync(0xffffffffu, raise && !fresh)) {
               l0 *= alpha;
               l1 *= alpha;
+              l2 *= alpha;
+              l3 *= alpha;
               if (!wait(kPvDone + st, (done - 1) & 1)) break;
               tc_fence_after();
 #pragma unroll 1
@@ -967,40 +994,50 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
             }
           } else {
             // P in bf16, in the place of S: 16 columns of pairs for 32 tokens, behind the reads of those
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              float* const yc = y + (S::kHold ? 32 * c : 0);
-              if constexpr (!S::kHold) {
-                tmem_ld<32>(s_col + 32 * c, yc);
-                tmem_wait_ld();
-                pin<32>(yc);
-                products(c, yc);
-              }
+            auto weights = [&](int c, float* x) {
               uint32_t w[16];
 #pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                fma2(yc[i], yc[i + 1], p.scale_log2, p.scale_log2, nm, nm);
-                yc[i] = ex2(yc[i]);
-                yc[i + 1] = ex2(yc[i + 1]);
-                add2(l0, l1, yc[i], yc[i + 1]);
+              for (int i = 0; i < 32; i += 4) {
+#pragma unroll
+                for (int k = i; k < i + 4; k += 2) {
+                  fma2(x[k], x[k + 1], p.scale_log2, p.scale_log2, nm, nm);
+                  x[k] = ex2(x[k]);
+                  x[k + 1] = ex2(x[k + 1]);
+                }
+                add2(l0, l1, x[i], x[i + 1]);
+                add2(l2, l3, x[i + 2], x[i + 3]);
               }
               if (kE4m3) {
 #pragma unroll
                 for (int i = 0; i < 32; i += 4) {
                   const float4 k = *reinterpret_cast<const float4*>(ring_vs + a * 128 + 32 * c + i);
-                  mul2(yc[i], yc[i + 1], k.x, k.y);
-                  mul2(yc[i + 2], yc[i + 3], k.z, k.w);
+                  mul2(x[i], x[i + 1], k.x, k.y);
+                  mul2(x[i + 2], x[i + 3], k.z, k.w);
                 }
                 if (__builtin_expect(!whole, 0)) {  // a weight of zero stays zero, whatever its scale
                   const uint32_t vis = c == 0 ? see[0] : c == 1 ? see[1] : c == 2 ? see[2] : see[3];
 #pragma unroll
                   for (int i = 0; i < 32; ++i)
-                    if (!((vis >> i) & 1)) yc[i] = 0.f;
+                    if (!((vis >> i) & 1)) x[i] = 0.f;
                 }
               }
 #pragma unroll
-              for (int i = 0; i < 16; ++i) w[i] = bf16x2(yc[2 * i], yc[2 * i + 1]);
+              for (int i = 0; i < 16; ++i) w[i] = bf16x2(x[2 * i], x[2 * i + 1]);
               tmem_st16(s_col + 16 * c, w);
+            };
+            if constexpr (S::kHold) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c) weights(c, y + 32 * c);
+            } else {
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                float x[32];
+                tmem_ld<32>(s_col + 32 * c, x);
+                tmem_wait_ld();
+                pin<32>(x);
+                products(c, x);
+                weights(c, x);
+              }
             }
           }
           tmem_wait_st();
@@ -1024,7 +1061,7 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
       if (!ok) break;
       tile += sg.ntiles;
       // ---- the segment's result
-      float m = fresh ? kUnset : -nm, l = l0 + l1;
+      float m = fresh ? kUnset : -nm, l = (l0 + l1) + (l2 + l3);
       float w_own = 1.f, w_other = 0.f;
       constexpr int kCols = kPair ? D : D / 2;  // this thread's columns of the result
       const int col0 = kPair ? 0 : st * kCols;
