@@ -68,7 +68,7 @@ struct SeqShape {
   static constexpr int kAddrReaders = (kE4m3 ? 8 : 4) + (kPair ? 8 : 4);  // loader and softmax warps of a tile
   static constexpr int kSegReaders = (kE4m3 ? 8 : 4) + 8 + 3;             // and MMA and address warps
   static constexpr int kRingBytes = kRing * 128 * (8 + (kE4m3 ? 8 : 0)) + kRing * 16;
-  static constexpr int kMisc = kRingBytes + kSegRing * 64 + 512 /*barriers*/ + 2 * 128 * 8 /*m and l*/ + 64 /*flags*/;
+  static constexpr int kMisc = kRingBytes + kSegRing * 64 + 512 /*barriers*/ + 2 * 128 * 8 /*m and l*/;
   static constexpr int kFree = kSmemLimit - kQBytes - kMisc;
   // over an E4M3 cache one or two units of each side (each side's loaders keep to slots of their own, so that a wait's
   // parity names one phase), so that what is left over goes to the copies ahead
@@ -102,6 +102,14 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
       "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float* x) {
+  uint32_t v[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(x[i]);
+  tmem_st16(taddr, v);
+  tmem_st16(taddr + 16, v + 16);
 }
 
 // Sequence b: its first row, rows and length; no rows where it is refused.
@@ -145,9 +153,88 @@ __device__ __forceinline__ Tokens tokens_of(const SeqAttnParams& p, int32_t n, i
   return t;
 }
 
+// What row r of an item sees of a window, in the item's numbering: [0, x) and [y, z).
+__device__ __forceinline__ void row_sees(const SeqAttnParams& p, const SeqSeg& sg, int r, int32_t& x, int32_t& y, int32_t& z) {
+  const int32_t end = sg.end0 + r;
+  z = end - sg.gap;
+  y = (end > p.window ? end - p.window : 0) - sg.gap;
+  x = sg.gap > 0 ? sg.s0 : min(p.sinks, z);
+}
+
 // Bits of the tokens below x among the 32 from e on.
 __device__ __forceinline__ uint32_t bits_below(int32_t x, int32_t e) {
   return x <= e ? 0u : x - e >= 32 ? 0xffffffffu : (1u << (x - e)) - 1u;
+}
+
+// Which of the 32 tokens from e on row r of an item sees (of those that are there).
+__device__ __forceinline__ uint32_t seen_by(const SeqAttnParams& p, const SeqSeg& sg, int32_t e, int r) {
+  if (!p.tree_mask) {
+    int32_t x, y, z;
+    row_sees(p, sg, r, x, y, z);
+    return bits_below(x, e) | (bits_below(z, e) & ~bits_below(y, e));
+  }
+  uint32_t v = bits_below(sg.end0, e);
+  const int32_t node = e - sg.end0;  // of the first token
+  if (node > -32 && r < sg.nrows) {
+    const int32_t* const words = p.tree_mask + (static_cast<int64_t>(sg.row0) + r) * p.mask_words;
+    const int i = node >> 5;  // (rounds down)
+    const uint32_t lo = i >= 0 && i < p.mask_words ? words[i] : 0;
+    const uint32_t hi = i + 1 < p.mask_words ? words[i + 1] : 0;
+    v |= __funnelshift_r(lo, hi, node & 31);
+  }
+  return v;
+}
+
+template <bool kE4m3>
+__device__ __forceinline__ float element(const void* base, int64_t at) {
+  if (kE4m3) {
+    uint32_t lo, hi;
+    widen4(static_cast<const uint8_t*>(base)[at], lo, hi);
+    return __uint_as_float(lo << 16);
+  }
+  return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(base)[at]) << 16);
+}
+
+// A row's O again, token by token and from the cache, of the tokens that it sees only: where an infinite value or NaN that
+// other rows see has met this row's weight of zero in the product, and for the rows that do see it. Rare, and slow. A warp's
+// call; the lanes with `need` replace their lanes of O, the sum of tiles tile0, tile0 + step, ... of the segment.
+template <int D, bool kE4m3>
+__device__ __noinline__ void redo_row(const SeqAttnParams& p, const SeqSeg& sg, int r, int h, int tile0, int step, float nm,
+                                      bool need, uint32_t o_col) {
+  float o[D];
+  for (int d = 0; d < D; ++d) o[d] = 0.f;
+  if (need) {
+    const int64_t head = static_cast<int64_t>(sg.kvh) * p.group + h;
+    const uint16_t* const q = p.q + (static_cast<int64_t>(sg.row0) + r) * p.q_stride + head * D;
+    for (int j = tile0; j < sg.ntiles; j += step) {
+      for (int32_t i = 0; i < kAttnTile; ++i) {
+        const int32_t e = (sg.tile0 + j) * kAttnTile + i;
+        if (e >= sg.count || !(seen_by(p, sg, e, r) & 1)) continue;
+        const int32_t pos = e < sg.s0 ? e : e + sg.gap, col = pos / p.page_size;
+        const int64_t page = sg.table_row < 0 ? -1 : p.block_table[static_cast<int64_t>(sg.table_row) * p.bt_stride + col];
+        if (page < 0 || page >= p.num_pages) continue;
+        const int64_t vec = static_cast<int64_t>(sg.kvh) * p.page_size + (pos - col * p.page_size);
+        const int64_t at = page * p.page_stride + vec * D;
+        float x = 0.f;
+        for (int d = 0; d < D; ++d) x = fmaf(element<false>(q, d), element<kE4m3>(p.k_cache, at + d), x);
+        if (kE4m3) x *= p.k_scales[page * p.scale_page_stride + vec];
+        if (p.negate) x = -x;
+        float w = ex2(fmaf(x, p.scale_log2, nm));
+        if (kE4m3) w *= p.v_scales[page * p.scale_page_stride + vec];
+        for (int d = 0; d < D; ++d) o[d] = fmaf(w, element<kE4m3>(p.v_cache, at + d), o[d]);
+      }
+    }
+  }
+  __syncwarp();
+  for (int c = 0; c < D; c += 8) {
+    float x[8];
+    tmem_ld<8>(o_col + c, x);
+    tmem_wait_ld();
+    pin<8>(x);
+    for (int i = 0; i < 8; ++i) x[i] = need ? o[c + i] : x[i];
+    tmem_st8(o_col + c, x);
+  }
+  tmem_wait_st();
 }
 
 }  // namespace
@@ -168,12 +255,11 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
   uint32_t* const ring_mask = reinterpret_cast<uint32_t*>(ring_vs + (kE4m3 ? kRing * 128 : 0));  // [ring][4]
   SeqSeg* const segs = reinterpret_cast<SeqSeg*>(ring_mask + kRing * 4);
   float2* const ml_s = reinterpret_cast<float2*>(segs + kSegRing);  // [2][128] maxima and sums to be joined
-  int* const flags = reinterpret_cast<int*>(ml_s + 256);            // [2][2][4] infinite values, [2] products left out
-  uint64_t* const bars = reinterpret_cast<uint64_t*>(flags + 20);
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(ml_s + 256);
   // kFull: keys, then values, of a stream's tile n (with kPair of both streams'), as many barriers as tiles may be ahead, so
   // that a wait's parity names one phase
   constexpr int kFull = 0, kEmpty = kFull + 8, kSFull = kEmpty + S::kSlots, kPFull = kSFull + 2, kPvDone = kPFull + 2,
-                kScan = kPvDone + 2, kJoin = kScan + 2, kQEmpty = kJoin + 1, kQFull = kQEmpty + 1, kSegFull = kQFull + 1,
+                kJoin = kPvDone + 2, kQEmpty = kJoin + 1, kQFull = kQEmpty + 1, kSegFull = kQFull + 1,
                 kSegEmpty = kSegFull + kSegRing, kAFull = kSegEmpty + kSegRing, kAEmpty = kAFull + kRing,
                 kDrain = kAEmpty + kRing, kScFull = kDrain + 2, kBars = kScFull + (kE4m3 ? kRing : 0);
   static_assert(kBars * 8 <= 512 && kBars <= kThreads, "");
@@ -199,8 +285,7 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
                       : i < kSFull ? (kPair ? 2 : 1)                    // freed by the MMAs of each stream that reads them
                       : i < kPFull ? 1                                  // S
                       : i < kPvDone ? 4                                 // P written: each softmax warp
-                      : i < kScan ? 1                                   // O
-                      : i < kJoin ? 4 : i < kQEmpty ? 8                 // values scanned; both streams' results
+                      : i < kJoin ? 1 : i < kQEmpty ? 8                 // O; both streams' results
                       : i < kQFull ? 2 : i < kSegFull ? kLoaders        // queries: freed by both streams; E4M3: each thread's copies
                       : i < kSegEmpty ? 1 : i < kAFull ? S::kSegReaders // segments
                       : i < kAEmpty ? 1 : i < kDrain ? S::kAddrReaders  // addresses
@@ -212,7 +297,6 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
     abort_flag = tensor_lock = 0;
     start_seq = -1;
   }
-  if (tid < 2) flags[16 + tid] = 0;
   if (warp == 5) tmem_alloc(smem_addr(&tmem_slot), S::kTmem);
   griddep_wait();
 
@@ -292,14 +376,18 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
       auto fetch_queries = [&](const SeqSeg& sg) {
         constexpr int kChunks = D / 8, kQTok = 32 / kChunks;  // 16-byte pieces of a query, queries per warp instruction
         const int c = lane % kChunks;
-        const uint16_t* const base = p.q + static_cast<int64_t>(sg.kvh) * p.group * D + c * 8;
+        const uint16_t* const base = p.q + sg.row0 * p.q_stride + static_cast<int64_t>(sg.kvh) * p.group * D + c * 8;
+        const uint32_t dst = smem_addr(q_s) + (c >> 3) * 16384;
+        const int nrows = sg.nrows;
+        const uint32_t inv = 65536 / p.group + 1;  // m * inv >> 16 is m / group for m below 128
 #pragma unroll 4
         for (int i = warp * kQTok + lane / kChunks; i < S::kQueries; i += 4 * kQTok) {
-          const int t = kPair ? i >> 7 : 0, m = i & 127, r = m / p.group, row = t * per_tile + r;
-          const bool there = r < per_tile && row < sg.nrows;
-          cp16(smem_addr(q_s) + t * S::kUnit + (c >> 3) * 16384 + m * 128 + (((c & 7) ^ (m & 7)) << 4),
-               base + (there ? (static_cast<int64_t>(sg.row0) + row) * p.q_stride + (m - r * p.group) * D : 0), there ? 16 : 0);
+          const int t = kPair ? i >> 7 : 0, m = i & 127, r = static_cast<int>(m * inv >> 16), row = t * per_tile + r;
+          const bool there = r < per_tile && row < nrows;
+          cp16(dst + t * S::kUnit + m * 128 + (((c & 7) ^ (m & 7)) << 4),
+               base + (there ? row * p.q_stride + (m - r * p.group) * D : 0), there ? 16 : 0);
         }
+        cp_arrive(bar(kQFull));
       };
       if constexpr (kE4m3) {
         // Warps 0-3 bring keys, warps 16-19 values. Each lane copies pieces of 16 codes into a place of its own and widens
@@ -385,7 +473,6 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
             if (!values) {
               if (!wait(kQEmpty, (seg + 1) & 1)) break;
               fetch_queries(segs[seg % kSegRing]);
-              cp_arrive(bar(kQFull));
             }
             __syncwarp();
             arrive_one(bar(kSegEmpty + seg % kSegRing), lane);
@@ -437,6 +524,7 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
         // Units: K 0, V 0, K 1, V 1, ... The unit's barrier counts each thread's copies when they land; the MMA warp's
         // proxy fence, after its wait, orders them before the tensor core's reads.
         int slot = 0, seg = 0, left = 0, tile = 0;  // left: tiles of this segment
+        bool asked = true;                          // its queries are on their way
         uint32_t turn = 1;                          // parity that says that the slot is free
         uint32_t mine_n = 0, other_n = 0;           // tiles so far of the next tile's stream, and of the other
         int stream = 0;
@@ -446,23 +534,26 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
           mine_n = other_n;
           other_n = x;
         };
+        auto ask = [&](int& at, bool& done) {
+          fetch_queries(segs[at % kSegRing]);
+          __syncwarp();
+          arrive_one(bar(kSegEmpty + at % kSegRing), lane);
+          ++at;
+          done = true;
+        };
         for (bool values = false; ok; values = !values) {
           if (!values) {
             if (left == 0) {
               if (stream == 1) swap_streams();  // a segment begins with stream 0
               if (!wait(kSegFull + seg % kSegRing, (seg / kSegRing) & 1)) break;
-              const SeqSeg& sg = segs[seg % kSegRing];
-              left = sg.ntiles;
+              left = segs[seg % kSegRing].ntiles;
               if (left == 0) break;
-              // the segment's queries: its first K tile's barrier covers them
-              if (!wait(kQEmpty, (seg + 1) & 1)) break;
-              fetch_queries(sg);
-              __syncwarp();
-              arrive_one(bar(kSegEmpty + seg % kSegRing), lane);
-              ++seg;
+              asked = false;
             }
             if (!wait(kAFull + tile % kRing, (tile / kRing) & 1)) break;
           }
+          // the segment's queries, as soon as their place is free; its first tile need not wait for that
+          if (!asked && __all_sync(0xffffffffu, mbar_test_wait(bar(kQEmpty), (seg + 1) & 1))) ask(seg, asked);
           if (!wait(kEmpty + slot, turn)) break;
           const uint8_t* const base = static_cast<const uint8_t*>(values ? p.v_cache : p.k_cache) + piece * 16;
           const int64_t* const offs = ring_off + tile % kRing * 128 + warp * 32 + sub;
@@ -495,6 +586,10 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
           if (++slot == S::kSlots) {
             slot = 0;
             turn ^= 1;
+          }
+          if (values && !asked) {
+            if (!wait(kQEmpty, (seg + 1) & 1)) break;
+            ask(seg, asked);
           }
           if (values) {
             __syncwarp();
@@ -641,11 +736,10 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
             const bool values = j >= 0, scores = j + step < n;
             const uint32_t nv = kPair ? v >> 1 : done;  // the tile's number at its barriers, and the next one's
             if ((values && !full(1, nv)) || (scores && !full(0, kPair ? k >> 1 : done + values))) break;
-            if (kE4m3 && !values && !wait(kQFull, seg & 1)) break;
+            if (!values && !wait(kQFull, seg & 1)) break;
             fence_proxy_async_smem();
             if (values && !wait(kPFull + st, done & 1)) break;
             tc_fence_after();
-            const bool left_out = flags[16 + st];  // the softmax has added this tile itself
             const uint32_t v_lo = desc_lo(units_a + slot_of(v) * S::kUnit, 16384), k_lo = desc_lo(units_a + slot_of(k) * S::kUnit, 16);
             if (elect_one()) {
               // Both products of a tile go to the tensor core together: mixed with the other stream's they would end with
@@ -654,11 +748,9 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
               for (int tries = 0; tries < 100000 && atomicCAS(&tensor_lock, 0, 1) != 0; ++tries) {
               }
               if (values) {
-                if (!left_out) {
 #pragma unroll
-                  for (int i = 0; i < 8; ++i)  // 16 tokens
-                    mma_tmem_a(o_at, s_at + i * 8, v_lo + ((i * 16 * 128) >> 4), kRowHi, pv_idesc(D), j < step && i == 0 ? 0 : 1);
-                }
+                for (int i = 0; i < 8; ++i)  // 16 tokens
+                  mma_tmem_a(o_at, s_at + i * 8, v_lo + ((i * 16 * 128) >> 4), kRowHi, pv_idesc(D), j < step && i == 0 ? 0 : 1);
                 if (!scores) mma_commit(bar(kPvDone + st));
               }
               if (scores) {
@@ -797,24 +889,23 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
       const int rows = min(per_tile, sg.nrows - first_row);
       const bool mine_q = my_r < rows;                  // this thread has a query
       const int my_row = sg.row0 + first_row + my_r;
-      // what this thread's row sees, in the item's numbering: [0, see_a) and [see_b, see_c) for a window; what all rows of
-      // the tile of queries see: [0, all_a) and [all_b, all_c)
-      int32_t see_a = 0, see_b = 0, see_c = 0, all_a = 0, all_b = 0, all_c = 0;
-      if (p.tree_mask) {
-        all_c = sg.end0;
-      } else {
-        auto range = [&](int r, int32_t& x, int32_t& y, int32_t& z) {
-          const int32_t end = sg.end0 + first_row + r;
-          z = end - sg.gap;
-          y = (end > p.window ? end - p.window : 0) - sg.gap;
-          x = sg.gap > 0 ? sg.s0 : min(p.sinks, z);
-        };
+      // what all rows of the tile of queries see: [0, all_a) and [all_b, all_c)
+      int32_t all_a = 0, all_b = 0, all_c = sg.end0;
+      if (!p.tree_mask) {
         int32_t skip;
-        range(my_r, see_a, see_b, see_c);
-        range(0, all_a, skip, all_c);
-        range(rows - 1, skip, all_b, skip);
+        row_sees(p, sg, first_row, all_a, skip, all_c);
+        row_sees(p, sg, first_row + rows - 1, skip, all_b, skip);
         if (all_b <= all_a) all_b = 0;
       }
+      auto scaled = [](float* x, const float* by) {  // 32 tokens' scales
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          const float4 k = *reinterpret_cast<const float4*>(by + i);
+          mul2(x[i], x[i + 1], k.x, k.y);
+          mul2(x[i + 2], x[i + 3], k.z, k.w);
+        }
+      };
+      bool hidden = false;  // some token that other rows see, and this one does not, was in its tiles
       const int step = kPair ? 1 : 2;
       float nm = 0.f, l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;  // running maximum, negated; sum, in four parts
       bool fresh = true;                   // no score above minus infinity so far
@@ -828,69 +919,27 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
           const uint4 there = *reinterpret_cast<const uint4*>(ring_mask + a * 4);
           const bool whole = (there.x & there.y & there.z & there.w) == 0xffffffffu &&
                              ((e0 >= all_b && e0 + kAttnTile <= all_c) || e0 + kAttnTile <= all_a);
-          uint32_t see[4] = {there.x, there.y, there.z, there.w};
-          bool special = false;  // an infinite value that some row does not see: zero weights do not keep it out
+          // A tile that some row does not see all of: minus infinity takes the place of a score in TMEM. In a loop, and
+          // apart from the common path, as code that is read past costs time too.
           if (__builtin_expect(!whole, 0)) {
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const int32_t e = e0 + 32 * w;
-              uint32_t v;
-              if (p.tree_mask) {
-                v = bits_below(sg.end0, e);
-                const int32_t node = e - sg.end0;  // of the word's first token
-                if (node > -32 && mine_q) {
-                  const int32_t* const words = p.tree_mask + static_cast<int64_t>(my_row) * p.mask_words;
-                  const int i = node >> 5, sh = node & 31;  // (rounds down)
-                  const uint32_t lo = i >= 0 && i < p.mask_words ? words[i] : 0;
-                  const uint32_t hi = i + 1 < p.mask_words ? words[i + 1] : 0;
-                  v |= __funnelshift_r(lo, hi, sh);
-                }
-              } else {
-                v = bits_below(see_a, e) | (bits_below(see_c, e) & ~bits_below(see_b, e));
-              }
-              see[w] = mine_q ? see[w] & v : 0u;
-            }
-            // The values of a tile in which a row does not see a token that is there: are they all finite? Each warp looks
-            // at a quarter, whatever its own rows see.
-            const uint32_t vu = 2 * (tile + j) + 1, nv = kPair ? tile + j : done;
-            if (!wait(full_bar(st, 1, nv), full_parity(nv))) break;
-            const uint4* const v = reinterpret_cast<const uint4*>(units + (vu % S::kSlots) * S::kUnit + quarter * (S::kUnit / 4));
-            uint32_t inf = 0;
-#pragma unroll 4
-            for (int i = lane; i < S::kUnit / 64; i += 32) {
-              const uint4 x = v[i];
-              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                inf |= ((w[k] & 0x7f80u) == 0x7f80u) | ((w[k] & 0x7f800000u) == 0x7f800000u);
-            }
-            inf = __any_sync(0xffffffffu, inf);
-            int* const found = flags + (st * 2 + (scans & 1)) * 4;
-            if (lane == 0) {
-              found[quarter] = inf;
-              mbar_arrive(bar(kScan + st));
-            }
-            if (!wait(kScan + st, scans & 1)) break;
-            ++scans;
-            special = found[0] | found[1] | found[2] | found[3];
-          }
-          // 32 tokens' products, times their key scales; minus infinity where the row does not see the token
-          auto products = [&](int c, float* y) {
-            if (kE4m3) {
-#pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                const float4 k = *reinterpret_cast<const float4*>(ring_ks + a * 128 + 32 * c + i);
-                mul2(y[i], y[i + 1], k.x, k.y);
-                mul2(y[i + 2], y[i + 3], k.z, k.w);
-              }
-            }
-            if (__builtin_expect(!whole, 0)) {
-              const uint32_t w = c == 0 ? see[0] : c == 1 ? see[1] : c == 2 ? see[2] : see[3];
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t here = c == 0 ? there.x : c == 1 ? there.y : c == 2 ? there.z : there.w;
+              const uint32_t v = mine_q ? here & seen_by(p, sg, e0 + 32 * c, first_row + my_r) : 0u;
+              hidden |= mine_q && v != here;
+              float x[32];
+              __syncwarp();
+              tmem_ld<32>(s_col + 32 * c, x);
+              tmem_wait_ld();
+              pin<32>(x);
+              if (kE4m3) scaled(x, ring_ks + a * 128 + 32 * c);
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                if (!((w >> i) & 1)) y[i] = -INFINITY;
+                if (!((v >> i) & 1)) x[i] = -INFINITY;
+              tmem_st32(s_col + 32 * c, x);
             }
-          };
+            tmem_wait_st();
+          }
           float y[S::kHold ? 128 : 1];
           float most = -INFINITY, most2 = -INFINITY;
           auto look = [&](const float* y) {
@@ -906,8 +955,6 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
             tmem_wait_ld();
             pin<128>(y);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) products(c, y + 32 * c);
-#pragma unroll
             for (int c = 0; c < 4; ++c) look(y + 32 * c);
           } else {
 #pragma unroll 1
@@ -916,7 +963,7 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
               tmem_ld<32>(s_col + 32 * c, x);
               tmem_wait_ld();
               pin<32>(x);
-              products(c, x);
+              if (kE4m3 && whole) scaled(x, ring_ks + a * 128 + 32 * c);
               look(x);
             }
           }
@@ -946,53 +993,7 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
             }
             fresh = fresh && !raise;
           }
-          if (__builtin_expect(special, 0)) {
-            // Weights times values here, of what the row sees only, in fp32. Rare and slow.
-            if (!first && !wait(kPvDone + st, (done - 1) & 1)) break;
-            tc_fence_after();
-            const uint32_t vu = 2 * (tile + j) + 1;
-            const uint8_t* const v = units + (vu % S::kSlots) * S::kUnit;
-#pragma unroll 1
-            for (int d0 = 0; d0 < D; d0 += 8) {
-              float o[8];
-              if (!first) {
-                tmem_ld<8>(o_col + d0, o);
-                tmem_wait_ld();
-                pin<8>(o);
-              } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = 0.f;
-              }
-#pragma unroll 1
-              for (int t = 0; t < 128; t += 8) {
-                float x[8];
-                __syncwarp();
-                tmem_ld<8>(s_col + t, x);
-                tmem_wait_ld();
-                pin<8>(x);
-                const uint32_t w = (t < 32 ? see[0] : t < 64 ? see[1] : t < 96 ? see[2] : see[3]) >> (t & 31);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  if (!((w >> i) & 1)) continue;
-                  float z = x[i];
-                  if (kE4m3) z *= ring_ks[a * 128 + t + i];
-                  float pt = ex2(fmaf(z, p.scale_log2, nm));
-                  if (d0 == 0) l0 += pt;
-                  if (kE4m3) pt *= ring_vs[a * 128 + t + i];
-                  const uint4 e = *reinterpret_cast<const uint4*>(v + (d0 >> 6) * 16384 + (t + i) * 128 +
-                                                                  ((((d0 >> 3) & 7) ^ ((t + i) & 7)) << 4));
-                  const uint32_t ew[4] = {e.x, e.y, e.z, e.w};
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    o[2 * k] = fmaf(pt, __uint_as_float(ew[k] << 16), o[2 * k]);
-                    o[2 * k + 1] = fmaf(pt, __uint_as_float(ew[k] & 0xffff0000u), o[2 * k + 1]);
-                  }
-                }
-              }
-              __syncwarp();
-              tmem_st8(o_col + d0, o);
-            }
-          } else {
+          {
             // P in bf16, in the place of S: 16 columns of pairs for 32 tokens, behind the reads of those
             auto weights = [&](int c, float* x) {
               uint32_t w[16];
@@ -1007,20 +1008,7 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
                 add2(l0, l1, x[i], x[i + 1]);
                 add2(l2, l3, x[i + 2], x[i + 3]);
               }
-              if (kE4m3) {
-#pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                  const float4 k = *reinterpret_cast<const float4*>(ring_vs + a * 128 + 32 * c + i);
-                  mul2(x[i], x[i + 1], k.x, k.y);
-                  mul2(x[i + 2], x[i + 3], k.z, k.w);
-                }
-                if (__builtin_expect(!whole, 0)) {  // a weight of zero stays zero, whatever its scale
-                  const uint32_t vis = c == 0 ? see[0] : c == 1 ? see[1] : c == 2 ? see[2] : see[3];
-#pragma unroll
-                  for (int i = 0; i < 32; ++i)
-                    if (!((vis >> i) & 1)) x[i] = 0.f;
-                }
-              }
+              if (kE4m3) scaled(x, ring_vs + a * 128 + 32 * c);
 #pragma unroll
               for (int i = 0; i < 16; ++i) w[i] = bf16x2(x[2 * i], x[2 * i + 1]);
               tmem_st16(s_col + 16 * c, w);
@@ -1035,14 +1023,13 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
                 tmem_ld<32>(s_col + 32 * c, x);
                 tmem_wait_ld();
                 pin<32>(x);
-                products(c, x);
+                if (kE4m3 && whole) scaled(x, ring_ks + a * 128 + 32 * c);
                 weights(c, x);
               }
             }
           }
           tmem_wait_st();
           tc_fence_before();
-          if (quarter == 0) flags[16 + st] = special;
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(bar(kPFull + st));
@@ -1066,7 +1053,28 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
       constexpr int kCols = kPair ? D : D / 2;  // this thread's columns of the result
       const int col0 = kPair ? 0 : st * kCols;
       const int mine_n = kPair ? sg.ntiles : (sg.ntiles + 1 - st) / 2, other_n = kPair ? 0 : sg.ntiles - mine_n;
-      if (rows > 0 && mine_n > 0 && !wait(kPvDone + st, (done - 1) & 1)) break;
+      if (rows > 0 && mine_n > 0) {
+        if (!wait(kPvDone + st, (done - 1) & 1)) break;
+        // A weight of zero does not keep out an infinite value: where this row did not see all of its tiles' tokens, and its
+        // weights are finite, its result is finite or suspect.
+        if (__builtin_expect(__any_sync(0xffffffffu, hidden), 0)) {
+          tc_fence_after();
+          uint32_t odd = 0;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 16) {
+            float o[16];
+            tmem_ld<16>(o_col + c, o);
+            tmem_wait_ld();
+            pin<16>(o);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) odd |= (__float_as_uint(o[i]) & 0x7f800000u) == 0x7f800000u;
+          }
+          const bool need = odd && hidden && fabsf(l) < INFINITY;
+          if (__any_sync(0xffffffffu, need))
+            redo_row<D, kE4m3>(p, sg, first_row + my_r, my_h, kPair ? 0 : st, step, nm, need, o_col);
+          tc_fence_before();
+        }
+      }
       if (!kPair) {
         other += other_n;
         ml_s[st * 128 + m_row] = make_float2(m, l);
@@ -1089,29 +1097,28 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
         const int m_item = (kPair ? st * 128 : 0) + m_row;
         float* const part = p.part_o + (static_cast<int64_t>(max(sg.slot, 0)) * D + col0) * S::kQueries + m_item;
         uint16_t* const out = p.out + head * D + col0;
-#pragma unroll 2
-        for (int c = 0; c < kCols; c += 8) {
-          float o[8], x[8];
+#pragma unroll 1
+        for (int c = 0; c < kCols; c += 16) {
+          float o[16], x[16];
           __syncwarp();
-          if (kPair || mine_n > 0) tmem_ld<8>(o_col + col0 + c, o);
-          if (!kPair && other_n > 0) tmem_ld<8>(tmem + lanes + 256 + (st ^ 1) * D + col0 + c, x);
+          if (kPair || mine_n > 0) tmem_ld<16>(o_col + col0 + c, o);
+          if (!kPair && other_n > 0) tmem_ld<16>(tmem + lanes + 256 + (st ^ 1) * D + col0 + c, x);
           tmem_wait_ld();
-          pin<8>(o);
-          pin<8>(x);
+          pin<16>(o);
+          pin<16>(x);
           if (!kPair) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = (mine_n > 0 ? o[i] * w_own : 0.f) + (other_n > 0 ? x[i] * w_other : 0.f);
+            for (int i = 0; i < 16; ++i) o[i] = (mine_n > 0 ? o[i] * w_own : 0.f) + (other_n > 0 ? x[i] * w_other : 0.f);
           }
           if (sg.slot >= 0) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) part[(c + i) * S::kQueries] = o[i];
+            for (int i = 0; i < 16; ++i) part[(c + i) * S::kQueries] = o[i];
           } else if (mine_q) {
-            uint4 w;
-            w.x = bf16x2(o[0] * inv, o[1] * inv);
-            w.y = bf16x2(o[2] * inv, o[3] * inv);
-            w.z = bf16x2(o[4] * inv, o[5] * inv);
-            w.w = bf16x2(o[6] * inv, o[7] * inv);
-            *reinterpret_cast<uint4*>(out + c) = w;
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
+            *reinterpret_cast<uint4*>(out + c) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(out + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
           }
         }
         if (kPair || st == 0) {
