@@ -878,7 +878,7 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
       ok = wait_phase(bar(b), parity, abort, limit);
       return ok;
     };
-    uint32_t done = 0, other = 0, tile = 0, scans = 0, joins = 0;  // tiles of this stream and of the other; of all; ...
+    uint32_t done = 0, other = 0, tile = 0, joins = 0;  // tiles of this stream and of the other; of all; rendezvous of the streams
     for (int seg = 0;; ++seg) {
       if (!wait(kSegFull + seg % kSegRing, (seg / kSegRing) & 1)) break;
       const SeqSeg sg = segs[seg % kSegRing];
@@ -889,6 +889,7 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
       const int rows = min(per_tile, sg.nrows - first_row);
       const bool mine_q = my_r < rows;                  // this thread has a query
       const int my_row = sg.row0 + first_row + my_r;
+      const bool any_q = quarter * 32 < rows * p.group;  // a thread of this warp has
       // what all rows of the tile of queries see: [0, all_a) and [all_b, all_c)
       int32_t all_a = 0, all_b = 0, all_c = sg.end0;
       if (!p.tree_mask) {
@@ -912,6 +913,13 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
       if (rows > 0) {
         for (int j = kPair ? 0 : st; j < sg.ntiles; j += step) {
           const int a = (tile + j) % kRing;
+          if (!kPair && !any_q) {  // nothing to do: what stands in this warp's part of P does not matter
+            if (!wait(kSFull + st, done & 1)) break;
+            arrive_one(bar(kPFull + st), lane);
+            arrive_one(bar(kAEmpty + a), lane);
+            ++done;
+            continue;
+          }
           if (!wait((kE4m3 ? kScFull : kAFull) + a, ((tile + j) / kRing) & 1)) break;  // the tile's mask and scales
           if (!wait(kSFull + st, done & 1)) break;
           tc_fence_after();
@@ -1090,7 +1098,7 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
         l = (mine_n > 0 ? l * w_own : 0.f) + (other_n > 0 ? x.y * w_other : 0.f);
         m = top;
       }
-      if (rows > 0) {
+      if (kPair ? rows > 0 : any_q) {
         tc_fence_after();
         const int64_t head = (static_cast<int64_t>(my_row) * p.kv_heads + sg.kvh) * p.group + my_h;
         const float inv = l == 0.f ? 0.f : __fdividef(1.f, l);
