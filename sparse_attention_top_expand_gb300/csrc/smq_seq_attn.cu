@@ -63,8 +63,7 @@ struct SeqShape {
   static constexpr int kSoftmaxRegs = kE4m3 ? 152 : 184;
   static constexpr int kOtherRegs = kE4m3 ? 56 : 72;
   static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= kThreads * kRegs, "");
-  // a thread holds a tile's scores in registers, or reads them twice in loops of 32
-  static constexpr bool kHold = !kE4m3;
+  static constexpr int kStep = 32;  // tokens that a softmax thread takes at a time
   static constexpr int kAddrReaders = (kE4m3 ? 8 : 4) + (kPair ? 8 : 4);  // loader and softmax warps of a tile
   static constexpr int kSegReaders = (kE4m3 ? 8 : 4) + 8 + 3;             // and MMA and address warps
   static constexpr int kRingBytes = kRing * 128 * (8 + (kE4m3 ? 8 : 0)) + kRing * 16;
@@ -270,7 +269,7 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
   auto full_parity = [](uint32_t n) { return (n >> (kPair ? 2 : 1)) & 1; };
 
   __shared__ uint32_t tmem_slot;
-  __shared__ int abort_flag, tensor_lock;
+  __shared__ int abort_flag;
   __shared__ long long warp_sum[kThreads / 32];
   __shared__ int start_seq;
   __shared__ long long start_idx;
@@ -294,7 +293,7 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
     mbar_init_fence();
   }
   if (tid == 0) {
-    abort_flag = tensor_lock = 0;
+    abort_flag = 0;
     start_seq = -1;
   }
   if (warp == 5) tmem_alloc(smem_addr(&tmem_slot), S::kTmem);
@@ -742,11 +741,6 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
             tc_fence_after();
             const uint32_t v_lo = desc_lo(units_a + slot_of(v) * S::kUnit, 16384), k_lo = desc_lo(units_a + slot_of(k) * S::kUnit, 16);
             if (elect_one()) {
-              // Both products of a tile go to the tensor core together: mixed with the other stream's they would end with
-              // them, and the two softmaxes would run side by side instead of one behind the other's products. The holder
-              // waits for nothing, so the lock is free again soon; without it (the limit is never reached) only time is lost.
-              for (int tries = 0; tries < 100000 && atomicCAS(&tensor_lock, 0, 1) != 0; ++tries) {
-              }
               if (values) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)  // 16 tokens
@@ -768,7 +762,6 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
                 if (values) mma_commit(bar(kPvDone + st));
               }
               if (values) mma_commit(bar(kEmpty + slot_of(v)));
-              atomicExch(&tensor_lock, 0);
             }
             __syncwarp();
             issued = true;
@@ -898,9 +891,9 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
         row_sees(p, sg, first_row + rows - 1, skip, all_b, skip);
         if (all_b <= all_a) all_b = 0;
       }
-      auto scaled = [](float* x, const float* by) {  // 32 tokens' scales
+      auto scaled = [](float* x, const float* by) {  // kStep tokens' scales
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
+        for (int i = 0; i < S::kStep; i += 4) {
           const float4 k = *reinterpret_cast<const float4*>(by + i);
           mul2(x[i], x[i + 1], k.x, k.y);
           mul2(x[i + 2], x[i + 3], k.z, k.w);
@@ -948,34 +941,25 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
             }
             tmem_wait_st();
           }
-          float y[S::kHold ? 128 : 1];
-          float most = -INFINITY, most2 = -INFINITY;
-          auto look = [&](const float* y) {
+          constexpr int kStep = S::kStep;  // tokens at a time
+          auto load = [&](int c, float* x) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              most = fmaxf(fmaxf(most, y[i]), y[i + 1]);
-              most2 = fmaxf(fmaxf(most2, y[i + 2]), y[i + 3]);
-            }
-          };
-          if constexpr (S::kHold) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld<32>(s_col + 32 * c, y + 32 * c);
+            for (int i = 0; i < kStep; i += 32) tmem_ld<32>(s_col + c + i, x + i);
             tmem_wait_ld();
-            pin<128>(y);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) look(y + 32 * c);
-          } else {
+            pin<kStep>(x);
+            if (kE4m3 && whole) scaled(x, ring_ks + a * 128 + c);
+          };
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              float x[32];
-              tmem_ld<32>(s_col + 32 * c, x);
-              tmem_wait_ld();
-              pin<32>(x);
-              if (kE4m3 && whole) scaled(x, ring_ks + a * 128 + 32 * c);
-              look(x);
-            }
+          for (int c = 0; c < 128; c += kStep) {
+            float x[kStep];
+            load(c, x);
+#pragma unroll
+            for (int i = 0; i < kStep; i += 8)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) top[k] = fmaxf(fmaxf(top[k], x[i + 2 * k]), x[i + 2 * k + 1]);
           }
-          most = fmaxf(most, most2) * p.scale_log2;
+          float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2;
           const bool raise = fresh ? most > -INFINITY : most + nm > kTau;
           const bool first = j < step;
           if (__builtin_expect(__any_sync(0xffffffffu, raise), 0)) {
@@ -1002,11 +986,14 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
             fresh = fresh && !raise;
           }
           {
-            // P in bf16, in the place of S: 16 columns of pairs for 32 tokens, behind the reads of those
-            auto weights = [&](int c, float* x) {
-              uint32_t w[16];
+            // P in bf16, in the place of S: a column for two tokens, behind the reads of those
+#pragma unroll 1
+            for (int c = 0; c < 128; c += kStep) {
+              float x[kStep];
+              load(c, x);
+              uint32_t w[kStep / 2];
 #pragma unroll
-              for (int i = 0; i < 32; i += 4) {
+              for (int i = 0; i < kStep; i += 4) {
 #pragma unroll
                 for (int k = i; k < i + 4; k += 2) {
                   fma2(x[k], x[k + 1], p.scale_log2, p.scale_log2, nm, nm);
@@ -1016,24 +1003,11 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
                 add2(l0, l1, x[i], x[i + 1]);
                 add2(l2, l3, x[i + 2], x[i + 3]);
               }
-              if (kE4m3) scaled(x, ring_vs + a * 128 + 32 * c);
+              if (kE4m3) scaled(x, ring_vs + a * 128 + c);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) w[i] = bf16x2(x[2 * i], x[2 * i + 1]);
-              tmem_st16(s_col + 16 * c, w);
-            };
-            if constexpr (S::kHold) {
+              for (int i = 0; i < kStep / 2; ++i) w[i] = bf16x2(x[2 * i], x[2 * i + 1]);
 #pragma unroll
-              for (int c = 0; c < 4; ++c) weights(c, y + 32 * c);
-            } else {
-#pragma unroll 1
-              for (int c = 0; c < 4; ++c) {
-                float x[32];
-                tmem_ld<32>(s_col + 32 * c, x);
-                tmem_wait_ld();
-                pin<32>(x);
-                if (kE4m3 && whole) scaled(x, ring_ks + a * 128 + 32 * c);
-                weights(c, x);
-              }
+              for (int i = 0; i < kStep / 2; i += 16) tmem_st16(s_col + c / 2 + i, w + i);
             }
           }
           tmem_wait_st();
