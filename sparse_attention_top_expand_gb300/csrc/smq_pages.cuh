@@ -12,6 +12,8 @@
 namespace smq {
 
 constexpr int kStatusNoPages = 32;  // SMQ_ERR_NO_PAGES
+constexpr int kSegmentUnit = 2048;  // pages
+constexpr int kMaxSegments = 1024;
 
 struct Planes {
   smq_page_plane plane[SMQ_MAX_PLANES];
@@ -34,9 +36,12 @@ struct PagesParams {
   const int32_t* row_end;    // resize: end; fork: length
   const int32_t* src_rows;   // fork: sources, else null
   int32_t* takes;            // [num_rows] pages that row i takes, -1: the row is skipped
-  int32_t* free_count;       // entries of free_list
-  int32_t* free_list;        // the lowest free pages, at most free_cap
-  int32_t free_cap;
+  // The pool in `segments` runs of `segment` pages: the free ones of run k, in order, at free_list + k * segment, and
+  // their number.
+  int32_t segments;
+  int32_t segment;           // a multiple of kSegmentUnit
+  int32_t* free_counts;      // [segments]
+  int32_t* free_list;        // [segments * segment]
   int32_t* snapshot;         // fork: [num_rows][columns] the sources' entries
   int32_t* status;
 };

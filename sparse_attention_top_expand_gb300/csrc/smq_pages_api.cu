@@ -24,21 +24,25 @@ constexpr int kMaxVectors = 1024;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-// Workspace: [status word, 256 B][free count, 256 B][takes or counts][free list][sources' entries of a fork].
+// Workspace: [status word, 256 B][free pages of each segment][takes or counts][free list][sources' entries of a fork].
 struct Scratch {
-  size_t free_count, takes, free_list, snapshot, end;
-  int64_t free_cap;
+  size_t free_counts, takes, free_list, snapshot, end;
+  int64_t segment, segments;
 };
 
 Scratch scratch_of(const smq_page_plan* p) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   const int64_t entries = static_cast<int64_t>(p->desc.table_rows) * p->desc.table_columns;
   Scratch s;
-  s.free_cap = entries < p->desc.num_pages ? entries : p->desc.num_pages;
-  s.free_count = kStatusBytes;
-  s.takes = s.free_count + 256;
+  // segments of 4096 pages, or longer ones so that there are no more than kMaxSegments
+  const int64_t units = (p->desc.num_pages + smq::kSegmentUnit - 1) / smq::kSegmentUnit;
+  const int64_t per = (units + smq::kMaxSegments - 1) / smq::kMaxSegments;
+  s.segment = (per < 2 ? 2 : per) * smq::kSegmentUnit;
+  s.segments = (p->desc.num_pages + s.segment - 1) / s.segment;
+  s.free_counts = kStatusBytes;
+  s.takes = s.free_counts + up(smq::kMaxSegments * sizeof(int32_t));
   s.free_list = s.takes + up(p->desc.table_rows * sizeof(int32_t));
-  s.snapshot = s.free_list + up(s.free_cap * sizeof(int32_t));
+  s.snapshot = s.free_list + up(s.segments * s.segment * sizeof(int32_t));
   s.end = s.snapshot + entries * sizeof(int32_t);
   return s;
 }
@@ -84,7 +88,9 @@ smq::PagesParams params_of(const smq_page_plan* plan, int32_t num_rows, int32_t*
   p.table = table;
   p.refs = refs;
   p.status = reinterpret_cast<int32_t*>(ws);
-  p.free_count = reinterpret_cast<int32_t*>(ws + w.free_count);
+  p.segment = static_cast<int32_t>(w.segment);
+  p.segments = static_cast<int32_t>(w.segments);
+  p.free_counts = reinterpret_cast<int32_t*>(ws + w.free_counts);
   p.takes = reinterpret_cast<int32_t*>(ws + w.takes);
   p.free_list = reinterpret_cast<int32_t*>(ws + w.free_list);
   p.snapshot = reinterpret_cast<int32_t*>(ws + w.snapshot);
@@ -153,8 +159,6 @@ SMQ_API int sparse_mqa_pages_resize(const smq_page_plan* plan, const smq_pages_r
   p.row_begin = a.row_begin;
   p.row_end = a.row_end;
   p.keep_first = a.keep_first;
-  const int64_t entries = static_cast<int64_t>(a.num_rows) * p.columns;  // as many pages as the rows can take
-  p.free_cap = static_cast<int32_t>(entries < p.num_pages ? entries : p.num_pages);
   smq::Planes none = {};
   return smq::launch_pages(p, none, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SMQ_OK : SMQ_ERR_CUDA;
 }
@@ -177,7 +181,6 @@ SMQ_API int sparse_mqa_pages_fork(const smq_page_plan* plan, const smq_pages_for
   p.rows = a.dst_rows;
   p.row_end = a.row_len;
   p.src_rows = a.src_rows;
-  p.free_cap = a.num_rows < p.num_pages ? a.num_rows : p.num_pages;  // a page each
   return smq::launch_pages(p, planes, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SMQ_OK : SMQ_ERR_CUDA;
 }
 
