@@ -302,11 +302,8 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
   // ---- this CTA's range of the tile list: sequences, kv heads, blocks of rows, tiles
   tc_fence_before();
   const int per_tile = 128 / p.group, per_item = (kPair ? 2 : 1) * per_tile;  // rows of a tile of queries, and of an item
-  // tiles of sequence base + lane on one kv head, for the sequences below end
-  auto head_tiles = [&](int base, int end, bool report) {
-    const int b = base + lane;
-    Sequence s = {0, 0, 0};
-    if (b < end) s = sequence_of(p, b, report);
+  // tiles of this lane's sequence on one kv head
+  auto tiles_of = [&](const Sequence& s) {
     long long mine = 0;
     if (s.rows > 0 && s.rows <= per_item) mine = tokens_of(p, s.rows, s.len, 0, s.rows).tiles();
     for (uint32_t many = __ballot_sync(0xffffffffu, s.rows > per_item); many; many &= many - 1) {
@@ -320,6 +317,11 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
     }
     return mine;
   };
+  auto head_tiles = [&](int base, int end, bool report) {  // of sequence base + lane, for the sequences below end
+    Sequence s = {0, 0, 0};
+    if (base + lane < end) s = sequence_of(p, base + lane, report);
+    return tiles_of(s);
+  };
   auto scan_lanes = [&](long long v) {  // inclusive prefix sums
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -328,30 +330,34 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
     }
     return v;
   };
-  constexpr int kWarps = kThreads / 32;
-  const int groups = (p.num_seqs + 31) / 32, per_warp = (groups + kWarps - 1) / kWarps;
-  const int seq0 = warp * per_warp * 32, seq1 = min(p.num_seqs, (warp + 1) * per_warp * 32);
-  long long mine = 0;
-  for (int base = seq0; base < seq1; base += 32) mine += head_tiles(base, seq1, blockIdx.x == 0);
-  mine = scan_lanes(mine * p.kv_heads);
-  if (lane == 31) warp_sum[warp] = mine;
-  __syncthreads();
-  long long before = 0, total = 0;
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += warp_sum[w];
-    total += warp_sum[w];
-  }
-  const long long chunk = div_of(total + gridDim.x - 1, gridDim.x), begin = chunk * blockIdx.x;
-  const long long work = begin < total ? min(chunk, total - begin) : 0;
-  if (work > 0 && begin >= before && begin < before + warp_sum[warp]) {
-    long long at = before;
-    for (int base = seq0; base < seq1; base += 32) {
-      const long long t = head_tiles(base, seq1, false) * p.kv_heads, incl = scan_lanes(t);
-      if (begin >= at + incl - t && begin < at + incl) {
-        start_seq = base + lane;
-        start_idx = begin - (at + incl - t);
+  long long total = 0, chunk = 0, work = 0;  // the scheduler's, which works them out alone where a lane a sequence is enough
+  if (p.num_seqs > 32) {
+    constexpr int kWarps = kThreads / 32;
+    const int groups = (p.num_seqs + 31) / 32, per_warp = (groups + kWarps - 1) / kWarps;
+    const int seq0 = warp * per_warp * 32, seq1 = min(p.num_seqs, (warp + 1) * per_warp * 32);
+    long long mine = 0;
+    for (int base = seq0; base < seq1; base += 32) mine += head_tiles(base, seq1, blockIdx.x == 0);
+    mine = scan_lanes(mine * p.kv_heads);
+    if (lane == 31) warp_sum[warp] = mine;
+    __syncthreads();
+    long long before = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += warp_sum[w];
+      total += warp_sum[w];
+    }
+    chunk = div_of(total + gridDim.x - 1, gridDim.x);
+    const long long begin = chunk * blockIdx.x;
+    work = begin < total ? min(chunk, total - begin) : 0;
+    if (work > 0 && begin >= before && begin < before + warp_sum[warp]) {
+      long long at = before;
+      for (int base = seq0; base < seq1; base += 32) {
+        const long long t = head_tiles(base, seq1, false) * p.kv_heads, incl = scan_lanes(t);
+        if (begin >= at + incl - t && begin < at + incl) {
+          start_seq = base + lane;
+          start_idx = begin - (at + incl - t);
+        }
+        at += __shfl_sync(0xffffffffu, incl, 31);
       }
-      at += __shfl_sync(0xffffffffu, incl, 31);
     }
   }
   __syncthreads();
@@ -604,7 +610,6 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
       cp_wait_all();
     } else if (warp == 4) {
       // ---------------------------------------------------------- scheduler
-      long long left = work;
       int b = 0, g = 0, k = 0, tile0 = 0;  // sequence, kv head, block, and tile of the block
       int base = -64;                      // sequences base .. base + 31 are held, one a lane
       Sequence mine_s = {0, 0, 0}, s = {0, 0, 0};
@@ -614,7 +619,7 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
           base = at;
           mine_s = {0, 0, 0};
           if (at + lane < p.num_seqs) {
-            mine_s = sequence_of(p, at + lane, false);
+            mine_s = sequence_of(p, at + lane, p.num_seqs <= 32 && blockIdx.x == 0);
             mine_t = p.seq_indices ? p.seq_indices[at + lane] : at + lane;
             if (mine_t < 0 || mine_t >= p.bt_rows) mine_t = -1;
           }
@@ -624,12 +629,26 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
         s.len = __shfl_sync(0xffffffffu, mine_s.len, at - base);
         table_row = __shfl_sync(0xffffffffu, mine_t, at - base);
       };
-      if (work > 0) {
-        // the first segment's place within its sequence
+      long long idx = 0, per_head = 1;  // the first segment's place within its sequence
+      if (p.num_seqs <= 32) {
+        load(0);
+        const long long t = tiles_of(mine_s), incl = scan_lanes(t * p.kv_heads);
+        total = __shfl_sync(0xffffffffu, incl, 31);
+        chunk = div_of(total + gridDim.x - 1, gridDim.x);
+        const long long begin = chunk * blockIdx.x;
+        work = begin < total ? min(chunk, total - begin) : 0;
+        const uint32_t here = __ballot_sync(0xffffffffu, begin >= incl - t * p.kv_heads && begin < incl);
+        if (here) b = __ffs(here) - 1;
+        idx = __shfl_sync(0xffffffffu, begin - (incl - t * p.kv_heads), b);
+        per_head = __shfl_sync(0xffffffffu, t, b);
+      } else if (work > 0) {
         b = start_seq;
+        idx = start_idx;
+        per_head = __shfl_sync(0xffffffffu, head_tiles(b, b + 1, false), 0);
+      }
+      long long left = work;
+      if (work > 0) {
         load(b);
-        const long long per_head = __shfl_sync(0xffffffffu, head_tiles(b, b + 1, false), 0);
-        long long idx = start_idx;
         g = static_cast<int>(div_of(idx, per_head));
         idx -= g * per_head;
         for (bool found = false; !found && k * per_item < s.rows; k += found ? 0 : 32) {
@@ -1129,19 +1148,32 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
 
 // Join the partials of an item that CTA `first` of the attention kernel began
 // and others continued: out = sum_i w_i O_i / sum_i w_i l_i with
-// w_i = 2^(m_i - max m), in the order of the list. A block per CTA and 32
+// w_i = 2^(m_i - max m), in the order of the list. A block per such item and 32
 // queries, a lane each; a warp has every eighth column of the result, or with
 // kFew (few items, whose partials are many) every eighth partial of 16 columns.
 template <int D, int kQueries, bool kFew>
-__global__ void __launch_bounds__(256) seq_combine_kernel(const __grid_constant__ SeqAttnParams p) {
+__global__ void __launch_bounds__(256) seq_combine_kernel(const __grid_constant__ SeqAttnParams p, int ctas) {
   constexpr int kCols = kFew ? 16 : D, kPer = kFew ? 16 : D / 8, kWarpParts = kFew ? 8 : 1;
   griddep_launch_dependents();
   griddep_wait();
   __shared__ float o_s[kFew ? 8 : 1][kCols][33];
   __shared__ float2 ml_s[8][32];
-  const int first = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ int first_s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 0) {  // the CTA that began the blockIdx.x-th item that is shared
+    int first = -1, seen = 0;
+    for (int c = 0; c < ctas && first < 0; c += 32) {
+      const uint32_t some = __ballot_sync(0xffffffffu, c + lane < ctas && p.seg_info[c + lane].w > 0);
+      const int skip = static_cast<int>(blockIdx.x) - seen;
+      seen += __popc(some);
+      if (skip < __popc(some)) first = c + static_cast<int>(__fns(some, 0, skip + 1));
+    }
+    if (lane == 0) first_s = first;
+  }
+  __syncthreads();
+  const int first = first_s;
+  if (first < 0) return;
   const int4 info = p.seg_info[first];
-  if (info.w == 0) return;
   const int parts = info.w + 1, per_tile = 128 / p.group;
   const int m0 = blockIdx.y * 32, mi = m0 + lane, col0 = kFew ? blockIdx.z * kCols : 0;
   auto row_of = [&](int i, int& h) {  // the item's row of query i, -1: none
@@ -1249,11 +1281,14 @@ cudaError_t with_kernel(int head_dim, bool e4m3, bool pair, F f) {
 
 template <int D, int kQueries>
 cudaError_t launch_combine(const SeqAttnParams& p, int grid, cudaStream_t stream) {
+  // at most as many items as CTAs are shared, and no more than there are; blocks of 32 queries that some item can have
   const int64_t per = kQueries / 128 * (128 / p.group);
-  const int64_t items = (static_cast<int64_t>(p.rows) / per + p.num_seqs) * p.kv_heads;  // at most
+  const int64_t items = (static_cast<int64_t>(p.rows) / per + p.num_seqs) * p.kv_heads;
+  const unsigned shared = static_cast<unsigned>(items < grid ? items : grid);
+  const int queries = kQueries > 128 ? kQueries : p.max_seq_rows * p.group;
   if (items * 4 < grid)
-    return launch(seq_combine_kernel<D, kQueries, true>, dim3(grid, kQueries / 32, D / 16), 256, 0, stream, p);
-  return launch(seq_combine_kernel<D, kQueries, false>, dim3(grid, kQueries / 32), 256, 0, stream, p);
+    return launch(seq_combine_kernel<D, kQueries, true>, dim3(shared, (queries + 31) / 32, D / 16), 256, 0, stream, p, grid);
+  return launch(seq_combine_kernel<D, kQueries, false>, dim3(shared, (queries + 31) / 32), 256, 0, stream, p, grid);
 }
 
 }  // namespace
