@@ -11,11 +11,52 @@
 // m is raised only when a score exceeds it by kTau (in log2), so the rescale of
 // O stays out of the common path.
 //
-// Two streams, each with its own S, P and O in TMEM and its own softmax group,
-// keep the tensor core busy: one stream's products run behind the other's
-// softmax. Where sequences have more queries than a tile (kPair) the streams are
-// two tiles of queries, and each key and value is read once for both. Otherwise
-// they are one tile of queries over every other tile of tokens, joined in TMEM.
+// Two streams, each with its own S, P and O in TMEM, its own softmax group and
+// its own product warp, keep the tensor core busy: one stream's products run
+// behind the other's softmax. Where sequences have more queries than a tile
+// (kPair) the streams are two tiles of queries, and each key and value is read
+// once for both. Otherwise they are one tile of queries over every other tile of
+// tokens, joined in TMEM.
+//
+// Rounding. Queries, keys and values go to the tensor core as they are held: bf16,
+// and E4M3 codes widened to bf16, which is exact. S, m, l and O are fp32. P is
+// rounded to bf16 (times its token's value scale before that): 2^-8 of a weight at
+// most, some 0.0015 of a result's norm beside the 0.0017 of its own rounding. Two
+// numbers a weight, as in smq_attn.cu, would be half as many products again, and
+// these are what a prefill's time is made of.
+//
+// What a row does not see. Scores of tokens that are not there, or not seen, are
+// minus infinity, so their weights are zeros. That does not keep out an infinite
+// value, or NaN, of a token that other rows of the tile see: at a segment's end
+// rows that missed a token look at their result, and one that is not finite is
+// made again, token by token, from what the row sees.
+//
+// Split. The tiles of all items form one list, cut into equal ranges, one per CTA
+// and SM, whatever the lengths are. A range that starts or ends inside an item
+// leaves an unnormalised partial in the workspace, and seq_combine_kernel joins
+// those of an item in the order of the list: results do not depend on timing.
+//
+// Roles: warps 0-3 copy K, V and Q (cp.async; over an E4M3 cache they bring keys
+// and warps 16-19 values, and widen them), warp 4 cuts the work into segments,
+// warps 5 and 7 issue the products, warp 6 looks up addresses, warps 8-15 are the
+// softmax.
+//
+// What bounds it. A pair of tiles (256 queries by 128 tokens, D 128) is 2048 cycles
+// of products at the tensor core's rate and takes some 3500: S to P, P to the next
+// S and the hand-offs between are a chain that two streams do not cover. The
+// roles run from one instruction cache, and the size of the softmax's loop decides:
+// 4096 rows, 64 heads on 8, a window of 4096 took 536 us with the 128 scores of a
+// thread in registers, 532 in loops of 64 tokens, 454 in loops of 32 that read S
+// from TMEM twice, 516 in loops of 16, and 552 to 607 with the next 32 asked for
+// ahead. It is 1.21 PFLOP/s, 63 % of what a library's product of 8192^3 reaches.
+//  - trees of 64 tokens over contexts of 4096 to 32768, 16 sequences, the same
+//    heads: 507 us, 1.21 PFLOP/s.
+//  - 64 sequences of up to 4 rows, a window of 4096, E4M3: 265 us for 567 MB; a
+//    tile of 128 tokens takes 3400 cycles, of which a loader warp 1400 to widen
+//    its part and 1100 to copy the next (twice as many loader warps: 260), and
+//    every product has 128 queries' rows, of which 8 to 32 are there.
+//  - small calls, 18 to 20 us: three dependent loads to the first key (sequence,
+//    block table, cache), one tile's chain, the join (a launch of its own).
 #include "smq_attn.cuh"
 #include "smq_attn_ptx.cuh"
 #include "smq_kernels.cuh"
@@ -27,7 +68,7 @@ namespace smq {
 
 namespace {
 
-constexpr int kLoaders = 128;  // threads; over an E4M3 cache as many again, a group for keys and one for values
+constexpr int kLoaders = 128;  // threads that copy K, V and Q; over an E4M3 cache these keys and queries, as many again values
 constexpr int kSegRing = 8;    // segments published ahead
 constexpr int kRing = 4;       // tiles whose addresses, masks and scales may be ahead of the softmax
 constexpr float kUnset = -3.0e38f;         // the running maximum of a partial without tokens
@@ -740,14 +781,17 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
       for (int seg = 0; ok; ++seg) {
         if (!wait(kSegFull + seg % kSegRing, (seg / kSegRing) & 1)) break;
         const int n = segs[seg % kSegRing].ntiles;
-        const bool idle = kPair && st == 1 && segs[seg % kSegRing].nrows <= per_tile;  // no queries for this stream
+        // Stream 1 has nothing to do: no queries, or no tile. It gives no sign for the queries' place then, as it could be a
+        // segment ahead: stream 0 gives two.
+        const bool alone = kPair ? segs[seg % kSegRing].nrows <= per_tile : n == 1;
         __syncwarp();
         arrive_one(bar(kSegEmpty + seg % kSegRing), lane);
         if (n == 0) break;
-        if (idle) {  // as if it had read them: each unit when it is there, so that its phases pass one by one
-          for (uint32_t u = unit; u < unit + 2 * n && full(u & 1, u >> 1); ++u) arrive_one(bar(kEmpty + slot_of(u)), lane);
-          arrive_one(bar(kQEmpty), lane);
-        } else if (kPair || st < n) {
+        if (alone && st == 1) {
+          // as if it had read the units: each when it is there, so that its phases pass one by one
+          if (kPair)
+            for (uint32_t u = unit; u < unit + 2 * n && full(u & 1, u >> 1); ++u) arrive_one(bar(kEmpty + slot_of(u)), lane);
+        } else {
           // O += P V of tile j, and S = Q K^T of this stream's next tile behind it
           for (int j = st * (kPair ? 0 : 1) - step; j < n; j += step) {
             const uint32_t v = unit + 2 * j + 1, k = unit + 2 * (j + step);
@@ -776,7 +820,7 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
                 mma_commit(bar(kEmpty + slot_of(k)));
                 if (j + 2 * step >= n) {
                   mma_commit(bar(kQEmpty));
-                  if (!kPair && n == 1) mma_commit(bar(kQEmpty));  // for the stream that has no tile
+                  if (alone) mma_commit(bar(kQEmpty));
                 }
                 if (values) mma_commit(bar(kPvDone + st));
               }
@@ -1004,30 +1048,28 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
             }
             fresh = fresh && !raise;
           }
-          {
-            // P in bf16, in the place of S: a column for two tokens, behind the reads of those
+          // P in bf16, in the place of S: a column for two tokens, behind the reads of those
 #pragma unroll 1
-            for (int c = 0; c < 128; c += kStep) {
-              float x[kStep];
-              load(c, x);
-              uint32_t w[kStep / 2];
+          for (int c = 0; c < 128; c += kStep) {
+            float x[kStep];
+            load(c, x);
+            uint32_t w[kStep / 2];
 #pragma unroll
-              for (int i = 0; i < kStep; i += 4) {
+            for (int i = 0; i < kStep; i += 4) {
 #pragma unroll
-                for (int k = i; k < i + 4; k += 2) {
-                  fma2(x[k], x[k + 1], p.scale_log2, p.scale_log2, nm, nm);
-                  x[k] = ex2(x[k]);
-                  x[k + 1] = ex2(x[k + 1]);
-                }
-                add2(l0, l1, x[i], x[i + 1]);
-                add2(l2, l3, x[i + 2], x[i + 3]);
+              for (int k = i; k < i + 4; k += 2) {
+                fma2(x[k], x[k + 1], p.scale_log2, p.scale_log2, nm, nm);
+                x[k] = ex2(x[k]);
+                x[k + 1] = ex2(x[k + 1]);
               }
-              if (kE4m3) scaled(x, ring_vs + a * 128 + c);
-#pragma unroll
-              for (int i = 0; i < kStep / 2; ++i) w[i] = bf16x2(x[2 * i], x[2 * i + 1]);
-#pragma unroll
-              for (int i = 0; i < kStep / 2; i += 16) tmem_st16(s_col + c / 2 + i, w + i);
+              add2(l0, l1, x[i], x[i + 1]);
+              add2(l2, l3, x[i + 2], x[i + 3]);
             }
+            if (kE4m3) scaled(x, ring_vs + a * 128 + c);
+#pragma unroll
+            for (int i = 0; i < kStep / 2; ++i) w[i] = bf16x2(x[2 * i], x[2 * i + 1]);
+#pragma unroll
+            for (int i = 0; i < kStep / 2; i += 16) tmem_st16(s_col + c / 2 + i, w + i);
           }
           tmem_wait_st();
           tc_fence_before();

@@ -63,6 +63,17 @@ def test_many_sequences():
     ref.Batch(rng, 4, 2, 64, 16, "bf16", seqs).window(50, 3)
 
 
+@pytest.mark.parametrize("heads,kv_heads,dtype", [(64, 8, "bf16"), (12, 2, "e4m3"), (128, 1, "bf16")])
+def test_many_sequences_of_many_blocks(heads, kv_heads, dtype):
+    """More sequences than a warp's lanes, of none to several blocks of rows each."""
+    rng = _rng(13, heads)
+    seqs = []
+    for i in range(150):
+        n = int(rng.integers(0, 70)) if i % 3 else int(rng.integers(0, 2))
+        seqs.append((n, n + int(rng.integers(0, 200))))
+    ref.Batch(rng, heads, kv_heads, 64, 16, dtype, seqs).window(90, 5)
+
+
 @pytest.mark.parametrize("heads,kv_heads,dim,page,dtype", GEOMETRIES)
 def test_tree_matches(heads, kv_heads, dim, page, dtype):
     rng = _rng(heads, dim, 9)
