@@ -108,7 +108,8 @@ struct SeqShape {
   static constexpr int kAddrReaders = (kE4m3 ? 8 : 4) + (kPair ? 8 : 4);  // loader and softmax warps of a tile
   static constexpr int kSegReaders = (kE4m3 ? 8 : 4) + 8 + 3;             // and MMA and address warps
   static constexpr int kRingBytes = kRing * 128 * (8 + (kE4m3 ? 8 : 0)) + kRing * 16;
-  static constexpr int kMisc = kRingBytes + kSegRing * 64 + 512 /*barriers*/ + 2 * 128 * 8 /*m and l*/;
+  static constexpr int kBarBytes = 576;
+  static constexpr int kMisc = kRingBytes + kSegRing * 64 + kBarBytes + 2 * 128 * 8 /*m and l*/;
   static constexpr int kFree = kSmemLimit - kQBytes - kMisc;
   // over an E4M3 cache one or two units of each side (each side's loaders keep to slots of their own, so that a wait's
   // parity names one phase), so that what is left over goes to the copies ahead
@@ -296,18 +297,19 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
   SeqSeg* const segs = reinterpret_cast<SeqSeg*>(ring_mask + kRing * 4);
   float2* const ml_s = reinterpret_cast<float2*>(segs + kSegRing);  // [2][128] maxima and sums to be joined
   uint64_t* const bars = reinterpret_cast<uint64_t*>(ml_s + 256);
-  // kFull: keys, then values, of a stream's tile n (with kPair of both streams'), as many barriers as tiles may be ahead, so
-  // that a wait's parity names one phase
-  constexpr int kFull = 0, kEmpty = kFull + 8, kSFull = kEmpty + S::kSlots, kPFull = kSFull + 2, kPvDone = kPFull + 2,
+  // kFull: keys, then values, of a stream's tile n (with kPair of both streams'): four each, as many as there may be tiles ahead,
+  // all of which can be one stream's, so that a wait's parity names one phase
+  constexpr int kFull = 0, kEmpty = kFull + (kPair ? 8 : 16), kSFull = kEmpty + S::kSlots, kPFull = kSFull + 2, kPvDone = kPFull + 2,
                 kJoin = kPvDone + 2, kQEmpty = kJoin + 1, kQFull = kQEmpty + 1, kSegFull = kQFull + 1,
                 kSegEmpty = kSegFull + kSegRing, kAFull = kSegEmpty + kSegRing, kAEmpty = kAFull + kRing,
                 kDrain = kAEmpty + kRing, kScFull = kDrain + 2, kBars = kScFull + (kE4m3 ? kRing : 0);
-  static_assert(kBars * 8 <= 512 && kBars <= kThreads, "");
+  static_assert(kBars * 8 <= S::kBarBytes && kBars <= kThreads, "");
   auto bar = [&](int i) { return smem_addr(bars + i); };
+  static_assert(S::kSlots <= 8, "");
   auto full_bar = [](int stream, int side, uint32_t n) {
-    return kFull + (kPair ? side * 4 + static_cast<int>(n & 3) : (stream * 2 + side) * 2 + static_cast<int>(n & 1));
+    return kFull + ((kPair ? 0 : stream) * 2 + side) * 4 + static_cast<int>(n & 3);
   };
-  auto full_parity = [](uint32_t n) { return (n >> (kPair ? 2 : 1)) & 1; };
+  auto full_parity = [](uint32_t n) { return (n >> 2) & 1; };
 
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;

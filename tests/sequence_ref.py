@@ -60,9 +60,17 @@ def attend(q, k, v, scale):
 
 
 def bound(out, mean, size, dim, tokens):
-    """As attention_bounds.bound, whose weights have 16 bits; here a weight, times its token's value scale, is rounded to
-    bf16: half a step, 2^-8 of it."""
-    return bounds.bound(out, mean, size, dim, tokens)[0] + 2.0 ** -8 * mean, size * (dim / 16 * 17 + 5) * 2.0 ** -24 + 2.0 ** -20
+    """The largest error of a bf16 result, and of its lse.
+
+    Scores, sums and joins as in attention_bounds.bound. Weights: one, times its token's value scale, is rounded to bf16, half a
+    step: 2^-8 of it. The result is then rounded to the nearest of 8 bits where it is by then: a value below a power of two can
+    be above it through what came before, and its half step is twice as long there, so the step is that of |out| plus all
+    other errors. Weights below 2^-126 of the largest are zero, and so are results below 2^-126."""
+    score = size * (dim / 16 * 17 + 5) * 2.0 ** -24
+    moved = (np.expm1(score) + 2.0 ** -21)[:, None]
+    off = (np.abs(out) + mean) * moved + mean * (2.0 ** -8 + 8 * math.ceil(tokens / 128) * 17 * 2.0 ** -24 + 2.0 ** -20)
+    top = np.maximum(np.abs(out) + off, 2.0 ** -126)
+    return off + 2.0 ** (np.floor(np.log2(top)) - 8) + 2.0 ** -100, score + 2.0 ** -20
 
 
 class Batch:

@@ -65,6 +65,23 @@ def test_many_tiles_for_each_cta(heads, kv_heads, dim, page, dtype, n):
     b.tree([m for r, _ in seqs for m in ref.random_tree(rng, r)])
 
 
+@pytest.mark.parametrize("heads,kv_heads,dim,dtype", [(64, 8, 64, "bf16"), (4, 4, 64, "bf16"), (64, 8, 128, "bf16"),
+                                                      (16, 8, 64, "e4m3"), (64, 8, 128, "e4m3")])
+@pytest.mark.parametrize("rows", [1, 3])
+def test_many_items_of_one_tile(heads, kv_heads, dim, dtype, rows):
+    """Short contexts, one tile each, so that tile after tile is the same stream's; sixty calls with the same bits."""
+    rng = _rng(heads, dim, rows)
+    seqs = [(rows, rows + int(rng.integers(0, 120))) for _ in range(700)]
+    b = ref.Batch(rng, heads, kv_heads, dim, 32, dtype, seqs)
+    b.window(1000)
+    first = b.out.clone(), b.lse.clone()
+    for _ in range(60):
+        b.out.fill_(3)
+        b.made()
+        assert torch.equal(first[0][:-2], b.out[:-2]) and torch.equal(first[1], b.lse)
+    assert smq.smq_get_status(b.workspace) == 0
+
+
 def test_two_calls_at_once():
     """Two streams, a workspace each, over one cache; sixteen rounds, the same bits every time."""
     rng = _rng(5)
