@@ -51,9 +51,9 @@
 // ahead. It is 1.21 PFLOP/s, 63 % of what a library's product of 8192^3 reaches.
 //  - trees of 64 tokens over contexts of 4096 to 32768, 16 sequences, the same
 //    heads: 507 us, 1.21 PFLOP/s.
-//  - 64 sequences of up to 4 rows, a window of 4096, E4M3: 265 us for 567 MB; a
+//  - 64 sequences of up to 4 rows, a window of 4096, E4M3: 260 us for 567 MB; a
 //    tile of 128 tokens takes 3400 cycles, of which a loader warp 1400 to widen
-//    its part and 1100 to copy the next (twice as many loader warps: 260), and
+//    its part and 1100 to copy the next (twice as many loader warps: the same), and
 //    every product has 128 queries' rows, of which 8 to 32 are there.
 //  - small calls, 18 to 20 us: three dependent loads to the first key (sequence,
 //    block table, cache), one tile's chain, the join (a launch of its own).
@@ -1010,9 +1010,21 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
           auto load = [&](int c, float* x) {
 #pragma unroll
             for (int i = 0; i < kStep; i += 32) tmem_ld<32>(s_col + c + i, x + i);
+            float4 by[kE4m3 ? kStep / 4 : 1];  // the scales come while the scores do
+            if (kE4m3) {
+#pragma unroll
+              for (int i = 0; i < kStep / 4; ++i) by[kE4m3 ? i : 0] = *reinterpret_cast<const float4*>(ring_ks + a * 128 + c + 4 * i);
+            }
             tmem_wait_ld();
             pin<kStep>(x);
-            if (kE4m3 && whole) scaled(x, ring_ks + a * 128 + c);
+            if (kE4m3 && whole) {
+#pragma unroll
+              for (int i = 0; i < kStep / 4; ++i) {
+                const float4 k = by[kE4m3 ? i : 0];
+                mul2(x[4 * i], x[4 * i + 1], k.x, k.y);
+                mul2(x[4 * i + 2], x[4 * i + 3], k.z, k.w);
+              }
+            }
           };
           float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
