@@ -6,7 +6,8 @@
 // each listed row takes), pages_apply_kernel writes. Ranks come from prefix
 // sums in the order of rows and columns; counts change by atomic additions,
 // whose order does not matter. A row is a block's work in both: with a warp a row
-// 512 rows of 2048 columns took 74 us.
+// 512 rows of 2048 columns over 524288 pages took 74 us, so 21. Small calls are two
+// launches, some 9 us.
 #include "smq_pages.cuh"
 
 #include "smq_kernels.cuh"
@@ -375,7 +376,10 @@ __global__ void __launch_bounds__(kApplyThreads)
 // CTAs share each round and meet in between; where no place is the source of
 // another, as when the newer part of a context moves forward, they need not.
 //
-// Bound by DRAM, half reads, half writes.
+// Bound by DRAM, half reads, half writes: 604 MB of 16 contexts, 256-byte tokens,
+// 238 us, 5.1 TB/s of both together. Two 16-byte pieces a thread and eight CTAs an
+// SM; four pieces measured 265, eight with the next round in flight 319. 64 rows of
+// up to eight tokens take 5.4 us.
 
 namespace {
 
