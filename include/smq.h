@@ -702,8 +702,8 @@ SMQ_API int sparse_mqa_pages_resize(const smq_page_plan *plan, const smq_pages_r
 typedef struct smq_page_plane {
   void *base;             /* device, 4-byte aligned */
   int64_t page_stride;    /* bytes, a multiple of 4, >= vectors * page_size * token_bytes */
-  int32_t vectors;        /* >= 1 */
-  int32_t token_bytes;    /* a multiple of 4 */
+  int32_t vectors;        /* 1 .. 1024 */
+  int32_t token_bytes;    /* a multiple of 4, at most 2048 */
 } smq_page_plane;
 
 enum { SMQ_MAX_PLANES = 8 };

@@ -386,6 +386,7 @@ namespace {
 constexpr int kMoveThreads = 256;
 constexpr int kMovePieces = 2;        // of 16 or 4 bytes, per thread and round
 constexpr int kMoveTokens = 256;      // most of a CTA's part of a round
+static_assert(kMaxTokenBytes / 4 <= kMoveThreads * kMovePieces, "a CTA's part of a round holds a token");
 constexpr int kCheckThreads = 1024;
 constexpr int kFusedKeep = 1024;      // longest list that every block checks for itself
 constexpr int kApart = 1 << 30;       // in a count: no place is the source of another

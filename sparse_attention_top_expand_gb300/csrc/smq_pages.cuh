@@ -14,6 +14,7 @@ namespace smq {
 constexpr int kStatusNoPages = 32;  // SMQ_ERR_NO_PAGES
 constexpr int kSegmentUnit = 2048;  // pages
 constexpr int kMaxSegments = 1024;
+constexpr int kMaxTokenBytes = 2048;  // of a plane
 
 struct Planes {
   smq_page_plane plane[SMQ_MAX_PLANES];

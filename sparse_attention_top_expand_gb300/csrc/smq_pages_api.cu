@@ -19,7 +19,6 @@ struct smq_page_plan {
 namespace {
 
 constexpr size_t kStatusBytes = 256;
-constexpr int kMaxTokenBytes = 4096;  // of a plane
 constexpr int kMaxVectors = 1024;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -67,7 +66,7 @@ int take_planes(const smq_page_plan* p, const smq_page_plane* from, int32_t coun
     const smq_page_plane& q = from[i];
     if (!q.base || !aligned(q.base, 4) || q.vectors <= 0 || q.token_bytes <= 0 || q.token_bytes % 4 != 0 || q.page_stride % 4 != 0)
       return SMQ_ERR_INVALID_ARG;
-    if (q.vectors > kMaxVectors || q.token_bytes > kMaxTokenBytes) return SMQ_ERR_UNSUPPORTED;
+    if (q.vectors > kMaxVectors || q.token_bytes > smq::kMaxTokenBytes) return SMQ_ERR_UNSUPPORTED;
     if (q.page_stride < static_cast<int64_t>(q.vectors) * p->desc.page_size * q.token_bytes) return SMQ_ERR_INVALID_ARG;
     to->plane[i] = q;
   }

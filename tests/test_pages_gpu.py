@@ -241,6 +241,22 @@ def test_compact_of_a_long_row():
     b.compact([1, 0], _pad([np.arange(2, page * columns), np.arange(1, page * columns)]))
 
 
+@pytest.mark.parametrize("width", [2048, 2044, 1040, 4])
+def test_tokens_of_every_size(width):
+    """The longest tokens of a plane, in pieces of 16 bytes and of 4, and the shortest."""
+    rng = _rng(width)
+    b = Both(8, 70, 4, 12, kinds=())
+    store = torch.randint(0, 256, (70, 2, 8, width), device=DEV, dtype=torch.uint8)
+    b.planes, b.stores = [store], [store]
+    b.host.planes = [b._bits(store)]
+    b.resize([90, 96, 50, 0])
+    b.compact([3, 0, 10], _pad([np.flatnonzero(rng.random(87) < 0.7) + 3, np.arange(48, 96), np.arange(10, 50)]), rows=[0, 1, 2])
+    long = np.full((1, 1100), -1, np.int32)
+    long[0, :60] = np.sort(rng.permutation(90)[:60])
+    b.compact([0], long, rows=[0])
+    b.fork([0, 1], [3, 2], [61, 95])
+
+
 def test_compact_refuses_rows_whole():
     b = Both(16, 40, 6, 5)
     b.resize([80, 80, 80, 80, 80, 40])
@@ -381,7 +397,7 @@ def test_the_library_refuses_bad_arguments(op, field, value, code):
 
 @pytest.mark.parametrize("field,value,code", [
     ("base", None, BAD), ("base", 2, BAD), ("page_stride", 6, BAD), ("page_stride", 4, BAD), ("vectors", 0, BAD), ("token_bytes", 0, BAD),
-    ("token_bytes", 6, BAD), ("vectors", 1025, smq.SMQ_ERR_UNSUPPORTED), ("token_bytes", 4100, smq.SMQ_ERR_UNSUPPORTED),
+    ("token_bytes", 6, BAD), ("vectors", 1025, smq.SMQ_ERR_UNSUPPORTED), ("token_bytes", 2052, smq.SMQ_ERR_UNSUPPORTED),
 ])
 def test_the_library_refuses_bad_planes(field, value, code):
     for op in ("fork", "compact"):
