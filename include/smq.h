@@ -459,6 +459,8 @@ typedef struct smq_attn_plan_desc {
   int32_t max_rows;      /* upper bound on rows per call, <= 8192 */
   int32_t device;        /* CUDA device ordinal the plan runs on */
   float softmax_scale;   /* finite; 0 picks 1 / sqrt(D) */
+  int32_t max_sequence_rows; /* upper bound on rows and sequences of a window or tree call below, <= 1048576; an append
+                                takes as many rows as the larger bound. 0, or a struct_size that ends before it: max_rows */
 } smq_attn_plan_desc;
 
 /* As smq_plan_create / destroy / set_wait_limit / inject_stall: host memory
@@ -490,7 +492,7 @@ SMQ_API int smq_attn_workspace_init(const smq_attn_plan *plan, void *workspace, 
  * sparse_mqa_quantize_q. Inputs to an E4M3 cache must be finite. */
 typedef struct smq_append_args {
   uint32_t struct_size;
-  int32_t rows;               /* tokens >= 0 */
+  int32_t rows;               /* tokens, 0 .. the larger of the plan's max_rows and max_sequence_rows */
   const uint16_t *q;          /* device bf16, row t at q + t * q_stride: [H][D], 16-byte aligned; or NULL */
   const uint16_t *k;          /* device bf16, row t at k + t * k_stride: [KVH][D], 16-byte aligned */
   const uint16_t *v;          /* device bf16, row t at v + t * v_stride: [KVH][D], 16-byte aligned */
@@ -592,7 +594,7 @@ SMQ_API int sparse_mqa_attention_selected(const smq_attn_plan *plan, const smq_a
  * --------------------------------------------------------------------------- */
 typedef struct smq_seq_attention_args {
   uint32_t struct_size;
-  int32_t rows;               /* rows of q, out and lse, 0 .. the plan's max_rows */
+  int32_t rows;               /* rows of q, out and lse, 0 .. the plan's max_sequence_rows */
   const uint16_t *q;          /* device bf16, row r at q + r * q_stride: [H][D], 16-byte aligned */
   int64_t q_stride;           /* elements, a multiple of 8, >= H * D */
   const void *k_cache;        /* device pages, 16-byte aligned */
@@ -605,8 +607,8 @@ typedef struct smq_seq_attention_args {
   const int32_t *block_table; /* device [bt_rows][bt_stride] page ids */
   int32_t bt_rows;
   int32_t bt_stride;
-  int32_t num_seqs;           /* sequences, 0 .. the plan's max_rows */
-  int32_t max_seq_rows;       /* no sequence has more rows: 1 .. the plan's max_rows */
+  int32_t num_seqs;           /* sequences, 0 .. the plan's max_sequence_rows */
+  int32_t max_seq_rows;       /* no sequence has more rows: 1 .. the plan's max_sequence_rows */
   const int32_t *seq_indices; /* device [num_seqs] sequence -> block-table row, or NULL = identity */
   const int32_t *cu_rows;     /* device [num_seqs + 1] */
   const int32_t *seq_len;     /* device [num_seqs] */

@@ -77,7 +77,7 @@ class SMQSourceArgs(ctypes.Structure):
 class SMQAttnPlanDesc(ctypes.Structure):
     _fields_ = [("struct_size", _c_u32), ("num_heads", _c_i32), ("num_kv_heads", _c_i32), ("head_dim", _c_i32),
                 ("page_size", _c_i32), ("cache_type", _c_i32), ("max_rows", _c_i32), ("device", _c_i32),
-                ("softmax_scale", ctypes.c_float)]
+                ("softmax_scale", ctypes.c_float), ("max_sequence_rows", _c_i32)]
 
 
 class SMQAppendArgs(ctypes.Structure):
@@ -543,7 +543,10 @@ _CACHE_TYPES = {"bf16": 0, "e4m3": 1}
 class AttentionPlan:
     """A validated attention geometry (smq_attn_plan_create); close() or GC frees it.
 
-    cache_dtype is "bf16" or "e4m3"; softmax_scale None is 1 / sqrt(head_dim)."""
+    cache_dtype is "bf16" or "e4m3"; softmax_scale None is 1 / sqrt(head_dim). max_rows bounds the rows of a call (up to
+    1048576); sparse_mqa_attention_decode and sparse_mqa_attention_selected take 8192 of them at most."""
+
+    MAX_SINGLE_ROWS = 8192  # of a call whose rows are sequences of their own
 
     def __init__(self, num_heads: int, num_kv_heads: int, head_dim: int, page_size: int, max_rows: int,
                  cache_dtype: str = "bf16", softmax_scale: Optional[float] = None, device: Optional[int] = None):
@@ -557,7 +560,8 @@ class AttentionPlan:
         self.device_index = int(device)
         self.device = torch.device("cuda", self.device_index)
         d = SMQAttnPlanDesc(ctypes.sizeof(SMQAttnPlanDesc), num_heads, num_kv_heads, head_dim, page_size,
-                            _CACHE_TYPES[cache_dtype], max_rows, self.device_index, softmax_scale or 0.0)
+                            _CACHE_TYPES[cache_dtype], min(max_rows, self.MAX_SINGLE_ROWS), self.device_index,
+                            softmax_scale or 0.0, max_rows)
         h = _vp()
         _check(lib.smq_attn_plan_create(ctypes.byref(d), ctypes.byref(h)), "smq_attn_plan_create")
         self.handle = h

@@ -6,6 +6,7 @@
 
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstddef>
 #include <cstdint>
@@ -24,6 +25,7 @@ struct smq_attn_plan {
 namespace {
 
 constexpr size_t kStatusBytes = 256;
+constexpr int kMaxSequenceRows = 1 << 20;  // of a window or tree call and of an append: no scratch of theirs grows with rows
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -170,8 +172,9 @@ int run_seq_attention(const smq_attn_plan* plan, const smq_seq_attention_args* a
   if (!plan || !args || args->struct_size < sizeof(smq_seq_attention_args)) return SMQ_ERR_INVALID_ARG;
   const smq_seq_attention_args& a = *args;
   const smq_attn_plan_desc& d = plan->desc;
-  if (a.rows < 0 || a.rows > d.max_rows || a.num_seqs < 0 || a.num_seqs > d.max_rows) return SMQ_ERR_INVALID_ARG;
-  if (a.max_seq_rows <= 0 || a.max_seq_rows > d.max_rows) return SMQ_ERR_INVALID_ARG;
+  const int32_t most = d.max_sequence_rows;
+  if (a.rows < 0 || a.rows > most || a.num_seqs < 0 || a.num_seqs > most) return SMQ_ERR_INVALID_ARG;
+  if (a.max_seq_rows <= 0 || a.max_seq_rows > most) return SMQ_ERR_INVALID_ARG;
   if (tree) {
     if (a.window != 0 || a.sinks != 0 || a.mask_words <= 0 || a.mask_words > 32 || a.max_seq_rows > 32 * a.mask_words)
       return SMQ_ERR_INVALID_ARG;
@@ -245,15 +248,19 @@ int run_seq_attention(const smq_attn_plan* plan, const smq_seq_attention_args* a
 extern "C" {
 
 SMQ_API int smq_attn_plan_create(const smq_attn_plan_desc* desc, smq_attn_plan** plan) {
-  if (!desc || !plan || desc->struct_size < sizeof(smq_attn_plan_desc)) return SMQ_ERR_INVALID_ARG;
+  constexpr size_t kWithoutSequences = offsetof(smq_attn_plan_desc, max_sequence_rows);  // callers built before that field
+  if (!desc || !plan || desc->struct_size < kWithoutSequences) return SMQ_ERR_INVALID_ARG;
   *plan = nullptr;
-  const smq_attn_plan_desc& d = *desc;
+  smq_attn_plan_desc d = {};
+  std::memcpy(&d, desc, desc->struct_size < sizeof d ? kWithoutSequences : sizeof d);
+  if (d.max_sequence_rows == 0) d.max_sequence_rows = d.max_rows;
   if (d.num_heads <= 0 || d.num_kv_heads <= 0 || d.num_heads % d.num_kv_heads != 0 || d.page_size <= 0 ||
-      d.max_rows <= 0 || d.device < 0 || !std::isfinite(d.softmax_scale))
+      d.max_rows <= 0 || d.max_sequence_rows <= 0 || d.device < 0 || !std::isfinite(d.softmax_scale))
     return SMQ_ERR_INVALID_ARG;
   if (d.cache_type != SMQ_CACHE_BF16 && d.cache_type != SMQ_CACHE_E4M3) return SMQ_ERR_INVALID_ARG;
   if ((d.head_dim != 64 && d.head_dim != 128) || d.num_heads > 1024 || d.num_kv_heads > 128 ||
-      d.num_heads / d.num_kv_heads > 128 || d.page_size > 65536 || d.max_rows > smq::kMaxRowsPerCall)
+      d.num_heads / d.num_kv_heads > 128 || d.page_size > 65536 || d.max_rows > smq::kMaxRowsPerCall ||
+      d.max_sequence_rows > kMaxSequenceRows)
     return SMQ_ERR_UNSUPPORTED;
   int count = 0;
   if (cudaGetDeviceCount(&count) != cudaSuccess || d.device >= count) return SMQ_ERR_CUDA;
@@ -308,7 +315,7 @@ SMQ_API int sparse_mqa_append_kv(const smq_attn_plan* plan, const smq_append_arg
   if (!plan || !args || args->struct_size < sizeof(smq_append_args)) return SMQ_ERR_INVALID_ARG;
   const smq_append_args& a = *args;
   const smq_attn_plan_desc& d = plan->desc;
-  if (a.rows < 0 || a.rows > d.max_rows) return SMQ_ERR_INVALID_ARG;
+  if (a.rows < 0 || a.rows > std::max(d.max_rows, d.max_sequence_rows)) return SMQ_ERR_INVALID_ARG;
   if (a.rows == 0) return SMQ_OK;
   const int64_t kv_row = static_cast<int64_t>(d.num_kv_heads) * d.head_dim;
   if (!strided_ok(a.k, a.k_stride, kv_row) || !strided_ok(a.v, a.v_stride, kv_row)) return SMQ_ERR_INVALID_ARG;

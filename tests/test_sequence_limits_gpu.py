@@ -1,0 +1,79 @@
+"""The sequences' attention at the ends of its ranges: more rows than a call of single rows takes, as many sequences, and one
+prefill of them all."""
+
+import numpy as np
+import pytest
+import torch
+
+import sparse_attention_top_expand_gb300 as smq
+
+import sequence_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+
+
+def _rng(*seed):
+    return np.random.Generator(np.random.PCG64(list(seed)))
+
+
+def _sets(seqs, window, sinks):
+    """What ref.window_sets says, by ranges: the contexts here are long."""
+    got = []
+    for n, length in seqs:
+        per = []
+        for at in range(length - n, length):
+            lo = max(0, at + 1 - window)
+            per.append(np.concatenate([np.arange(min(sinks, lo)), np.arange(lo, max(0, at + 1))]).astype(np.int64))
+        got.append(per)
+    return got
+
+
+def test_the_sets_are_those_of_the_plain_form():
+    for n, length, window, sinks in ((3, 6, 2, 1), (3, 2, 5, 0), (9, 40, 7, 12), (5, 5, 1, 2)):
+        want = ref.window_sets(n, length, window, sinks)
+        assert [x.tolist() for x in _sets([(n, length)], window, sinks)[0]] == [x.tolist() for x in want]
+
+
+@pytest.mark.parametrize("heads,kv_heads,dtype,seqs", [
+    (8, 1, "bf16", [(213 + 40 * i // 59, 213 + 40 * i // 59 + 10 * i) for i in range(60)]),  # ragged chunks, 13954 rows with padding
+    (4, 2, "e4m3", [(9001, 9300), (1, 50)]),                                                 # one long prefill
+    (2, 1, "bf16", [(1, 1 + i % 90) for i in range(9500)]),                                  # a token of each of many sequences
+])
+def test_more_rows_than_a_call_of_single_rows(heads, kv_heads, dtype, seqs):
+    b = ref.Batch(_rng(heads, len(seqs)), heads, kv_heads, 64, 64, dtype, seqs)
+    assert b.rows > smq.AttentionPlan.MAX_SINGLE_ROWS and b.plan.max_rows == b.rows
+    assert b.call(window=300, sinks=3) == 0
+    sets = _sets(seqs, 300, 3)
+    b.check(sets, rows={i for n, _ in seqs[:70] for i in range(n) if i < 3 or i % 97 == 0 or i > n - 4})
+    if max(n for n, _ in seqs) == 1:
+        b.tree([{0}] * len(seqs))
+
+
+def test_an_append_of_as_many_rows():
+    rows, page, pages = 9000, 64, 150
+    plan = smq.AttentionPlan(4, 2, 64, page, max_rows=rows)
+    data = torch.zeros(pages, 2, 2, page, 64, device=DEV, dtype=torch.bfloat16)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    k, v = (torch.randn(rows, 2, 64, generator=g, device=DEV).to(torch.bfloat16) for _ in range(2))
+    slots = torch.randperm(pages * page, generator=g, device=DEV)[:rows]
+    ws = plan.workspace()
+    smq.sparse_mqa_append_kv(plan, None, k, v, None, None, slots, data[:, 0], data[:, 1], ws)
+    assert smq.smq_get_status(ws) == 0
+    for side, x in ((0, k), (1, v)):
+        assert torch.equal(data[slots // page, side, :, slots % page], x)
+
+
+def test_calls_of_single_rows_keep_their_bound():
+    rows = smq.AttentionPlan.MAX_SINGLE_ROWS + 1
+    plan = smq.AttentionPlan(1, 1, 64, 16, max_rows=rows)
+    data = torch.zeros(2, 2, 1, 16, 64, device=DEV, dtype=torch.bfloat16)
+    q = torch.zeros(rows, 1, 64, device=DEV, dtype=torch.bfloat16)
+    out, table = torch.full_like(q, 5), torch.zeros(1, 1, dtype=torch.int32, device=DEV)
+    ws, at = plan.workspace(), torch.zeros(rows, dtype=torch.int32, device=DEV)
+    with pytest.raises(smq.SMQError) as e:
+        smq.sparse_mqa_attention_decode(plan, q, data[:, 0], data[:, 1], table, at, at + 1, out, ws)
+    assert e.value.code == smq.SMQ_ERR_INVALID_ARG and (out == 5).all()
+    smq.sparse_mqa_attention_decode(plan, q[1:], data[:, 0], data[:, 1], table, at[1:], at[1:] + 1, out[1:], ws)
+    assert smq.smq_get_status(ws) == 0 and (out[1:] == 0).all() and (out[0] == 5).all()
