@@ -100,6 +100,10 @@ __device__ __forceinline__ void sts16(uint32_t a, uint32_t x, uint32_t y, uint32
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
+__device__ __forceinline__ void lds16(uint32_t a, uint32_t* v) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(a) : "memory");
+}
+
 // kN consecutive columns of this thread's TMEM lane; valid after tmem_wait_ld, behind pin().
 template <int kN>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, float* v) {

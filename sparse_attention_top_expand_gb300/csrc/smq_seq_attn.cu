@@ -27,9 +27,11 @@
 //
 // What a row does not see. Scores of tokens that are not there, or not seen, are
 // minus infinity, so their weights are zeros. That does not keep out an infinite
-// value, or NaN, of a token that other rows of the tile see: at a segment's end
-// rows that missed a token look at their result, and one that is not finite is
-// made again, token by token, from what the row sees.
+// value, or NaN, of a token that other rows of the tile see. So a warp looks
+// through the values of the tokens that some row of its own does not see, of a
+// masked tile only; where one is not finite it sums that tile for its rows by
+// hand, with each row's own tokens, in place of the product. The work is that of
+// the tile (some 160 us), whatever the context's length.
 //
 // Split. The tiles of all items form one list, cut into equal ranges, one per CTA
 // and SM, whatever the lengths are. A range that starts or ends inside an item
@@ -226,56 +228,91 @@ __device__ __forceinline__ uint32_t seen_by(const SeqAttnParams& p, const SeqSeg
   return v;
 }
 
-template <bool kE4m3>
-__device__ __forceinline__ float element(const void* base, int64_t at) {
-  if (kE4m3) {
-    uint32_t lo, hi;
-    widen4(static_cast<const uint8_t*>(base)[at], lo, hi);
-    return __uint_as_float(lo << 16);
-  }
-  return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(base)[at]) << 16);
-}
-
-// A row's O again, token by token and from the cache, of the tokens that it sees only: where an infinite value or NaN that
-// other rows see has met this row's weight of zero in the product, and for the rows that do see it. Rare, and slow. A warp's
-// call; the lanes with `need` replace their lanes of O, the sum of tiles tile0, tile0 + step, ... of the segment.
-template <int D, bool kE4m3>
-__device__ __noinline__ void redo_row(const SeqAttnParams& p, const SeqSeg& sg, int r, int h, int tile0, int step, float nm,
-                                      bool need, uint32_t o_col) {
-  float o[D];
-  for (int d = 0; d < D; ++d) o[d] = 0.f;
-  if (need) {
-    const int64_t head = static_cast<int64_t>(sg.kvh) * p.group + h;
-    const uint16_t* const q = p.q + (static_cast<int64_t>(sg.row0) + r) * p.q_stride + head * D;
-    for (int j = tile0; j < sg.ntiles; j += step) {
-      for (int32_t i = 0; i < kAttnTile; ++i) {
-        const int32_t e = (sg.tile0 + j) * kAttnTile + i;
-        if (e >= sg.count || !(seen_by(p, sg, e, r) & 1)) continue;
-        const int32_t pos = e < sg.s0 ? e : e + sg.gap, col = pos / p.page_size;
-        const int64_t page = sg.table_row < 0 ? -1 : p.block_table[static_cast<int64_t>(sg.table_row) * p.bt_stride + col];
-        if (page < 0 || page >= p.num_pages) continue;
-        const int64_t vec = static_cast<int64_t>(sg.kvh) * p.page_size + (pos - col * p.page_size);
-        const int64_t at = page * p.page_stride + vec * D;
-        float x = 0.f;
-        for (int d = 0; d < D; ++d) x = fmaf(element<false>(q, d), element<kE4m3>(p.k_cache, at + d), x);
-        if (kE4m3) x *= p.k_scales[page * p.scale_page_stride + vec];
-        if (p.negate) x = -x;
-        float w = ex2(fmaf(x, p.scale_log2, nm));
-        if (kE4m3) w *= p.v_scales[page * p.scale_page_stride + vec];
-        for (int d = 0; d < D; ++d) o[d] = fmaf(w, element<kE4m3>(p.v_cache, at + d), o[d]);
-      }
+// Whether a value is not finite among those of `tokens` (bits) of the 32 from t0 on of a unit of values; a warp's call, each
+// lane's answer is of its pieces.
+template <int D>
+__device__ __forceinline__ bool not_finite(uint32_t unit, uint32_t tokens, int t0, int lane) {
+  constexpr int kChunks = D / 8, kTok = 32 / kChunks;  // 16-byte pieces of a token, tokens per warp instruction
+  const int piece = lane % kChunks, sub = lane / kChunks;
+  const uint32_t base = unit + (piece >> 3) * 16384 + (t0 + sub) * 128;
+  __nv_bfloat162 most = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll 4
+  for (int i = 0; i < 32; i += kTok) {
+    uint32_t w[4];
+    lds16(base + i * 128 + (((piece & 7) ^ ((i + sub) & 7)) << 4), w);
+    const uint32_t keep = (tokens >> (i + sub)) & 1 ? 0x7fff7fffu : 0u;  // without signs
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      w[k] &= keep;
+      most = __hmax2_nan(most, *reinterpret_cast<const __nv_bfloat162*>(w + k));
     }
   }
+  const uint32_t m = *reinterpret_cast<const uint32_t*>(&most);
+  return (m & 0x7f80u) == 0x7f80u || (m & 0x7f800000u) == 0x7f800000u;
+}
+
+// A masked tile by hand, in fp32, for a warp's rows: O so far (zero for the `first` tile) and the values of the tokens that
+// each row sees. The product of the tile, which the other warps' rows need, goes ahead, and what it makes of these rows is
+// replaced. False where a wait ran out. bars: P written, addresses free, and the product done, of this tile and, with the
+// other parity, of the one before.
+template <int D>
+__device__ __noinline__ bool tile_by_hand(uint32_t p_col, uint32_t o_col, uint32_t unit, const uint32_t* seen, bool first,
+                                          uint32_t p_full, uint32_t a_empty, uint32_t pv_done, uint32_t parity,
+                                          const volatile int* abort, uint64_t limit) {
+  const int lane = threadIdx.x & 31;
+  if (!first && !wait_phase(pv_done, parity ^ 1, abort, limit)) return false;
+  tc_fence_after();
+  float w[64], sum[D];  // (local memory)
+#pragma unroll 1
+  for (int c = 0; c < 64; c += 16) {
+    float x[16];
+    tmem_ld<16>(p_col + c, x);
+    tmem_wait_ld();
+    pin<16>(x);
+    for (int i = 0; i < 16; ++i) w[c + i] = x[i];
+  }
+#pragma unroll 1
+  for (int c = 0; c < D; c += 16) {
+    float o[16];
+    tmem_ld<16>(o_col + c, o);
+    tmem_wait_ld();
+    pin<16>(o);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] = first ? 0.f : o[i];
+#pragma unroll 1
+    for (int t = 0; t < 128; ++t) {
+      uint32_t v[8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        lds16(unit + (c >> 6) * 16384 + t * 128 + (((((c & 63) >> 3) + h) ^ (t & 7)) << 4), v + 4 * h);
+      if (!((seen[t >> 5] >> (t & 31)) & 1)) continue;
+      const uint32_t pair = __float_as_uint(w[t >> 1]);
+      const float p = __uint_as_float(t & 1 ? pair & 0xffff0000u : pair << 16);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        o[2 * i] = fmaf(p, __uint_as_float(v[i] << 16), o[2 * i]);
+        o[2 * i + 1] = fmaf(p, __uint_as_float(v[i] & 0xffff0000u), o[2 * i + 1]);
+      }
+    }
+    __syncwarp();
+    for (int i = 0; i < 16; ++i) sum[c + i] = o[i];
+  }
+  tc_fence_before();
   __syncwarp();
+  arrive_one(p_full, lane);
+  arrive_one(a_empty, lane);
+  if (!wait_phase(pv_done, parity, abort, limit)) return false;
+  tc_fence_after();
+#pragma unroll 1
   for (int c = 0; c < D; c += 8) {
     float x[8];
-    tmem_ld<8>(o_col + c, x);
-    tmem_wait_ld();
-    pin<8>(x);
-    for (int i = 0; i < 8; ++i) x[i] = need ? o[c + i] : x[i];
+    for (int i = 0; i < 8; ++i) x[i] = sum[c + i];
     tmem_st8(o_col + c, x);
   }
   tmem_wait_st();
+  tc_fence_before();
+  __syncwarp();
+  return true;
 }
 
 }  // namespace
@@ -964,135 +1001,164 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
           mul2(x[i + 2], x[i + 3], k.z, k.w);
         }
       };
-      bool hidden = false;  // some token that other rows see, and this one does not, was in its tiles
       const int step = kPair ? 1 : 2;
+      auto unit_of = [&](int j) { return smem_addr(units) + (2 * (tile + j) + 1) % S::kSlots * S::kUnit; };  // tile j's values
       float nm = 0.f, l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;  // running maximum, negated; sum, in four parts
       bool fresh = true;                   // no score above minus infinity so far
       if (rows > 0) {
-        for (int j = kPair ? 0 : st; j < sg.ntiles; j += step) {
-          const int a = (tile + j) % kRing;
-          if (!kPair && !any_q) {  // nothing to do: what stands in this warp's part of P does not matter
+        for (int j = kPair ? 0 : st;; j += step) {
+          bool odd = false;  // a value that is not finite, of a token that some row of this warp does not see; uniform
+          for (; j < sg.ntiles; j += step) {
+            const int a = (tile + j) % kRing;
+            if (!kPair && !any_q) {  // nothing to do: what stands in this warp's part of P does not matter
+              if (!wait(kSFull + st, done & 1)) break;
+              arrive_one(bar(kPFull + st), lane);
+              arrive_one(bar(kAEmpty + a), lane);
+              ++done;
+              continue;
+            }
+            if (!wait((kE4m3 ? kScFull : kAFull) + a, ((tile + j) / kRing) & 1)) break;  // the tile's mask and scales
             if (!wait(kSFull + st, done & 1)) break;
-            arrive_one(bar(kPFull + st), lane);
-            arrive_one(bar(kAEmpty + a), lane);
-            ++done;
-            continue;
-          }
-          if (!wait((kE4m3 ? kScFull : kAFull) + a, ((tile + j) / kRing) & 1)) break;  // the tile's mask and scales
-          if (!wait(kSFull + st, done & 1)) break;
-          tc_fence_after();
-          const int32_t e0 = (sg.tile0 + j) * kAttnTile;
-          const uint4 there = *reinterpret_cast<const uint4*>(ring_mask + a * 4);
-          const bool whole = (there.x & there.y & there.z & there.w) == 0xffffffffu &&
-                             ((e0 >= all_b && e0 + kAttnTile <= all_c) || e0 + kAttnTile <= all_a);
-          // A tile that some row does not see all of: minus infinity takes the place of a score in TMEM. In a loop, and
-          // apart from the common path, as code that is read past costs time too.
-          if (__builtin_expect(!whole, 0)) {
+            tc_fence_after();
+            const int32_t e0 = (sg.tile0 + j) * kAttnTile;
+            const uint4 there = *reinterpret_cast<const uint4*>(ring_mask + a * 4);
+            const bool whole = (there.x & there.y & there.z & there.w) == 0xffffffffu &&
+                               ((e0 >= all_b && e0 + kAttnTile <= all_c) || e0 + kAttnTile <= all_a);
+            // A tile that some row does not see all of: minus infinity takes the place of a score in TMEM. In a loop, and
+            // apart from the common path, as code that is read past costs time too.
+            if (__builtin_expect(!whole, 0)) {
+              uint32_t hid = 0;  // in lane c, of the 32 tokens from 32 c on those that are there and that some row does not see
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              const uint32_t here = c == 0 ? there.x : c == 1 ? there.y : c == 2 ? there.z : there.w;
-              const uint32_t v = mine_q ? here & seen_by(p, sg, e0 + 32 * c, first_row + my_r) : 0u;
-              hidden |= mine_q && v != here;
-              float x[32];
-              __syncwarp();
-              tmem_ld<32>(s_col + 32 * c, x);
-              tmem_wait_ld();
-              pin<32>(x);
-              if (kE4m3) scaled(x, ring_ks + a * 128 + 32 * c);
+              for (int c = 0; c < 4; ++c) {
+                const uint32_t here = c == 0 ? there.x : c == 1 ? there.y : c == 2 ? there.z : there.w;
+                const uint32_t v = mine_q ? here & seen_by(p, sg, e0 + 32 * c, first_row + my_r) : 0u;
+                const uint32_t unseen = __reduce_or_sync(0xffffffffu, mine_q ? here & ~v : 0u);
+                if (lane == c) hid = unseen;
+                float x[32];
+                __syncwarp();
+                tmem_ld<32>(s_col + 32 * c, x);
+                tmem_wait_ld();
+                pin<32>(x);
+                if (kE4m3) scaled(x, ring_ks + a * 128 + 32 * c);
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!((v >> i) & 1)) x[i] = -INFINITY;
-              tmem_st32(s_col + 32 * c, x);
+                for (int i = 0; i < 32; ++i)
+                  if (!((v >> i) & 1)) x[i] = -INFINITY;
+                tmem_st32(s_col + 32 * c, x);
+              }
+              tmem_wait_st();
+              if (__any_sync(0xffffffffu, hid != 0)) {
+                const uint32_t n = kPair ? tile + j : done;
+                if (!wait(full_bar(st, 1, n), full_parity(n))) break;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                  const uint32_t unseen = __shfl_sync(0xffffffffu, hid, c);
+                  if (unseen) {
+                    bool mine = not_finite<D>(unit_of(j), unseen, 32 * c, lane);
+                    if (kE4m3) mine |= ((unseen >> lane) & 1) && !(fabsf(ring_vs[a * 128 + 32 * c + lane]) < INFINITY);
+                    odd |= __any_sync(0xffffffffu, mine);
+                  }
+                }
+              }
+            }
+            constexpr int kStep = S::kStep;  // tokens at a time
+            auto load = [&](int c, float* x) {
+#pragma unroll
+              for (int i = 0; i < kStep; i += 32) tmem_ld<32>(s_col + c + i, x + i);
+              float4 by[kE4m3 ? kStep / 4 : 1];  // the scales come while the scores do
+              if (kE4m3) {
+#pragma unroll
+                for (int i = 0; i < kStep / 4; ++i) by[kE4m3 ? i : 0] = *reinterpret_cast<const float4*>(ring_ks + a * 128 + c + 4 * i);
+              }
+              tmem_wait_ld();
+              pin<kStep>(x);
+              if (kE4m3 && whole) {
+#pragma unroll
+                for (int i = 0; i < kStep / 4; ++i) {
+                  const float4 k = by[kE4m3 ? i : 0];
+                  mul2(x[4 * i], x[4 * i + 1], k.x, k.y);
+                  mul2(x[4 * i + 2], x[4 * i + 3], k.z, k.w);
+                }
+              }
+            };
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+            for (int c = 0; c < 128; c += kStep) {
+              float x[kStep];
+              load(c, x);
+#pragma unroll
+              for (int i = 0; i < kStep; i += 8)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) top[k] = fmaxf(fmaxf(top[k], x[i + 2 * k]), x[i + 2 * k + 1]);
+            }
+            float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2;
+            const bool raise = fresh ? most > -INFINITY : most + nm > kTau;
+            const bool first = j < step;
+            if (__builtin_expect(__any_sync(0xffffffffu, raise), 0)) {
+              const float now = raise ? -most : nm, alpha = raise && !fresh ? ex2(now - nm) : 1.f;
+              nm = now;
+              if (!first && __any_sync(0xffffffffu, raise && !fresh)) {
+                l0 *= alpha;
+                l1 *= alpha;
+                l2 *= alpha;
+                l3 *= alpha;
+                if (!wait(kPvDone + st, (done - 1) & 1)) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < D; c += 8) {
+                  float o[8];
+                  tmem_ld<8>(o_col + c, o);
+                  tmem_wait_ld();
+                  pin<8>(o);
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) o[i] *= alpha;
+                  tmem_st8(o_col + c, o);
+                }
+              }
+              fresh = fresh && !raise;
+            }
+            // P in bf16, in the place of S: a column for two tokens, behind the reads of those
+#pragma unroll 1
+            for (int c = 0; c < 128; c += kStep) {
+              float x[kStep];
+              load(c, x);
+              uint32_t w[kStep / 2];
+#pragma unroll
+              for (int i = 0; i < kStep; i += 4) {
+#pragma unroll
+                for (int k = i; k < i + 4; k += 2) {
+                  fma2(x[k], x[k + 1], p.scale_log2, p.scale_log2, nm, nm);
+                  x[k] = ex2(x[k]);
+                  x[k + 1] = ex2(x[k + 1]);
+                }
+                add2(l0, l1, x[i], x[i + 1]);
+                add2(l2, l3, x[i + 2], x[i + 3]);
+              }
+              if (kE4m3) scaled(x, ring_vs + a * 128 + c);
+#pragma unroll
+              for (int i = 0; i < kStep / 2; ++i) w[i] = bf16x2(x[2 * i], x[2 * i + 1]);
+#pragma unroll
+              for (int i = 0; i < kStep / 2; i += 16) tmem_st16(s_col + c / 2 + i, w + i);
             }
             tmem_wait_st();
+            if (__builtin_expect(odd, 0)) break;
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(bar(kPFull + st));
+              mbar_arrive(bar(kAEmpty + a));
+            }
+            __syncwarp();
+            ++done;
           }
-          constexpr int kStep = S::kStep;  // tokens at a time
-          auto load = [&](int c, float* x) {
-#pragma unroll
-            for (int i = 0; i < kStep; i += 32) tmem_ld<32>(s_col + c + i, x + i);
-            float4 by[kE4m3 ? kStep / 4 : 1];  // the scales come while the scores do
-            if (kE4m3) {
-#pragma unroll
-              for (int i = 0; i < kStep / 4; ++i) by[kE4m3 ? i : 0] = *reinterpret_cast<const float4*>(ring_ks + a * 128 + c + 4 * i);
-            }
-            tmem_wait_ld();
-            pin<kStep>(x);
-            if (kE4m3 && whole) {
-#pragma unroll
-              for (int i = 0; i < kStep / 4; ++i) {
-                const float4 k = by[kE4m3 ? i : 0];
-                mul2(x[4 * i], x[4 * i + 1], k.x, k.y);
-                mul2(x[4 * i + 2], x[4 * i + 3], k.z, k.w);
-              }
-            }
-          };
-          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          if (!ok || j >= sg.ntiles) break;
+          // The tile's weights are written. Out of the loop over tiles: a call in it costs 16 % of a prefill's time.
+          const int a = (tile + j) % kRing, e0 = (sg.tile0 + j) * kAttnTile;
+          uint32_t seen[4];
 #pragma unroll 1
-          for (int c = 0; c < 128; c += kStep) {
-            float x[kStep];
-            load(c, x);
-#pragma unroll
-            for (int i = 0; i < kStep; i += 8)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) top[k] = fmaxf(fmaxf(top[k], x[i + 2 * k]), x[i + 2 * k + 1]);
-          }
-          float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2;
-          const bool raise = fresh ? most > -INFINITY : most + nm > kTau;
-          const bool first = j < step;
-          if (__builtin_expect(__any_sync(0xffffffffu, raise), 0)) {
-            const float now = raise ? -most : nm, alpha = raise && !fresh ? ex2(now - nm) : 1.f;
-            nm = now;
-            if (!first && __any_sync(0xffffffffu, raise && !fresh)) {
-              l0 *= alpha;
-              l1 *= alpha;
-              l2 *= alpha;
-              l3 *= alpha;
-              if (!wait(kPvDone + st, (done - 1) & 1)) break;
-              tc_fence_after();
-#pragma unroll 1
-              for (int c = 0; c < D; c += 8) {
-                float o[8];
-                tmem_ld<8>(o_col + c, o);
-                tmem_wait_ld();
-                pin<8>(o);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] *= alpha;
-                tmem_st8(o_col + c, o);
-              }
-            }
-            fresh = fresh && !raise;
-          }
-          // P in bf16, in the place of S: a column for two tokens, behind the reads of those
-#pragma unroll 1
-          for (int c = 0; c < 128; c += kStep) {
-            float x[kStep];
-            load(c, x);
-            uint32_t w[kStep / 2];
-#pragma unroll
-            for (int i = 0; i < kStep; i += 4) {
-#pragma unroll
-              for (int k = i; k < i + 4; k += 2) {
-                fma2(x[k], x[k + 1], p.scale_log2, p.scale_log2, nm, nm);
-                x[k] = ex2(x[k]);
-                x[k + 1] = ex2(x[k + 1]);
-              }
-              add2(l0, l1, x[i], x[i + 1]);
-              add2(l2, l3, x[i + 2], x[i + 3]);
-            }
-            if (kE4m3) scaled(x, ring_vs + a * 128 + c);
-#pragma unroll
-            for (int i = 0; i < kStep / 2; ++i) w[i] = bf16x2(x[2 * i], x[2 * i + 1]);
-#pragma unroll
-            for (int i = 0; i < kStep / 2; i += 16) tmem_st16(s_col + c / 2 + i, w + i);
-          }
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(bar(kPFull + st));
-            mbar_arrive(bar(kAEmpty + a));
-          }
-          __syncwarp();
+          for (int c = 0; c < 4; ++c) seen[c] = mine_q ? ring_mask[a * 4 + c] & seen_by(p, sg, e0 + 32 * c, first_row + my_r) : 0u;
+          ok = tile_by_hand<D>(s_col, o_col, unit_of(j), seen, j < step, bar(kPFull + st), bar(kAEmpty + a), bar(kPvDone + st), done & 1,
+                               abort, limit);
+          if (!ok) break;
           ++done;
         }
       } else if (kPair) {
@@ -1112,25 +1178,6 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
       const int mine_n = kPair ? sg.ntiles : (sg.ntiles + 1 - st) / 2, other_n = kPair ? 0 : sg.ntiles - mine_n;
       if (rows > 0 && mine_n > 0) {
         if (!wait(kPvDone + st, (done - 1) & 1)) break;
-        // A weight of zero does not keep out an infinite value: where this row did not see all of its tiles' tokens, and its
-        // weights are finite, its result is finite or suspect.
-        if (__builtin_expect(__any_sync(0xffffffffu, hidden), 0)) {
-          tc_fence_after();
-          uint32_t odd = 0;
-#pragma unroll 1
-          for (int c = 0; c < D; c += 16) {
-            float o[16];
-            tmem_ld<16>(o_col + c, o);
-            tmem_wait_ld();
-            pin<16>(o);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) odd |= (__float_as_uint(o[i]) & 0x7f800000u) == 0x7f800000u;
-          }
-          const bool need = odd && hidden && fabsf(l) < INFINITY;
-          if (__any_sync(0xffffffffu, need))
-            redo_row<D, kE4m3>(p, sg, first_row + my_r, my_h, kPair ? 0 : st, step, nm, need, o_col);
-          tc_fence_before();
-        }
       }
       if (!kPair) {
         other += other_n;
