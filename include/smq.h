@@ -653,7 +653,8 @@ SMQ_API int sparse_mqa_attention_tree(const smq_attn_plan *plan, const smq_seq_a
  * Rows are listed: distinct rows of the table. One out of range, or listed
  * again, raises SMQ_ERR_BOUNDS and is skipped. Any negative entry is no page. An
  * entry past the pool, and a count that would pass below zero, raise
- * SMQ_ERR_BOUNDS and change no count.
+ * SMQ_ERR_BOUNDS and change no count; a call's additions come before its
+ * subtractions, and a page whose count was zero before it cannot be given back.
  * --------------------------------------------------------------------------- */
 typedef struct smq_page_plan smq_page_plan;
 

@@ -1,11 +1,15 @@
 // Pages of the paged caches (sm_103a): rows of the block table that take, share
 // and give back pages, and the tokens that move between pages.
 //
-// State and result are counts and ids, so a call must not depend on timing. A
-// call is two launches: pages_plan_kernel only reads (which pages are free, what
-// each listed row takes), pages_apply_kernel writes. Ranks come from prefix
-// sums in the order of rows and columns; counts change by atomic additions,
-// whose order does not matter. A row is a block's work in both: with a warp a row
+// State and result are counts and ids, so a call must not depend on timing, also
+// where a table and its counts do not agree. A call is two launches.
+// pages_plan_kernel finds which pages are free, as a list and as bits, and what
+// each listed row takes, and counts the pages that forks share: a count above zero
+// grows, so what is free does not change. pages_apply_kernel writes the rest. Ranks
+// come from prefix sums in the order of rows and columns. Counts change by atomic
+// operations whose order does not matter: pages that are taken were free, and a
+// free page is not given back (its bit says so); of the others all additions
+// come before all subtractions, which stop at zero. A row is a block's work in both: with a warp a row
 // 512 rows of 2048 columns over 524288 pages took 74 us, so 21. Small calls are two
 // launches, some 9 us.
 #include "smq_pages.cuh"
@@ -131,6 +135,10 @@ __device__ __forceinline__ void list_free_pages(const PagesParams& p, int k) {
   for (int64_t i0 = begin; i0 < end; i0 += 128) {
     const int64_t i = i0 + lane * 4;
     uint32_t m = i < end ? free_bits(p, wide, i, end) : 0;
+    uint32_t word = m << (lane % 8 * 4);  // of eight lanes
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) word |= __shfl_xor_sync(0xffffffffu, word, o);
+    if (lane % 8 == 0) p.free_bits[i / 32] = word;
     int incl = __popc(m);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -180,9 +188,9 @@ struct FreeList {
 
 }  // namespace
 
-// Reads only: blocks [0, segments) list the free pages, the others say for a
-// listed row each how many pages it takes. A fork's sources are also copied, as
-// its destinations may be sources of others.
+// Blocks [0, segments) list the free pages, the others say for a listed row each
+// how many pages it takes. A fork's sources are also copied, as its destinations
+// may be sources of others, and the whole pages that it shares are counted.
 template <bool kFork>
 __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(const __grid_constant__ PagesParams p) {
   griddep_launch_dependents();
@@ -221,6 +229,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(const __grid_c
       }
       to[c] = page < 0 ? -1 : page;
       take |= c == n.full && page >= 0;
+      if (c < n.full && page >= 0) atomicAdd(p.refs + page, 1);
     }
     takes = __syncthreads_or(take) ? 1 : 0;
   } else {
@@ -239,7 +248,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(const __grid_c
 namespace {
 
 __device__ __forceinline__ void give_back(const PagesParams& p, int32_t page) {
-  bool bad = page >= p.num_pages;
+  bool bad = page >= p.num_pages || ((p.free_bits[page / 32] >> (page % 32)) & 1);  // nobody's page, that another row may take
   if (!bad && atomicSub(p.refs + page, 1) <= 0) {
     atomicAdd(p.refs + page, 1);
     bad = true;
@@ -348,7 +357,7 @@ __global__ void __launch_bounds__(kApplyThreads)
       int32_t page = c < n.full ? from[c] : -1;
       if (c == n.full && takes > 0) page = fresh;
       entries[c] = page;
-      if (page >= 0) atomicAdd(p.refs + page, 1);
+      if (c == n.full && page >= 0) atomicAdd(p.refs + page, 1);  // (the others' counts: pages_plan_kernel)
       if (old >= 0) give_back(p, old);
     }
     if (threadIdx.x == 0 && takes > 0 && fresh < 0) atomicOr(p.status, kStatusNoPages);

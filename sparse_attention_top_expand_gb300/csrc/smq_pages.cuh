@@ -43,6 +43,7 @@ struct PagesParams {
   int32_t segment;           // a multiple of kSegmentUnit
   int32_t* free_counts;      // [segments]
   int32_t* free_list;        // [segments * segment]
+  uint32_t* free_bits;       // [segments * segment / 32] a bit a page
   int32_t* snapshot;         // fork: [num_rows][columns] the sources' entries
   int32_t* status;
 };

@@ -23,9 +23,10 @@ constexpr int kMaxVectors = 1024;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-// Workspace: [status word, 256 B][free pages of each segment][takes or counts][free list][sources' entries of a fork].
+// Workspace: [status word, 256 B][free pages of each segment][takes or counts][free list][its
+// pages as bits][sources' entries of a fork].
 struct Scratch {
-  size_t free_counts, takes, free_list, snapshot, end;
+  size_t free_counts, takes, free_list, free_bits, snapshot, end;
   int64_t segment, segments;
 };
 
@@ -41,7 +42,8 @@ Scratch scratch_of(const smq_page_plan* p) {
   s.free_counts = kStatusBytes;
   s.takes = s.free_counts + up(smq::kMaxSegments * sizeof(int32_t));
   s.free_list = s.takes + up(p->desc.table_rows * sizeof(int32_t));
-  s.snapshot = s.free_list + up(s.segments * s.segment * sizeof(int32_t));
+  s.free_bits = s.free_list + up(s.segments * s.segment * sizeof(int32_t));
+  s.snapshot = s.free_bits + up(s.segments * s.segment / 8);
   s.end = s.snapshot + entries * sizeof(int32_t);
   return s;
 }
@@ -92,6 +94,7 @@ smq::PagesParams params_of(const smq_page_plan* plan, int32_t num_rows, int32_t*
   p.free_counts = reinterpret_cast<int32_t*>(ws + w.free_counts);
   p.takes = reinterpret_cast<int32_t*>(ws + w.takes);
   p.free_list = reinterpret_cast<int32_t*>(ws + w.free_list);
+  p.free_bits = reinterpret_cast<uint32_t*>(ws + w.free_bits);
   p.snapshot = reinterpret_cast<int32_t*>(ws + w.snapshot);
   return p;
 }
