@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kApplyThreads)
     const FreeList list(p, before_s, scratch);
     const Want want = want_of(p, i, &past);
     int32_t* const entries = p.table + static_cast<int64_t>(p.rows ? p.rows[i] : i) * p.columns;
-    bool none = false;
+    bool none = false, bad = false;
     constexpr int kPer = 4;  // columns of a thread, next to each other so that ranks follow them
     for (int32_t c0 = 0; c0 < p.columns; c0 += kApplyThreads * kPer) {
       int32_t old[kPer];
@@ -328,6 +328,7 @@ __global__ void __launch_bounds__(kApplyThreads)
         const int32_t c = c0 + threadIdx.x * kPer + k;
         if (c >= p.columns) break;
         if (want(c)) {
+          bad |= old[k] >= p.num_pages;
           if (old[k] >= 0) continue;
           const int32_t page = list.page(p, r++);
           none |= page < 0;
@@ -341,6 +342,7 @@ __global__ void __launch_bounds__(kApplyThreads)
       }
     }
     if (none) atomicOr(p.status, kStatusNoPages);
+    if (bad) atomicOr(p.status, kStatusBounds);
     return;
   }
   const Length n = length_of(p, i, &past);

@@ -96,3 +96,17 @@ def test_counts_below_zero_stay():
     status, got, after = b.many(lambda plan, r, t, ws: smq.sparse_mqa_pages_fork(
         plan, r, t, _i32([0]), _i32([1]), _i32([2 * PAGE]), [], ws))
     assert status == pages_ref.BOUNDS and got.tolist() == [-2, 2, 0, 0] and after.tolist() == [[0, 1], [-1, 1]]
+
+
+@pytest.mark.parametrize("entry", [50, 2 ** 31 - 1])
+def test_an_entry_past_the_pool_that_a_row_keeps(entry):
+    """It is reported, as one that is given back is, and stays; the row's other columns have their pages."""
+    refs = np.zeros(50)
+    refs[[3, 4]] = 1
+    b = Pool(refs, [[-1, entry, 3, -1], [4, -1, -1, entry]])
+    status, got, after = b.many(lambda plan, r, t, ws: smq.sparse_mqa_pages_resize(plan, r, t, _i32([3 * PAGE, PAGE]), ws), 3)
+    assert status == pages_ref.BOUNDS and after.tolist() == [[0, entry, 3, -1], [4, -1, -1, -1]]
+    assert got.tolist() == [1, 0, 0, 1, 1] + [0] * 45
+    status, got, after = b.many(lambda plan, r, t, ws: smq.sparse_mqa_pages_resize(
+        plan, r, t, _i32([3 * PAGE]), ws, row_begin=_i32([PAGE])), 3)
+    assert status == pages_ref.BOUNDS and after[0].tolist() == [-1, entry, 3, -1] and got.sum() == 2
