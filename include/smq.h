@@ -678,7 +678,10 @@ SMQ_API int smq_page_workspace_init(const smq_page_plan *plan, void *workspace, 
 
 /* Row rows[i] (i where NULL) is to cover the positions [begin, end): begin =
  * row_begin[i] (0 where NULL), end = row_end[i], both as many as the table's
- * row holds at most (more raises SMQ_ERR_BOUNDS), negative as 0. The first
+ * row holds at most (more raises SMQ_ERR_BOUNDS), negative as 0. Its columns are
+ * those from begin / page_size up to the one that end ends in, so that an empty
+ * range that begins inside a page, as of a window that has left all tokens
+ * behind, holds that page, the next token's: begin >= end in the same page. The first
  * keep_first positions stay too, as far as they are below end: the sinks of a
  * sliding layer. Wanted columns without a page take one; the others give
  * theirs back and become -1. row_end = 0 frees a row. */

@@ -1003,7 +1003,8 @@ def _resize_args(plan: PagePlan, page_refs, block_table, row_end, workspace, row
 def sparse_mqa_pages_resize(plan: PagePlan, page_refs, block_table, row_end, workspace, row_begin=None, keep_first: int = 0,
                             rows=None, stream=None) -> None:
     """Give row rows[i] (row i where None) of block_table the pages for positions row_begin[i] (0 where None) to row_end[i]
-    (int32), and for its first keep_first positions; pages of other positions are given back."""
+    (int32), and for its first keep_first positions; pages of other positions are given back. An empty range that begins
+    inside a page holds that page."""
     a = _resize_args(plan, page_refs, block_table, row_end, workspace, row_begin, keep_first, rows)
     _check(load_library().sparse_mqa_pages_resize(plan.handle, ctypes.byref(a), _stream(stream)), "sparse_mqa_pages_resize")
 

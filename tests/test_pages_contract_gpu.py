@@ -110,3 +110,13 @@ def test_an_entry_past_the_pool_that_a_row_keeps(entry):
     status, got, after = b.many(lambda plan, r, t, ws: smq.sparse_mqa_pages_resize(
         plan, r, t, _i32([3 * PAGE]), ws, row_begin=_i32([PAGE])), 3)
     assert status == pages_ref.BOUNDS and after[0].tolist() == [-1, entry, 3, -1] and got.sum() == 2
+
+
+def test_empty_ranges():
+    """One that begins inside a page holds that page, one that begins at a page's start, or behind the end's page, holds none."""
+    ranges = [(20, 20), (16, 16), (30, 17), (32, 20), (0, 0), (40, 33), (47, 48), (48, 48)]
+    b = Pool(np.zeros(40), np.full((len(ranges), 5), -1))
+    begin, end = zip(*ranges)
+    status, got, after = b.many(lambda plan, r, t, ws: smq.sparse_mqa_pages_resize(plan, r, t, _i32(end), ws, row_begin=_i32(begin)), 3)
+    held = [np.flatnonzero(row >= 0).tolist() for row in after]
+    assert status == 0 and held == [[1], [], [1], [], [], [2], [2], []] and got.sum() == 4
