@@ -77,3 +77,25 @@ def test_calls_of_single_rows_keep_their_bound():
     assert e.value.code == smq.SMQ_ERR_INVALID_ARG and (out == 5).all()
     smq.sparse_mqa_attention_decode(plan, q[1:], data[:, 0], data[:, 1], table, at[1:], at[1:] + 1, out[1:], ws)
     assert smq.smq_get_status(ws) == 0 and (out[1:] == 0).all() and (out[0] == 5).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("heads,kv_heads", [(8, 2), (128, 1)])
+def test_drafted_tokens_past_the_table(dtype, heads, kv_heads):
+    """A drafted token without a place in the table is an error only where a row's mask has it, or has its position."""
+    page, columns, n = 16, 5, 40
+    top = page * columns
+    for length, bits, status in (
+            (top + 3, lambda i: {j for j in range(37) if j <= i}, 0),                # nodes 37 to 39 are seen by nobody
+            (top + 3, lambda i: {0, 5} | {40, 50, 63}, 0),                           # bits past the rows are not read
+            (top + 3, lambda i: {36, 37} if i == 33 else {36}, smq.SMQ_ERR_BOUNDS),  # one row sees one
+            (top + 39, lambda i: {0}, 0), (top + 39, lambda i: {1}, smq.SMQ_ERR_BOUNDS),
+            (top + 40, lambda i: set(), 0),                                          # the context ends with the table
+            (top + 41, lambda i: set(), smq.SMQ_ERR_BOUNDS)):                        # every row sees a token past it
+        masks = [bits(i) for i in range(n)]
+        b = ref.Batch(_rng(length), heads, kv_heads, 64, page, dtype, [(3, 20), (n, top)])
+        b.seqs = [(3, 20), (n, length)]
+        packed = ref.pack([{0}] * 3 + masks + [set()] * 2, 2)
+        assert b.call(tree_mask=packed) == status, length
+        sets = [ref.tree_sets(3, 20, [{0}] * 3), [s[s < top] for s in ref.tree_sets(n, length, masks)]]
+        b.check(sets)
