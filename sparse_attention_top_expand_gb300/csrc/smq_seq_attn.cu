@@ -178,7 +178,8 @@ struct Tokens {
   int32_t s0, lo, hi;
   bool past;  // the rows' last token (of a tree: the sequence's) is past the block table
   __device__ int32_t count() const { return s0 + hi - lo; }
-  __device__ int32_t tiles() const { return max(1, (count() + kAttnTile - 1) / kAttnTile); }  // without tokens there still is a result
+  // (without tokens there still is a result; up to 2^31 - 1 tokens, so nothing is added to a count or a token's number)
+  __device__ int32_t tiles() const { return (count() - 1) / kAttnTile + 1; }
 };
 __device__ __forceinline__ Tokens tokens_of(const SeqAttnParams& p, int32_t n, int32_t len, int32_t i0, int32_t rows) {
   const int64_t room = static_cast<int64_t>(p.bt_stride) * p.page_size;
@@ -1043,7 +1044,7 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
             const int32_t e0 = (sg.tile0 + j) * kAttnTile;
             const uint4 there = *reinterpret_cast<const uint4*>(ring_mask + a * 4);
             const bool whole = (there.x & there.y & there.z & there.w) == 0xffffffffu &&
-                               ((e0 >= all_b && e0 + kAttnTile <= all_c) || e0 + kAttnTile <= all_a);
+                               ((e0 >= all_b && e0 <= all_c - kAttnTile) || e0 <= all_a - kAttnTile);
             // A tile that some row does not see all of: minus infinity takes the place of a score in TMEM. In a loop, and
             // apart from the common path, as code that is read past costs time too.
             if (__builtin_expect(!whole, 0)) {

@@ -99,3 +99,52 @@ def test_drafted_tokens_past_the_table(dtype, heads, kv_heads):
         assert b.call(tree_mask=packed) == status, length
         sets = [ref.tree_sets(3, 20, [{0}] * 3), [s[s < top] for s in ref.tree_sets(n, length, masks)]]
         b.check(sets)
+
+
+@pytest.mark.parametrize("length", [2 ** 31 - 129, 2 ** 31 - 128, 2 ** 31 - 127, 2 ** 31 - 5, 2 ** 31 - 1])
+@pytest.mark.parametrize("max_seq_rows", [1, 200])
+def test_the_longest_contexts(length, max_seq_rows):
+    """Every token has the same score. The first page's values are -1, all others' are one page's, 1, so a result that counts every
+    token is 1 - 2 * 65536 / length, 1 in bf16; sums of ones are exact in fp32 up to 2^24, and a CTA's are 2^24 at most."""
+    page, columns = 65536, 32768
+    plan = smq.AttentionPlan(1, 1, 64, page, max_rows=200)
+    data = torch.zeros(2, 2, 1, page, 64, device=DEV, dtype=torch.bfloat16)
+    data[0, 1], data[1, 1] = -1, 1
+    table = torch.ones(1, columns, dtype=torch.int32, device=DEV)
+    table[0, 0] = 0
+    q = torch.ones(1, 1, 64, device=DEV, dtype=torch.bfloat16)
+    cu, lens = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([0, 1], [length]))
+    ws = plan.sequence_workspace()
+    for what in (dict(window=2 ** 31 - 1), dict(tree_mask=torch.ones(1, 1, dtype=torch.int32, device=DEV))):
+        if max_seq_rows > 32 and "tree_mask" in what:
+            what["tree_mask"] = torch.ones(1, 7, dtype=torch.int32, device=DEV)
+        out, lse = torch.zeros_like(q), torch.zeros(1, 1, device=DEV)
+        smq.SequenceAttentionCall(plan, q, data[:, 0], data[:, 1], table, cu, lens, max_seq_rows, out, ws, lse=lse, **what)()
+        assert smq.smq_get_status(ws) == 0
+        assert (out == 1).all() and abs(float(lse) - np.log(float(length))) < 1e-5
+
+
+def test_a_window_at_the_end_of_the_longest_context():
+    """The newest rows of a context of 2^31 - 1 tokens, whose pages before the window are gone."""
+    page, columns = 65536, 32768
+    plan = smq.AttentionPlan(2, 1, 64, page, max_rows=200)
+    g = torch.Generator(device=DEV).manual_seed(2)
+    data = torch.randn(3, 2, 1, page, 64, generator=g, device=DEV).to(torch.bfloat16)
+    table = torch.full((1, columns), -1, dtype=torch.int32, device=DEV)
+    table[0, 0], table[0, -1], table[0, -2] = 2, 0, 1
+    rows, length, window, sinks = 150, 2 ** 31 - 1, 70000, 3
+    q = torch.randn(rows, 2, 64, generator=g, device=DEV).to(torch.bfloat16)
+    out, lse, ws = torch.zeros_like(q), torch.zeros(rows, 2, device=DEV), plan.sequence_workspace()
+    cu, lens = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([0, rows], [length]))
+    smq.sparse_mqa_attention_window(plan, q, data[:, 0], data[:, 1], table, cu, lens, rows, out, ws, window, sinks, lse=lse)
+    assert smq.smq_get_status(ws) == 0
+    both = torch.cat([data[2, :, 0, :sinks], data[1, :, 0], data[0, :, 0]], 1).double().cpu().numpy()  # sinks, the last two pages
+    for r in (0, 1, 77, 149):
+        at = length - rows + r  # position; the last two pages begin at (columns - 2) * page
+        hi = at + 1 - (columns - 2) * page
+        seen = np.r_[0:sinks, sinks + hi - window:sinks + hi]
+        k, v = both[0][seen][:, None], both[1][seen][:, None]
+        want, mean, want_lse, size = ref.attend(q[r].double().cpu().numpy(), k, v, 0.125)
+        off, lse_off = ref.bound(want, mean, size, 64, len(seen))
+        assert (np.abs(out[r].double().cpu().numpy() - want) <= off).all(), r
+        assert (np.abs(lse[r].double().cpu().numpy() - want_lse) <= lse_off + 2.0 ** -22 * np.abs(want_lse)).all(), r
