@@ -73,7 +73,8 @@ namespace {
 constexpr int kLoaders = 128;  // threads that copy K, V and Q; over an E4M3 cache these keys and queries, as many again values
 constexpr int kSegRing = 8;    // segments published ahead
 constexpr int kRing = 4;       // tiles whose addresses, masks and scales may be ahead of the softmax
-constexpr float kUnset = -3.0e38f;         // the running maximum of a partial without tokens
+constexpr float kUnset = -3.402823466e38f;  // the running maximum of a partial without tokens: no score is below it
+constexpr float kFar = 134217728.f;        // 2^27: a maximum whose rounding a fused scale and maximum would show as a factor of 2^4
 constexpr int kSmemLimit = 232448 - 1024;  // less the static part
 constexpr float kTau = 8.f;                // log2 of the largest P
 
@@ -334,6 +335,36 @@ __device__ __noinline__ bool tile_by_hand(uint32_t p_col, uint32_t o_col, uint32
   tc_fence_before();
   __syncwarp();
   return true;
+}
+
+// A tile's weights where a maximum is past kFar: score times scale is rounded before the maximum is taken off, as the maximum
+// was, since a fused one would show the maximum's rounding as a factor. By each query's own maximum, so that equal scores weigh
+// alike in all tiles. The sum of this thread's weights.
+template <bool kE4m3>
+__device__ __noinline__ float far_weights(uint32_t s_col, const float* k_scales, const float* v_scales, bool scaled, float scale,
+                                          float nm) {
+  const bool apart = fabsf(nm) > kFar;
+  float sum = 0.f;
+#pragma unroll 1
+  for (int c = 0; c < 128; c += 16) {
+    float x[16];
+    tmem_ld<16>(s_col + c, x);
+    tmem_wait_ld();
+    pin<16>(x);
+    float w[8];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (kE4m3 && !scaled) x[i] *= k_scales[c + i];
+      x[i] = ex2(apart ? __fadd_rn(__fmul_rn(x[i], scale), nm) : fmaf(x[i], scale, nm));
+      sum += x[i];
+      if (kE4m3) x[i] *= v_scales[c + i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = __uint_as_float(bf16x2(x[2 * i], x[2 * i + 1]));
+    tmem_st8(s_col + c / 2, w);
+  }
+  tmem_wait_st();
+  return sum;
 }
 
 }  // namespace
@@ -1026,9 +1057,11 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
       auto unit_of = [&](int j) { return smem_addr(units) + (2 * (tile + j) + 1) % S::kSlots * S::kUnit; };  // tile j's values
       float nm = 0.f, l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;  // running maximum, negated; sum, in four parts
       bool fresh = true;                   // no score above minus infinity so far
+      bool far = false;                    // a maximum of this warp's is past kFar; uniform
       if (rows > 0) {
         for (int j = kPair ? 0 : st;; j += step) {
           bool odd = false;  // a value that is not finite, of a token that some row of this warp does not see; uniform
+          bool masked = false;  // the tile's scores have been masked, and have their keys' scales
           for (; j < sg.ntiles; j += step) {
             const int a = (tile + j) % kRing;
             if (!kPair && !any_q) {  // nothing to do: what stands in this warp's part of P does not matter
@@ -1136,6 +1169,11 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
                 }
               }
               fresh = fresh && !raise;
+              far = __any_sync(0xffffffffu, fabsf(nm) > kFar);
+            }
+            if (__builtin_expect(far, 0)) {
+              masked = !whole;
+              break;
             }
             // P in bf16, in the place of S: a column for two tokens, behind the reads of those
 #pragma unroll 1
@@ -1172,14 +1210,22 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
             ++done;
           }
           if (!ok || j >= sg.ntiles) break;
-          // The tile's weights are written. Out of the loop over tiles: a call in it costs 16 % of a prefill's time.
+          // Rare tiles. Out of the loop over tiles: a call in it, or as much code, costs 16 % of a prefill's time.
           const int a = (tile + j) % kRing, e0 = (sg.tile0 + j) * kAttnTile;
           uint32_t seen[4];
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) seen[c] = mine_q ? ring_mask[a * 4 + c] & seen_by(p, sg, e0 + 32 * c, first_row + my_r) : 0u;
-          ok = tile_by_hand<D>(s_col, o_col, unit_of(j), seen, j < step, bar(kPFull + st), bar(kAEmpty + a), bar(kPvDone + st), done & 1,
-                               abort, limit);
-          if (!ok) break;
+          if (far) l0 += far_weights<kE4m3>(s_col, ring_ks + a * 128, ring_vs + a * 128, masked, p.scale_log2, nm);
+          if (odd) {
+            ok = tile_by_hand<D>(s_col, o_col, unit_of(j), seen, j < step, bar(kPFull + st), bar(kAEmpty + a), bar(kPvDone + st),
+                                 done & 1, abort, limit);
+            if (!ok) break;
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            arrive_one(bar(kPFull + st), lane);
+            arrive_one(bar(kAEmpty + a), lane);
+          }
           ++done;
         }
       } else if (kPair) {

@@ -7,6 +7,7 @@ import torch
 
 import sparse_attention_top_expand_gb300 as smq
 
+import attention_bounds as bounds
 import sequence_ref as ref
 
 pytestmark = pytest.mark.gpu
@@ -148,3 +149,34 @@ def test_a_window_at_the_end_of_the_longest_context():
         off, lse_off = ref.bound(want, mean, size, 64, len(seen))
         assert (np.abs(out[r].double().cpu().numpy() - want) <= off).all(), r
         assert (np.abs(lse[r].double().cpu().numpy() - want_lse) <= lse_off + 2.0 ** -22 * np.abs(want_lse)).all(), r
+
+
+@pytest.mark.parametrize("heads,kv_heads,dtype", [(64, 8, "bf16"), (3, 1, "bf16"), (16, 2, "e4m3"), (128, 1, "e4m3")])
+@pytest.mark.parametrize("scale", [1.0, -1.0])
+@pytest.mark.parametrize("top", [1e5, 3e8, 1e10, 1e20, 2.2e38])
+def test_scores_far_from_zero(heads, kv_heads, dtype, scale, top):
+    """Scores up to `top` in steps of an eighth of it, of either sign, many of them equal: the largest share all the weight. Their
+    roundings do not matter, as equal scores round alike and others are far off; lse has seven, of products, scales and sums,
+    2^-24 of it each."""
+    if dtype == "e4m3":  # a product is of a query and a code, 448 here, before the token's scale: 56 * top, which has to be finite
+        top = min(top, 5e36)
+    rng = _rng(heads, int(np.log10(top)))
+    seqs = [(1, 1), (2, 130), (40, 400), (1, 3000), (3, 5)]
+    b = ref.Batch(rng, heads, kv_heads, 128, 64, dtype, seqs, scale=scale)
+    b.q[:] = 0
+    strength = torch.from_numpy(rng.choice([-1.0, 1.0, 0.3], b.q.shape[:2]) * top / 8).to(torch.bfloat16)
+    b.q[:, :, 3] = strength
+    for i, (_, n) in enumerate(seqs):
+        keys = np.zeros((n, kv_heads, 128))
+        keys[:, :, 3] = rng.integers(1, 9, (n, kv_heads)) * rng.choice([-1, 1], (1, kv_heads))  # of one sign: all scores far off, or none
+        bounds.put(b.cache, i, np.arange(n), 0, keys)
+    sets = _sets(seqs, 1500, 4)
+    assert b.call(sets, window=1500, sinks=4) == 0
+    out, lse = b.out.double().cpu().numpy(), b.lse.double().cpu().numpy()
+    for i, per in enumerate(sets):
+        for r, at in zip(range(b.cu[i], b.cu[i + 1]), per):
+            k, v = b.cache.tokens(i, at)
+            want, mean, want_lse, _ = ref.attend(b.q[r].double().numpy(), k, v, scale)
+            off, lse_off = ref.bound(want, mean, np.zeros(heads), 128, len(at))
+            assert (np.abs(out[r] - want) <= off).all(), (i, r)
+            assert (np.abs(lse[r] - want_lse) <= lse_off + 2.0 ** -21 * np.abs(want_lse)).all(), (i, r)
