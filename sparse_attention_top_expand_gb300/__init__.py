@@ -561,7 +561,7 @@ class AttentionPlan:
         self.device = torch.device("cuda", self.device_index)
         d = SMQAttnPlanDesc(ctypes.sizeof(SMQAttnPlanDesc), num_heads, num_kv_heads, head_dim, page_size,
                             _CACHE_TYPES[cache_dtype], min(max_rows, self.MAX_SINGLE_ROWS), self.device_index,
-                            softmax_scale or 0.0, max_rows)
+                            softmax_scale or 0.0, _int32(max_rows, "max_rows"))
         h = _vp()
         _check(lib.smq_attn_plan_create(ctypes.byref(d), ctypes.byref(h)), "smq_attn_plan_create")
         self.handle = h
@@ -637,6 +637,14 @@ def _inner_ptr(t: Optional[torch.Tensor], dtypes, name: str, device, shape):
     if any(s != w and n != 1 for s, w, n in zip(t.stride()[1:], reversed(want), shape)):
         raise ValueError(f"{name} must be contiguous within a row")
     return t.data_ptr(), int(t.stride(0)) if t.shape[0] > 1 else size  # one row: its stride means nothing
+
+
+def _int32(x, name: str) -> int:
+    """A whole number for a 32-bit field, which ctypes would cut to 32 bits without a word."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} {x} does not fit 32 bits")
+    return x
 
 
 def _shaped(t, name, shape):
@@ -809,7 +817,7 @@ def _seq_attention_args(plan: AttentionPlan, q, k_cache, v_cache, block_table, c
     a.bt_rows = int(block_table.shape[0])
     a.bt_stride = int(block_table.shape[1])
     a.num_seqs = seqs = int(seq_len.shape[0])
-    a.max_seq_rows = int(max_seq_rows)
+    a.max_seq_rows = _int32(max_seq_rows, "max_seq_rows")
     a.seq_indices = _ptr(seq_indices, _I32, "seq_indices", dev)
     a.cu_rows = _ptr(cu_rows, _I32, "cu_rows", dev)
     a.seq_len = _ptr(seq_len, _I32, "seq_len", dev)
@@ -819,7 +827,7 @@ def _seq_attention_args(plan: AttentionPlan, q, k_cache, v_cache, block_table, c
     if seq_indices is None and a.bt_rows < seqs:
         raise ValueError("block_table needs a row for each sequence, or seq_indices")
     if tree_mask is None:
-        a.window, a.sinks = int(window), int(sinks)
+        a.window, a.sinks = _int32(window, "window"), _int32(sinks, "sinks")
     else:
         a.tree_mask = _ptr(tree_mask, _I32, "tree_mask", dev)
         _shaped(tree_mask, "tree_mask", (rows, tree_mask.shape[-1]))
@@ -898,7 +906,8 @@ class PagePlan:
             device = torch.cuda.current_device()
         self.device_index = int(device)
         self.device = torch.device("cuda", self.device_index)
-        d = SMQPagePlanDesc(ctypes.sizeof(SMQPagePlanDesc), page_size, num_pages, table_rows, table_columns, self.device_index)
+        d = SMQPagePlanDesc(ctypes.sizeof(SMQPagePlanDesc), _int32(page_size, "page_size"), num_pages,
+                            _int32(table_rows, "table_rows"), _int32(table_columns, "table_columns"), self.device_index)
         h = _vp()
         _check(lib.smq_page_plan_create(ctypes.byref(d), ctypes.byref(h)), "smq_page_plan_create")
         self.handle = h
@@ -996,7 +1005,7 @@ def _resize_args(plan: PagePlan, page_refs, block_table, row_end, workspace, row
     a.row_begin = _ptr(row_begin, _I32, "row_begin", plan.device)
     _shaped(row_end, "row_end", (a.num_rows,))
     _shaped(row_begin, "row_begin", (a.num_rows,))
-    a.keep_first = int(keep_first)
+    a.keep_first = _int32(keep_first, "keep_first")
     return a
 
 

@@ -180,3 +180,21 @@ def test_scores_far_from_zero(heads, kv_heads, dtype, scale, top):
             off, lse_off = ref.bound(want, mean, np.zeros(heads), 128, len(at))
             assert (np.abs(out[r] - want) <= off).all(), (i, r)
             assert (np.abs(lse[r] - want_lse) <= lse_off + 2.0 ** -21 * np.abs(want_lse)).all(), (i, r)
+
+
+@pytest.mark.parametrize("name", ["window", "sinks", "max_seq_rows", "keep_first"])
+def test_numbers_past_32_bits_are_refused(name):
+    """A window of 2^32 + 4 tokens is not one of 4."""
+    plan = smq.AttentionPlan(4, 2, 64, 16, max_rows=4)
+    data = torch.zeros(2, 2, 2, 16, 64, device=DEV, dtype=torch.bfloat16)
+    q = torch.zeros(1, 4, 64, device=DEV, dtype=torch.bfloat16)
+    table, cu, n = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([[0]], [0, 1], [5]))
+    what = dict(window=4, sinks=0, max_seq_rows=1)
+    with pytest.raises(ValueError, match="32 bits"):
+        if name == "keep_first":
+            pool = smq.PagePlan(16, 4, 1, 2)
+            refs, state = pool.state()
+            smq.ResizeCall(pool, refs, state, n, pool.workspace(), keep_first=2 ** 32)
+        else:
+            smq.SequenceAttentionCall(plan, q, data[:, 0], data[:, 1], table, cu, n, out=torch.empty_like(q),
+                                      workspace=plan.sequence_workspace(), **{**what, name: 2 ** 32 + 4})

@@ -43,3 +43,13 @@ def test_a_description_without_the_bound_is_taken(lib):
     old = smq.SMQAttnPlanDesc.max_sequence_rows.offset
     assert _create(lib, size=old, max_sequence_rows=-5) in PASSES  # past its end, not read
     assert _create(lib, size=old - 1) == smq.SMQ_ERR_INVALID_ARG
+
+
+def test_numbers_past_32_bits_are_refused(lib):
+    """2^32 + 64 is not 64."""
+    wide = 2 ** 32 + 64
+    for make in (lambda: smq.AttentionPlan(4, 2, 64, 16, max_rows=wide, device=0),
+                 lambda: smq.PagePlan(wide, 10, 4, 4, device=0), lambda: smq.PagePlan(16, 10, wide, 4, device=0),
+                 lambda: smq.PagePlan(16, 10, 4, wide, device=0)):
+        with pytest.raises(ValueError, match="32 bits"):
+            make()
