@@ -198,3 +198,27 @@ def test_numbers_past_32_bits_are_refused(name):
         else:
             smq.SequenceAttentionCall(plan, q, data[:, 0], data[:, 1], table, cu, n, out=torch.empty_like(q),
                                       workspace=plan.sequence_workspace(), **{**what, name: 2 ** 32 + 4})
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("rows", [1, 60])
+def test_a_wait_limit_of_a_nanosecond(dtype, rows):
+    """The clock is looked at every sixteenth try of a wait, each of which the hardware may hold up until the phase is there, so a call
+    in which nothing is late may end without an error; one with a tile that is never handed over may not. The next is right."""
+    seqs = [(rows, 2000 + 60 * i) for i in range(6)]
+    b = ref.Batch(_rng(rows), 64, 8, 128, 64, dtype, seqs)
+    sets = _sets(seqs, 1500, 4)
+    b.plan.set_wait_limit(1)
+    assert all(b.call(window=1500, sinks=4) in (0, smq.SMQ_ERR_TIMEOUT) for _ in range(5))
+    b.plan.inject_stall(1)
+    for _ in range(5):
+        assert b.call(window=1500, sinks=4) == smq.SMQ_ERR_TIMEOUT
+        b.plan.inject_stall(-1)
+        b.plan.set_wait_limit(2_000_000_000)
+        assert b.call(window=1500, sinks=4) == 0
+        b.plan.inject_stall(1)
+        b.plan.set_wait_limit(1)
+    b.plan.inject_stall(-1)
+    b.plan.set_wait_limit(2_000_000_000)
+    assert b.call(window=1500, sinks=4) == 0
+    b.check(sets, rows={0, rows - 1})
