@@ -630,7 +630,8 @@ cudaError_t launch_compact(const CompactParams& p, const Planes& planes, int num
   const int64_t blocks = static_cast<int64_t>(p.num_rows) * items.first[planes.count];
   items.ctas = 1;
   if (p.num_keep <= kFusedKeep) return launch(compact_kernel<true>, blocks, kMoveThreads, 1, stream, p, planes, items);
-  // few items: a cluster each, up to twelve CTAs an SM together
+  // Few items: a cluster each, until there are twelve CTAs an SM or clusters of eight. One context of 32768 tokens, 8 kv heads,
+  // 113 us, without clusters 676; 16 of them 362 and 801, 64 of 16384 tokens 685 and 697; until 6 or 24 an SM: the same within 2 %.
   while (items.ctas < 8 && blocks * items.ctas < 12ll * num_sms) items.ctas *= 2;
   cudaError_t rc = launch(compact_check_kernel, p.num_rows, kCheckThreads, 1, stream, p);
   if (rc != cudaSuccess) return rc;

@@ -12,7 +12,7 @@
 namespace smq {
 
 constexpr int kStatusNoPages = 32;  // SMQ_ERR_NO_PAGES
-constexpr int kSegmentUnit = 2048;  // pages
+constexpr int kSegmentUnit = 2048;  // pages: a segment's are shared by 16 warps in pieces of 128
 constexpr int kMaxSegments = 1024;
 constexpr int kMaxTokenBytes = 2048;  // of a plane
 

@@ -34,7 +34,9 @@ Scratch scratch_of(const smq_page_plan* p) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   const int64_t entries = static_cast<int64_t>(p->desc.table_rows) * p->desc.table_columns;
   Scratch s;
-  // segments of 4096 pages, or longer ones so that there are no more than kMaxSegments
+  // Segments of 4096 pages, or longer ones so that there are no more than kMaxSegments. A batch of 512 rows that turns over in a
+  // pool of 524288 pages takes 22 us, and two calls that fill and empty its table 33; with 2048 pages a segment 23 and 30, with
+  // 8192 the two calls 37, with 16384 42.
   const int64_t units = (p->desc.num_pages + smq::kSegmentUnit - 1) / smq::kSegmentUnit;
   const int64_t per = (units + smq::kMaxSegments - 1) / smq::kMaxSegments;
   s.segment = (per < 2 ? 2 : per) * smq::kSegmentUnit;

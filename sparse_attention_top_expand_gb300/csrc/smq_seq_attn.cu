@@ -1320,7 +1320,7 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
 // and others continued: out = sum_i w_i O_i / sum_i w_i l_i with
 // w_i = 2^(m_i - max m), in the order of the list. A block per such item and 32
 // queries, a lane each; a warp has every eighth column of the result, or with
-// kFew (few items, whose partials are many) every eighth partial of 16 columns.
+// kFew (few such blocks) every eighth partial of 16 columns.
 template <int D, int kQueries, bool kFew>
 __global__ void __launch_bounds__(256) seq_combine_kernel(const __grid_constant__ SeqAttnParams p, int ctas) {
   constexpr int kCols = kFew ? 16 : D, kPer = kFew ? 16 : D / 8, kWarpParts = kFew ? 8 : 1;
@@ -1455,10 +1455,13 @@ cudaError_t launch_combine(const SeqAttnParams& p, int grid, cudaStream_t stream
   const int64_t per = kQueries / 128 * (128 / p.group);
   const int64_t items = (static_cast<int64_t>(p.rows) / per + p.num_seqs) * p.kv_heads;
   const unsigned shared = static_cast<unsigned>(items < grid ? items : grid);
-  const int queries = kQueries > 128 ? kQueries : p.max_seq_rows * p.group;
-  if (items * 4 < grid)
-    return launch(seq_combine_kernel<D, kQueries, true>, dim3(shared, (queries + 31) / 32, D / 16), 256, 0, stream, p, grid);
-  return launch(seq_combine_kernel<D, kQueries, false>, dim3(shared, (queries + 31) / 32), 256, 0, stream, p, grid);
+  const unsigned blocks = ((kQueries > 128 ? kQueries : p.max_seq_rows * p.group) + 31) / 32;
+  // kFew spreads an item's partials and columns over warps and blocks, which pays as long as there are few blocks of 32 queries:
+  // a call in us, kFew and not, 64 heads on 8, D 128: one row of 1, 8, 16 and 64 sequences 20 and 33, 69 and 73, 120 and 122, 221
+  // and 223 (8 to 152 blocks); 64 rows of 2, 8 and 16 sequences 58 and 58, 107 and 85, 267 and 244 (384 and 1216 blocks).
+  if (shared * blocks <= 2u * static_cast<unsigned>(grid))
+    return launch(seq_combine_kernel<D, kQueries, true>, dim3(shared, blocks, D / 16), 256, 0, stream, p, grid);
+  return launch(seq_combine_kernel<D, kQueries, false>, dim3(shared, blocks), 256, 0, stream, p, grid);
 }
 
 }  // namespace
@@ -1479,6 +1482,8 @@ cudaError_t prepare_seq_attention(int head_dim, bool e4m3) {
 }
 
 cudaError_t launch_seq_attention(const SeqAttnParams& p, bool e4m3, int grid, cudaStream_t stream) {
+  // Two tiles of queries where some sequence may have more than one: 64 heads on 8, contexts of 8192, 16 sequences of 17 and of 64
+  // rows 130 and 244 us, 231 and 440 with one tile; 2 of 1024 rows 416 and 636; 31 of 5 rows, 32 heads on 1, 57 and 80.
   const bool pair = p.max_seq_rows > 128 / p.group;
   cudaError_t rc = with_kernel(p.head_dim, e4m3, pair, [&](auto kernel, auto shape) {
     return launch(kernel, dim3(grid), decltype(shape)::kThreads, decltype(shape)::kSmem, stream, p);
