@@ -9,6 +9,7 @@ import torch
 
 import sparse_attention_top_expand_gb300 as smq
 
+import attention_bounds as bounds
 import sequence_ref as ref
 
 pytestmark = pytest.mark.gpu
@@ -169,3 +170,63 @@ def test_a_long_context_does_not_pay(dtype):
     assert (out[:, :, rest].float() - clean[:, :, rest].float()).abs().max() <= 2.0 ** -6
     assert (out[~sees][:, :, 9].float() - clean[~sees][:, :, 9].float()).abs().max() <= 2.0 ** -6
     assert took < 0.02, took
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("heads", [2, 64])
+def test_with_scores_far_from_zero(dtype, heads):
+    """Both rare ways of a tile at once: scores past 1e12, of which the largest share all the weight, and values that some rows do not
+    see. A row's weights are those of equal scores, so roundings of scores do not matter."""
+    rng = _rng(heads, 3)
+    seqs = [(20, 250), (3, 100), (45, 300)]
+    b = ref.Batch(rng, heads, 1, 128, 64, dtype, seqs, scale=1.0)
+    b.q[:] = 0
+    b.q[:, :, 3] = torch.from_numpy(rng.choice([-3e12, 3e12, 0.5], b.q.shape[:2])).to(torch.bfloat16)
+    masks = []
+    for i, (n, length) in enumerate(seqs):
+        keys = np.zeros((length, 1, 128))
+        keys[:, :, 3] = rng.integers(1, 4, (length, 1))
+        bounds.put(b.cache, i, np.arange(length), 0, keys)
+        masks += ref.random_tree(rng, n)
+        for value in (np.nan, np.inf):
+            t = length - 1 - int(rng.integers(0, n - 1))
+            page, off = b.cache.table[i][t // 64], t % 64
+            if dtype == "bf16":
+                b.cache.data[page, 1, 0, off, 7] = value
+            else:
+                b.cache.data[page, 1, 0, off, 7] = 0x7F
+            b.cache.values[page, 1, 0, off, 7] = value if dtype == "bf16" else np.nan
+    assert b.call(tree_mask=ref.pack(masks + [set()] * 2, 2)) == 0
+    out = b.out.double().cpu().numpy()
+    sets = [ref.tree_sets(n, length, masks[b.cu[i]:b.cu[i] + n]) for i, (n, length) in enumerate(seqs)]
+    clean = 0
+    for i, per in enumerate(sets):
+        for r, at in zip(range(b.cu[i], b.cu[i + 1]), per):
+            k, v = b.cache.tokens(i, at)
+            odd = ~np.isfinite(v[:, 0]).all(0)  # by element
+            v = np.where(np.isfinite(v), v, 0)
+            want, mean, _, _ = ref.attend(b.q[r].double().numpy(), k, v, 1.0)
+            off, _ = ref.bound(want, mean, np.zeros(heads), 128, len(at))
+            assert (np.abs(out[r] - want) <= off)[:, ~odd].all(), (i, r)
+            assert not np.isfinite(out[r][:, odd]).any(), (i, r)
+            clean += not odd.any()
+    assert 0 < clean < len(masks)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("tile", [0, 1])  # of the first CTA, which has two: 5 * 2 * 8 items of 3 or 4 tiles over 152
+def test_a_withheld_tile_beside_such_values(dtype, tile):
+    rng = _rng(tile)
+    seqs = [(40, 700)] * 5
+    b = ref.Batch(rng, 64, 8, 128, 64, dtype, seqs)
+    sets = [ref.window_sets(n, length, 300, 4) for n, length in seqs]
+    for s in range(5):
+        for t in (5, 375, 520, 690):
+            _put(b, s, t, np.nan, rng)
+    b.plan.set_wait_limit(2_000_000)
+    b.plan.inject_stall(tile)
+    assert b.call(window=300, sinks=4) & smq.SMQ_ERR_TIMEOUT
+    b.plan.inject_stall(-1)
+    b.plan.set_wait_limit(2_000_000_000)
+    assert b.call(window=300, sinks=4) == 0
+    _check(b, sets)
