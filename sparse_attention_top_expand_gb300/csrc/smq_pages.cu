@@ -9,9 +9,9 @@
 // come from prefix sums in the order of rows and columns. Counts change by atomic
 // operations whose order does not matter: pages that are taken were free, and a
 // free page is not given back (its bit says so); of the others all additions
-// come before all subtractions, which stop at zero. A row is a block's work in both: with a warp a row
-// 512 rows of 2048 columns over 524288 pages took 74 us, so 21. Small calls are two
-// launches, some 9 us.
+// come before all subtractions, which stop at zero. A row is a block's work in
+// both: with a warp a row 512 rows of 2048 columns over 524288 pages took 74 us, so
+// 21 to 22. Small calls are two launches, some 9 us.
 #include "smq_pages.cuh"
 
 #include "smq_kernels.cuh"
@@ -388,9 +388,9 @@ __global__ void __launch_bounds__(kApplyThreads)
 // another, as when the newer part of a context moves forward, they need not.
 //
 // Bound by DRAM, half reads, half writes: 604 MB of 16 contexts, 256-byte tokens,
-// 238 us, 5.1 TB/s of both together. Two 16-byte pieces a thread and eight CTAs an
-// SM; four pieces measured 265, eight with the next round in flight 319. 64 rows of
-// up to eight tokens take 5.4 us.
+// 238 to 242 us, 5.0 to 5.1 TB/s of both together. Two 16-byte pieces a thread and
+// eight CTAs an SM; four pieces measured 265, eight with the next round in flight 319.
+// 64 rows of up to eight tokens take 5.4 us.
 
 namespace {
 

@@ -46,18 +46,19 @@
 // What bounds it. A pair of tiles (256 queries by 128 tokens, D 128) is 2048 cycles
 // of products at the tensor core's rate and takes some 3500: S to P, P to the next
 // S and the hand-offs between are a chain that two streams do not cover. The
-// roles run from one instruction cache, and the size of the softmax's loop decides:
-// 4096 rows, 64 heads on 8, a window of 4096 took 536 us with the 128 scores of a
-// thread in registers, 532 in loops of 64 tokens, 454 in loops of 32 that read S
-// from TMEM twice, 516 in loops of 16, and 552 to 607 with the next 32 asked for
-// ahead. It is 1.21 PFLOP/s, 63 % of what a library's product of 8192^3 reaches.
+// roles run from one instruction cache, and the size of the softmax's loop decides,
+// of code in it that is read past too. 4096 rows, 64 heads on 8, a window of 4096
+// take 468 to 476 us, 1.16 to 1.17 PFLOP/s, 60 % of what a library's product of
+// 8192^3 reaches; on kernels of their days 536 with the 128 scores of a thread in
+// registers, and against 454 in loops of 32 tokens that read S from TMEM twice 532
+// in loops of 64, 516 in loops of 16, and 552 to 607 with the next 32 asked for ahead.
 //  - trees of 64 tokens over contexts of 4096 to 32768, 16 sequences, the same
-//    heads: 507 us, 1.21 PFLOP/s.
-//  - 64 sequences of up to 4 rows, a window of 4096, E4M3: 260 us for 567 MB; a
-//    tile of 128 tokens takes 3400 cycles, of which a loader warp 1400 to widen
+//    heads: 504 to 543 us, 1.13 to 1.22 PFLOP/s.
+//  - 64 sequences of up to 4 rows, a window of 4096, E4M3: 251 us for 567 MB; a
+//    tile of 128 tokens takes 3300 cycles, of which a loader warp 1400 to widen
 //    its part and 1100 to copy the next (twice as many loader warps: the same), and
 //    every product has 128 queries' rows, of which 8 to 32 are there.
-//  - small calls, 18 to 20 us: three dependent loads to the first key (sequence,
+//  - small calls, 16 to 19 us: three dependent loads to the first key (sequence,
 //    block table, cache), one tile's chain, the join (a launch of its own).
 #include "smq_attn.cuh"
 #include "smq_attn_ptx.cuh"
@@ -889,6 +890,8 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
             const bool values = j >= 0, scores = j + step < n;
             const uint32_t nv = kPair ? v >> 1 : done;  // the tile's number at its barriers, and the next one's
             if ((values && !full(1, nv)) || (scores && !full(0, kPair ? k >> 1 : done + values))) break;
+            // The queries' parity names this segment's phase only because its first keys, which were asked for behind the queries
+            // of the segment before, have landed: stream 1 may have left that segment out.
             if (!values && !wait(kQFull, seg & 1)) break;
             fence_proxy_async_smem();
             if (values && !wait(kPFull + st, done & 1)) break;
@@ -935,7 +938,7 @@ __global__ void __launch_bounds__(SeqShape<D, kE4m3, kPair>::kThreads, 1)
       }
     } else {
       // ---------------------------------------------------------- addresses
-      // One warp, four tokens a lane; the next tile's pages are looked up while this tile's addresses are written.
+      // One warp, four tokens a lane; a tile's pages are looked up before the wait for its place in the ring.
       const int shift = p.page_shift;
       SeqSeg sg;
       sg.ntiles = 0;
