@@ -758,7 +758,7 @@ typedef struct smq_cache_compact_args {
   const int32_t *keep_ids;    /* device [num_rows][keep_ld] */
   int32_t num_keep;           /* 1 .. 1048576 */
   int32_t keep_ld;            /* >= num_keep */
-  const smq_page_plane *planes; /* host [num_planes], read during the call */
+  const smq_page_plane *planes; /* host [num_planes], read during the call; no two share bytes */
   int32_t num_planes;         /* 1 .. SMQ_MAX_PLANES */
   void *workspace;            /* device, 16-byte aligned */
   size_t workspace_bytes;

@@ -77,6 +77,19 @@ int take_planes(const smq_page_plan* p, const smq_page_plane* from, int32_t coun
   return SMQ_OK;
 }
 
+// Whether two planes share bytes of some page: one thing listed twice, or slices that overlap. Views of one allocation have one
+// page stride.
+bool share_bytes(const smq_page_plan* p, const smq_page_plane& x, const smq_page_plane& y) {
+  const bool first = reinterpret_cast<uintptr_t>(x.base) <= reinterpret_cast<uintptr_t>(y.base);
+  const smq_page_plane &a = first ? x : y, &b = first ? y : x;
+  const uint64_t apart = reinterpret_cast<uintptr_t>(b.base) - reinterpret_cast<uintptr_t>(a.base);
+  if (a.page_stride != b.page_stride) return apart == 0;
+  auto size = [&](const smq_page_plane& q) { return static_cast<uint64_t>(q.vectors) * p->desc.page_size * q.token_bytes; };
+  const uint64_t stride = a.page_stride, at = apart % stride;
+  if (apart >= stride * (p->desc.num_pages - 1) + size(a)) return false;  // b begins behind a's last page
+  return at < size(a) || at + size(b) > stride;
+}
+
 smq::PagesParams params_of(const smq_page_plan* plan, int32_t num_rows, int32_t* table, int32_t* refs, void* workspace) {
   const smq_page_plan_desc& d = plan->desc;
   const Scratch w = scratch_of(plan);
@@ -197,6 +210,9 @@ SMQ_API int sparse_mqa_cache_compact(const smq_page_plan* plan, const smq_cache_
   rc = take_planes(plan, a.planes, a.num_planes, &planes);
   if (rc != SMQ_OK) return rc;
   if (a.num_planes == 0 || a.num_keep <= 0 || a.num_keep > (1 << 20) || a.keep_ld < a.num_keep) return SMQ_ERR_INVALID_ARG;
+  for (int i = 0; i < planes.count; ++i)
+    for (int j = 0; j < i; ++j)
+      if (share_bytes(plan, planes.plane[i], planes.plane[j])) return SMQ_ERR_INVALID_ARG;  // their tokens would move twice
   if (a.num_rows == 0) return SMQ_OK;
   if (!a.block_table || !a.page_refs || !a.row_start || !a.keep_ids || !aligned(a.block_table, 4) ||
       !aligned(a.page_refs, 4) || !aligned(a.rows, 4) || !aligned(a.row_start, 4) || !aligned(a.keep_ids, 4))

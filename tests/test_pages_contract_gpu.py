@@ -120,3 +120,29 @@ def test_empty_ranges():
     status, got, after = b.many(lambda plan, r, t, ws: smq.sparse_mqa_pages_resize(plan, r, t, _i32(end), ws, row_begin=_i32(begin)), 3)
     held = [np.flatnonzero(row >= 0).tolist() for row in after]
     assert status == 0 and held == [[1], [], [1], [], [], [2], [2], []] and got.sum() == 4
+
+
+def test_planes_that_share_bytes_are_not_compacted():
+    """A token would move twice. Neighbours in a page, and whole pools behind one another, are taken."""
+    plan = smq.PagePlan(PAGE, 6, 2, 3)
+    refs, table = plan.state()
+    ws = plan.workspace()
+    smq.sparse_mqa_pages_resize(plan, refs, table, _i32([48, 48]), ws)
+    start, keep = _i32([0, 3]), _i32([[5, 9, 40], [7, 20, -1]])
+    data = torch.randint(0, 1 << 30, (12, 5, PAGE, 4), dtype=torch.int32, device=DEV)
+    before = data.clone()
+    a, b = data[:6], data[6:]
+    for planes in ([a[:, :2], a[:, :2]], [a[:, :2], a[:, 1:3]], [a[:, 3:], b[:, :1], a[:, 4:]], [a, data[1:7]], [a, data[3:9, :1]],
+                   [a, a[:, :1].view(torch.int16)]):
+        with pytest.raises(smq.SMQError) as e:
+            smq.sparse_mqa_cache_compact(plan, refs, table, start, keep, planes, ws)
+        assert e.value.code == smq.SMQ_ERR_INVALID_ARG and torch.equal(data, before)
+    smq.sparse_mqa_cache_compact(plan, refs, table, start, keep, [a[:, :2], a[:, 3:], b, a[:, 2:3]], ws)
+    assert smq.smq_get_status(ws) == 0
+    rows = table.cpu().numpy()
+    want = before.clone()
+    for pool in (0, 6):
+        for r, (s, ids) in enumerate(((0, (5, 9, 40)), (3, (7, 20)))):
+            for j, t in enumerate(ids):
+                want[pool + rows[r, (s + j) // PAGE], :, (s + j) % PAGE] = before[pool + rows[r, t // PAGE], :, t % PAGE]
+    assert torch.equal(data, want)
