@@ -23,7 +23,10 @@
 // rounded to bf16 (times its token's value scale before that): 2^-8 of a weight at
 // most, some 0.0015 of a result's norm beside the 0.0017 of its own rounding. Two
 // numbers a weight, as in smq_attn.cu, would be half as many products again, and
-// these are what a prefill's time is made of.
+// these are what a prefill's time is made of. Calls of few rows have time for them,
+// but the tensor core cuts what a step adds at 2^-24 of the sum so far, and twice
+// the steps with parts of 2^-8 lose more to that than a long context can spare:
+// 2^31 equal scores gave 0.93 for 1, with one number a weight 1.
 //
 // What a row does not see. Scores of tokens that are not there, or not seen, are
 // minus infinity, so their weights are zeros. That does not keep out an infinite
